@@ -276,6 +276,138 @@ int convrot_prepare_activations(const void* X_dev, int64_t M, int64_t K, int g, 
 int convrot_gemm(const void* workspace_dev, size_t ws_bytes, int64_t M, int64_t K, const void* image_dev,
                  const float* sw_dev, const void* bias_dev, int64_t N, int g, void* Y_dev, void* stream);
 
+/* ---- operators around the linears of a block ------------------------------ */
+/* What a transformer block runs between its rotated linears: the residual
+ * update with the norms on both sides, rotary positions for the query and key
+ * heads, and the product of a few rows with group-scaled 4-bit weights (the
+ * modulation linear of a conditioned block, a decoder's linears at one token).
+ * The conventions above hold, with these differences:
+ *   - many sizes and strides go in together, so each call takes one struct
+ *     (every field set; unused pointers NULL, unused numbers 0).  It is read
+ *     before the call returns and not kept;
+ *   - strides are in elements, inputs need only the alignment of their
+ *     elements (16-byte aligned rows run faster; the grouped linear's X and
+ *     codes have to be 16-byte aligned), and rows need not be dense;
+ *   - no workspace: nothing is shared between calls, on any stream or graph;
+ *   - outputs must not overlap inputs or one another, except where a field
+ *     says so (CONVROT_EINVAL).
+ * Sums, statistics and angles are held in 32 bits or more whatever the storage
+ * type, and each output is rounded to it once (nearest even).  None of these
+ * operators has a gradient. */
+
+/* Storage types. */
+#define CONVROT_BF16 1
+#define CONVROT_F16 2
+#define CONVROT_F32 3
+/* Position type besides CONVROT_F32. */
+#define CONVROT_I32 4
+
+/* Norms of a row v of `width` values: LAYER (v - mean) / sqrt(var + eps) with
+ * var the mean squared deviation, RMS v / sqrt(mean(v^2) + eps). */
+#define CONVROT_NORM_NONE 0
+#define CONVROT_NORM_LAYER 1
+#define CONVROT_NORM_RMS 2
+
+/* The residual update and the norms before and after it, for every row i:
+ *   z = P(y)                                P: post_norm, then post_weight
+ *   r = residual_scale * x + gate[v] * z
+ *   h = N(r) * weight * (1 + scale[v]) + shift[v]      N: norm
+ * v = i / rows_per_vec.  N works on r before its rounding.  Without y,
+ * r = residual_scale * x; a NULL gate, weight or post_weight counts as 1, a
+ * NULL scale or shift as 0; a NULL r or h is not written (not both). */
+typedef struct {
+    const void* x_dev;           /* [rows][width]                              */
+    const void* y_dev;           /* [rows][width] or NULL                      */
+    const void* gate_dev;        /* [vectors][width] or NULL (needs y)         */
+    const void* scale_dev;       /* [vectors][width] or NULL (needs h)         */
+    const void* shift_dev;       /* [vectors][width] or NULL (needs h)         */
+    const void* weight_dev;      /* [width] or NULL (needs h)                  */
+    const void* post_weight_dev; /* [width] or NULL (needs a post_norm)        */
+    void* r_dev;                 /* [rows][width] or NULL; may be x or y itself */
+    void* h_dev;                 /* [rows][width] or NULL; may be x or y itself */
+    int64_t rows, width;         /* 0 .. 16777216, 1 .. 16384                  */
+    int64_t x_stride, y_stride, r_stride, h_stride;      /* >= 0; r, h: >= width */
+    int64_t gate_stride, scale_stride, shift_stride;     /* >= 0; 0: one vector for all */
+    int64_t rows_per_vec;        /* >= 1                                       */
+    float residual_scale, eps;   /* eps >= 0                                   */
+    int dtype;                   /* of x, y, r, h                              */
+    int vec_dtype;               /* of the vectors and weights: dtype or F32   */
+    int norm, post_norm;         /* post_norm other than NONE needs y          */
+} convrot_residual_norm_args;
+int convrot_residual_norm(const convrot_residual_norm_args* args_host, void* stream);
+/* Its checks alone (host only). */
+int convrot_validate_residual_norm(const convrot_residual_norm_args* args_host);
+
+/* Pairs of a head: INTERLEAVED elements (2i, 2i + 1), HALVES (i, i + pairs). */
+#define CONVROT_ROPE_INTERLEAVED 1
+#define CONVROT_ROPE_HALVES 2
+
+/* The heads of the queries or of the keys: [batch][tokens][heads][head_dim],
+ * the last dimension dense.  out may be in itself (same strides). */
+typedef struct {
+    const void* in_dev;
+    void* out_dev;
+    const void* weight_dev;      /* [head_dim] or NULL (needs norm)            */
+    int64_t heads;               /* 1 .. 65535                                 */
+    int64_t in_batch_stride, in_token_stride, in_head_stride;    /* >= 0       */
+    int64_t out_batch_stride, out_token_stride, out_head_stride; /* no element twice */
+} convrot_heads;
+
+/* Rotary positions over several axes: pair i of every head of token t turns by
+ *   angle = positions[b][t][axis_host[i]] * freq_host[i]   (radians)
+ *   (u, v) -> (u cos - v sin, u sin + v cos),
+ * elements from 2 pairs on pass through.  With norm = CONVROT_NORM_RMS every
+ * head is first divided by sqrt(mean(x^2) + eps) over its head_dim values and
+ * multiplied by its weight.  The angle is formed and reduced in binary64.
+ * Negated positions turn back. */
+typedef struct {
+    convrot_heads heads[2];
+    int count;                   /* tensors in use: 1 or 2                     */
+    int64_t batch, tokens;       /* 0 .. 65535, 0 .. 16777216                  */
+    int head_dim;                /* 1 .. 256                                   */
+    const void* pos_dev;         /* [batch][tokens][axes], the last one dense  */
+    int64_t pos_batch_stride, pos_token_stride;                  /* >= 0       */
+    int pos_dtype;               /* CONVROT_I32 or CONVROT_F32                 */
+    int axes;                    /* 1 .. 8                                     */
+    int pairs;                   /* 1 .. head_dim / 2                          */
+    const double* freq_host;     /* [pairs], finite                            */
+    const int32_t* axis_host;    /* [pairs], 0 .. axes - 1                     */
+    int layout, norm, dtype;     /* dtype: of heads and weights                */
+    float eps;
+} convrot_rope_args;
+int convrot_rope(const convrot_rope_args* args_host, void* stream);
+int convrot_validate_rope(const convrot_rope_args* args_host);
+
+/* Y = X W^T + bias for M <= 32 rows and 4-bit weights with a scale for every
+ * `group` input channels of an output:
+ *   W[n][k] = scales[n][k / group] * (code[n][k] - zeros[n][k / group]).
+ * codes is N x packed-K, uint8 [N][K/2], the low nibble the even channel:
+ * unsigned codes with zeros (uint8 [N][K/group], 0 .. 15), two's complement
+ * ones in [-8, 7] without (zeros NULL).  No rotation, no repacking.  A row of X
+ * that holds an infinity gives NaN. */
+typedef struct {
+    const void* x_dev;           /* [M][K], 16-byte aligned                    */
+    const void* codes_dev;       /* [N][K/2], 16-byte aligned                  */
+    const void* scales_dev;      /* [N][K/group]                               */
+    const void* zeros_dev;       /* [N][K/group] or NULL                       */
+    const void* bias_dev;        /* [N] or NULL                                */
+    void* y_dev;                 /* [M][N]                                     */
+    int64_t M, N, K;             /* 0 .. 32, 0 .. 16777216, group .. 65536     */
+    int group;                   /* 32, 64 or 128, dividing K                  */
+    int dtype;                   /* of X, scales, bias and Y: BF16 or F16      */
+} convrot_grouped_args;
+int convrot_linear_grouped(const convrot_grouped_args* args_host, void* stream);
+int convrot_validate_linear_grouped(const convrot_grouped_args* args_host);
+
+/* Such a weight from W [N][K] (dtype BF16 or F16, dense): per group, without
+ * zeros_dev, scale = absmax / 7 rounded to dtype and codes clamp(rint(w /
+ * scale), -7, 7); with it, lo = min(0, w), hi = max(0, w), scale = (hi - lo) /
+ * 15 rounded, zero = min(rint(-lo / scale), 15), codes clamp(rint(w / scale) +
+ * zero, 0, 15).  A group of zeros has scale 0 and codes 0; a value that is not
+ * finite makes its group's scale NaN. */
+int convrot_quantize_weight_grouped(const void* W_dev, int64_t N, int64_t K, int group, int dtype, uint8_t* codes_dev,
+                                    void* scales_dev, uint8_t* zeros_dev, void* stream);
+
 /* ---- parity hooks (same kernels, exposed intermediate results) ---------- */
 
 /* Rotation + row absmax + quantization of `rows` bf16 rows, with plain

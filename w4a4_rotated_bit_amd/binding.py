@@ -62,6 +62,34 @@ _I64 = ctypes.c_int64
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
 
+
+class _NormArgs(ctypes.Structure):      # convrot_residual_norm_args
+    _fields_ = ([(n, _P) for n in ("x_dev", "y_dev", "gate_dev", "scale_dev", "shift_dev", "weight_dev",
+                                   "post_weight_dev", "r_dev", "h_dev")] +
+                [(n, _I64) for n in ("rows", "width", "x_stride", "y_stride", "r_stride", "h_stride", "gate_stride",
+                                     "scale_stride", "shift_stride", "rows_per_vec")] +
+                [("residual_scale", ctypes.c_float), ("eps", ctypes.c_float)] +
+                [(n, _I) for n in ("dtype", "vec_dtype", "norm", "post_norm")])
+
+
+class _Heads(ctypes.Structure):         # convrot_heads
+    _fields_ = ([(n, _P) for n in ("in_dev", "out_dev", "weight_dev")] +
+                [(n, _I64) for n in ("heads", "in_batch_stride", "in_token_stride", "in_head_stride",
+                                     "out_batch_stride", "out_token_stride", "out_head_stride")])
+
+
+class _RopeArgs(ctypes.Structure):      # convrot_rope_args
+    _fields_ = [("heads", _Heads * 2), ("count", _I), ("batch", _I64), ("tokens", _I64), ("head_dim", _I),
+                ("pos_dev", _P), ("pos_batch_stride", _I64), ("pos_token_stride", _I64), ("pos_dtype", _I),
+                ("axes", _I), ("pairs", _I), ("freq_host", _P), ("axis_host", _P), ("layout", _I), ("norm", _I),
+                ("dtype", _I), ("eps", ctypes.c_float)]
+
+
+class _GroupedArgs(ctypes.Structure):   # convrot_grouped_args
+    _fields_ = ([(n, _P) for n in ("x_dev", "codes_dev", "scales_dev", "zeros_dev", "bias_dev", "y_dev")] +
+                [("M", _I64), ("N", _I64), ("K", _I64), ("group", _I), ("dtype", _I)])
+
+
 _SIGNATURES = {
     "convrot_status_string": ([_I], ctypes.c_char_p),
     "convrot_version": ([], ctypes.c_char_p),
@@ -89,6 +117,13 @@ _SIGNATURES = {
                                 ctypes.POINTER(_SZ)], _I),
     "convrot_matrix_core_probe_bytes": ([ctypes.POINTER(_SZ)], _I),
     "convrot_matrix_core_probe": ([_I, _I, _P, _SZ, ctypes.POINTER(_I64), _P], _I),
+    "convrot_residual_norm": ([ctypes.POINTER(_NormArgs), _P], _I),
+    "convrot_validate_residual_norm": ([ctypes.POINTER(_NormArgs)], _I),
+    "convrot_rope": ([ctypes.POINTER(_RopeArgs), _P], _I),
+    "convrot_validate_rope": ([ctypes.POINTER(_RopeArgs)], _I),
+    "convrot_linear_grouped": ([ctypes.POINTER(_GroupedArgs), _P], _I),
+    "convrot_validate_linear_grouped": ([ctypes.POINTER(_GroupedArgs)], _I),
+    "convrot_quantize_weight_grouped": ([_P, _I64, _I64, _I, _I, _P, _P, _P, _P], _I),
     "convrot_host_pack_nk": ([_P, _I64, _I64, _P], _I),
     "convrot_host_unpack_nk": ([_P, _I64, _I64, _P], _I),
     "convrot_host_nk_to_kn": ([_P, _I64, _I64, _P], _I),
@@ -501,4 +536,335 @@ def convrot_linear_w4a16(X, image, sw, bias, N: int, g: int, Y=None, workspace=N
     _call("convrot_linear_w4a16", _dev(X, torch.bfloat16, "X"), M, K, _dev(image, torch.uint8, "image"),
           _dev(sw, torch.float32, "sw"), bias_p, N, g, _dev(Y, torch.bfloat16, "Y"),
           _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream))
+    return Y
+
+
+# --------------------------------------------------------------------------
+# operators around the linears of a block
+# --------------------------------------------------------------------------
+
+CONVROT_BF16 = 1
+CONVROT_F16 = 2
+CONVROT_F32 = 3
+CONVROT_I32 = 4
+CONVROT_NORM_NONE = 0
+CONVROT_NORM_LAYER = 1
+CONVROT_NORM_RMS = 2
+CONVROT_ROPE_INTERLEAVED = 1
+CONVROT_ROPE_HALVES = 2
+
+_NORMS = {None: CONVROT_NORM_NONE, "layer": CONVROT_NORM_LAYER, "rms": CONVROT_NORM_RMS}
+_LAYOUTS = {"interleaved": CONVROT_ROPE_INTERLEAVED, "halves": CONVROT_ROPE_HALVES}
+_types = None   # torch dtype -> storage type, filled on first use
+
+
+def _type_of(t, name, allowed=None):
+    global _types
+    if _types is None:
+        import torch
+        _types = {torch.bfloat16: CONVROT_BF16, torch.float16: CONVROT_F16, torch.float32: CONVROT_F32}
+    code = _types.get(t.dtype)
+    if code is None or (allowed is not None and code not in allowed):
+        raise TypeError(f"{name} has an unsupported type {t.dtype}")
+    return code
+
+
+def _choice(table, key, what):
+    try:
+        return table[key]
+    except (KeyError, TypeError):
+        raise ValueError(f"unknown {what} {key!r}") from None
+
+
+def _check_tensor(t, name, device):
+    """A tensor of this call: on its device, and one that asks for no gradient here."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.requires_grad and torch.is_grad_enabled():
+        raise RuntimeError(f"{name} requires a gradient, and this operator has none: call it under torch.no_grad()")
+
+
+def _on_gpu(t, name):
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    return t.device
+
+
+class _Launch:
+    """The device and stream of a call: work and the outputs it allocates go to
+    ``stream`` (or the device's current stream), whatever device is current."""
+
+    def __init__(self, device, stream):
+        import torch
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+        other = device.index != torch.cuda.current_device()
+        self._scope = torch.cuda.stream(stream) if stream is not None else torch.cuda.device(device) if other else None
+        self._raw = (stream or torch.cuda.current_stream(device)).cuda_stream
+
+    def __enter__(self):
+        if self._scope is not None:
+            self._scope.__enter__()
+        return self._raw
+
+    def __exit__(self, *exc):
+        if self._scope is not None:
+            self._scope.__exit__(*exc)
+
+
+def _rows(t, name, width=None):
+    """(rows, row stride) of a tensor seen as rows of its dense last dimension."""
+    if t.dim() == 0 or (width is not None and t.shape[-1] != width):
+        raise ValueError(f"{name} must have rows of {width} values, got shape {tuple(t.shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be dense in its last dimension")
+    if t.numel() == 0:
+        return 0, 0
+    rows, stride = 1, 0
+    for n, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
+            continue
+        if rows == 1:
+            stride = s
+        elif s != rows * stride:
+            raise ValueError(f"the rows of {name} are not evenly spaced: strides {t.stride()}")
+        rows *= n
+    return rows, stride
+
+
+def convrot_residual_norm(x, y=None, *, gate=None, scale=None, shift=None, weight=None, post_weight=None,
+                          norm="layer", post_norm=None, residual_scale: float = 1.0, eps: float = 1e-6, r=None,
+                          h=None, want_r: bool = True, want_h: bool = True, stream=None):
+    """r = residual_scale x + gate * P(y);  h = N(r) * weight * (1 + scale) + shift.
+
+    x, y: bf16, f16 or f32 [..., width].  norm, post_norm: "layer", "rms" or
+    None.  gate, scale, shift: of the same type or f32, [width] for all rows, or
+    [..., width] with the leading dimensions of x, or the first of them (one
+    vector a batch entry; ones may follow); for a matrix x also [V, width], one
+    vector for every rows / V rows.  weight, post_weight: [width], of the
+    vectors' type.  Returns (r, h) of x's shape; r or h given is written (x or
+    y itself may be), and one not wanted is None."""
+    import torch
+    device = _on_gpu(x, "x")
+    width = x.shape[-1] if x.dim() else 0
+    a = _NormArgs()
+    a.dtype = _type_of(x, "x")
+    a.norm, a.post_norm = _choice(_NORMS, norm, "norm"), _choice(_NORMS, post_norm, "norm")
+    a.residual_scale, a.eps, a.width = residual_scale, eps, width
+    rows, a.x_stride = _rows(x, "x", width)
+    a.rows, a.x_dev = rows, x.data_ptr()
+    _check_tensor(x, "x", device)
+    if y is not None:
+        _check_tensor(y, "y", device)
+        if y.shape != x.shape or y.dtype != x.dtype:
+            raise ValueError(f"y must have the shape and type of x, got {tuple(y.shape)} {y.dtype}")
+        a.y_stride, a.y_dev = _rows(y, "y", width)[1], y.data_ptr()
+    per, a.vec_dtype = 0, 0
+    for name, v in (("gate", gate), ("scale", scale), ("shift", shift), ("weight", weight),
+                    ("post_weight", post_weight)):
+        if v is None:
+            continue
+        _check_tensor(v, name, device)
+        code = _type_of(v, name, (a.dtype, CONVROT_F32))
+        if a.vec_dtype and code != a.vec_dtype:
+            raise TypeError("the vectors and weights must have one type")
+        a.vec_dtype = code
+        n, step = _rows(v, name, width)
+        setattr(a, name + "_dev", v.data_ptr())
+        if name in ("weight", "post_weight"):
+            if n != 1:
+                raise ValueError(f"{name} must be one vector of {width} values")
+            continue
+        lead = list(v.shape[:-1])
+        while lead and lead[-1] == 1:
+            lead.pop()
+        if n == 1:
+            step = 0
+        elif (rows % n if x.dim() == 2 and len(lead) == 1 and n else tuple(lead) != tuple(x.shape[:len(lead)])):
+            raise ValueError(f"{name} of shape {tuple(v.shape)} does not fit x of shape {tuple(x.shape)}")
+        elif rows:
+            if per and per != rows // n:
+                raise ValueError("gate, scale and shift must have one vector, or as many as one another")
+            per = rows // n
+        setattr(a, name + "_stride", step)
+    a.vec_dtype = a.vec_dtype or a.dtype
+    a.rows_per_vec = max(per, 1)
+    with _Launch(device, stream) as raw:
+        outs = []
+        for name, out, wanted in (("r", r, want_r), ("h", h, want_h)):
+            if out is None and not wanted:
+                outs.append(None)
+                continue
+            if out is None:
+                out = torch.empty(x.shape, dtype=x.dtype, device=device)
+            else:
+                _check_tensor(out, name, device)
+                if out.shape != x.shape or out.dtype != x.dtype:
+                    raise ValueError(f"{name} must have the shape and type of x")
+            setattr(a, name + "_stride", _rows(out, name, width)[1])
+            setattr(a, name + "_dev", out.data_ptr())
+            outs.append(out)
+        _call("convrot_residual_norm", ctypes.byref(a), raw)
+    return outs[0], outs[1]
+
+
+def rope_frequencies(sizes, theta: float = 10000.0, shared: bool = False):
+    """(freq float64 [pairs], axis int32 [pairs]) of a rotation over several axes.
+
+    Axis a owns sizes[a] of a head's elements (an even number) and runs through
+    a spectrum of its own, theta^(-2 i / sizes[a]); with ``shared`` all axes
+    cut one spectrum over sum(sizes) elements into sections, in order."""
+    sizes = [int(s) for s in sizes]
+    if not sizes or any(s < 2 or s % 2 for s in sizes):
+        raise ValueError("every axis needs an even, positive number of elements")
+    axis = np.repeat(np.arange(len(sizes), dtype=np.int32), [s // 2 for s in sizes])
+    if shared:
+        freq = theta ** (-np.arange(len(axis)) * 2.0 / sum(sizes))
+    else:
+        freq = np.concatenate([theta ** (-np.arange(s // 2) * 2.0 / s) for s in sizes])
+    return freq, axis
+
+
+def _heads(slot, t, out, weight, name, a, device):
+    """Fill one convrot_heads; t and out are [batch, tokens, heads, head_dim]."""
+    if t.dim() != 4 or tuple(t.shape[:2]) != (a.batch, a.tokens) or t.shape[3] != a.head_dim:
+        raise ValueError(f"{name} must be [batch, tokens, heads, head_dim], got {tuple(t.shape)}")
+    if out.shape != t.shape or out.dtype != t.dtype:
+        raise ValueError(f"{name}_out must have the shape and type of {name}")
+    for v in (t, out):
+        if v.shape[3] > 1 and v.stride(3) != 1:
+            raise ValueError(f"{name} and its output must be dense in their last dimension")
+    slot.in_dev, slot.out_dev, slot.heads = t.data_ptr(), out.data_ptr(), t.shape[2]
+    slot.in_batch_stride, slot.in_token_stride, slot.in_head_stride = t.stride()[:3]
+    slot.out_batch_stride, slot.out_token_stride, slot.out_head_stride = out.stride()[:3]
+    if weight is not None:
+        _check_tensor(weight, f"{name}_weight", device)
+        if weight.dtype != t.dtype or tuple(weight.shape) != (a.head_dim,) or not weight.is_contiguous():
+            raise ValueError(f"{name}_weight must be one dense vector of head_dim values of {name}'s type")
+        slot.weight_dev = weight.data_ptr()
+
+
+def convrot_rope(q, k, positions, freq, axis, *, layout: str = "interleaved", qk_norm: bool = False, q_weight=None,
+                 k_weight=None, eps: float = 1e-6, q_out=None, k_out=None, stream=None):
+    """Turn the pairs of every head by positions[..., axis] * freq.
+
+    q, k: bf16, f16 or f32 [batch, tokens, heads, head_dim] of any strides but a
+    dense last one (slices of a packed projection); k may be None.  positions:
+    int32 or float32 [batch or 1, tokens, axes].  freq (float64), axis (int32):
+    host arrays, one value a pair (``rope_frequencies``).  qk_norm: divide each
+    head by its root mean square first, times q_weight / k_weight [head_dim].
+    Returns (q_out, k_out); given ones are written and may be q, k themselves or
+    transposed views ([batch, heads, tokens, head_dim] storage)."""
+    import torch
+    device = _on_gpu(q, "q")
+    _check_tensor(q, "q", device)
+    if q.dim() != 4:
+        raise ValueError(f"q must be [batch, tokens, heads, head_dim], got {tuple(q.shape)}")
+    a = _RopeArgs()
+    a.dtype, a.layout, a.eps = _type_of(q, "q"), _choice(_LAYOUTS, layout, "layout"), eps
+    a.batch, a.tokens, a.head_dim = q.shape[0], q.shape[1], q.shape[3]
+    a.norm = CONVROT_NORM_RMS if qk_norm else CONVROT_NORM_NONE
+    freq, axis = np.ascontiguousarray(freq, np.float64), np.ascontiguousarray(axis, np.int32)
+    if freq.ndim != 1 or freq.shape != axis.shape:
+        raise ValueError("freq and axis must hold one value for every pair")
+    a.pairs, a.freq_host, a.axis_host = freq.shape[0], freq.ctypes.data, axis.ctypes.data
+    _check_tensor(positions, "positions", device)
+    if positions.dtype == torch.int32:
+        a.pos_dtype = CONVROT_I32
+    elif positions.dtype == torch.float32:
+        a.pos_dtype = CONVROT_F32
+    else:
+        raise TypeError(f"positions must be int32 or float32, got {positions.dtype}")
+    if positions.dim() != 3 or positions.shape[0] not in (1, a.batch) or positions.shape[1] != a.tokens:
+        raise ValueError(f"positions must be [batch or 1, tokens, axes], got {tuple(positions.shape)}")
+    if positions.shape[2] > 1 and positions.stride(2) != 1:
+        raise ValueError("positions must be dense in their last dimension")
+    a.axes, a.pos_dev = positions.shape[2], positions.data_ptr()
+    a.pos_batch_stride = positions.stride(0) if positions.shape[0] > 1 else 0
+    a.pos_token_stride = positions.stride(1)
+    a.count = 1
+    if k is not None:
+        _check_tensor(k, "k", device)
+        if k.dtype != q.dtype:
+            raise TypeError("k must have the type of q")
+        a.count = 2
+    elif k_weight is not None or k_out is not None:
+        raise ValueError("k_weight and k_out need k")
+    with _Launch(device, stream) as raw:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=device)
+        else:
+            _check_tensor(q_out, "q_out", device)
+        _heads(a.heads[0], q, q_out, q_weight, "q", a, device)
+        if k is not None:
+            if k_out is None:
+                k_out = torch.empty(k.shape, dtype=k.dtype, device=device)
+            else:
+                _check_tensor(k_out, "k_out", device)
+            _heads(a.heads[1], k, k_out, k_weight, "k", a, device)
+        _call("convrot_rope", ctypes.byref(a), raw)
+    return q_out, k_out
+
+
+def convrot_quantize_weight_grouped(W, group: int, asymmetric: bool = False, stream=None):
+    """W: bf16 or f16 [N, K] -> (codes uint8 [N, K/2], scales [N, K/group] of W's
+    type, zeros uint8 [N, K/group], or None unless ``asymmetric``)."""
+    import torch
+    device = _on_gpu(W, "W")
+    _check_tensor(W.detach(), "W", device)
+    if W.dim() != 2 or not W.is_contiguous():
+        raise ValueError("W must be a dense [N, K] tensor")
+    code = _type_of(W, "W", (CONVROT_BF16, CONVROT_F16))
+    N, K = W.shape
+    if group not in (32, 64, 128) or K % group:
+        raise ValueError(f"group must be 32, 64 or 128 and divide K = {K}, got {group}")
+    with _Launch(device, stream) as raw:
+        codes = torch.empty((N, K // 2), dtype=torch.uint8, device=device)
+        scales = torch.empty((N, K // group), dtype=W.dtype, device=device)
+        zeros = torch.empty((N, K // group), dtype=torch.uint8, device=device) if asymmetric else None
+        _call("convrot_quantize_weight_grouped", W.data_ptr(), N, K, group, code, codes.data_ptr(),
+              scales.data_ptr(), None if zeros is None else zeros.data_ptr(), raw)
+    return codes, scales, zeros
+
+
+def convrot_linear_grouped(X, codes, scales, zeros, bias, group: int, Y=None, stream=None):
+    """Y = X W^T + bias, W = scales * (codes - zeros) in groups of ``group``
+    channels.  X: bf16 or f16 [M, K], M <= 32; codes: uint8 [N, K/2] (N x
+    packed-K); scales: [N, K/group] of X's type; zeros: uint8 [N, K/group] with
+    unsigned codes, None with two's complement ones; bias: [N] or None."""
+    import torch
+    device = _on_gpu(X, "X")
+    a = _GroupedArgs()
+    a.dtype, a.group = _type_of(X, "X", (CONVROT_BF16, CONVROT_F16)), group
+    if X.dim() != 2 or codes.dim() != 2:
+        raise ValueError("X and codes must be matrices")
+    M, K = X.shape
+    N = codes.shape[0]
+    if group not in (32, 64, 128) or K % group:
+        raise ValueError(f"group must be 32, 64 or 128 and divide K = {K}, got {group}")
+    a.M, a.N, a.K = M, N, K
+    for name, t, dtype, shape in (("X", X, X.dtype, (M, K)), ("codes", codes, torch.uint8, (N, K // 2)),
+                                  ("scales", scales, X.dtype, (N, K // group)),
+                                  ("zeros", zeros, torch.uint8, (N, K // group)), ("bias", bias, X.dtype, (N,)),
+                                  ("Y", Y, X.dtype, (M, N))):
+        if t is None and name in ("zeros", "bias", "Y"):
+            continue
+        _check_tensor(t, name, device)
+        if t.dtype != dtype or tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if name != "Y":
+            setattr(a, name.lower() + "_dev", t.data_ptr())
+    with _Launch(device, stream) as raw:
+        if Y is None:
+            Y = torch.empty((M, N), dtype=X.dtype, device=device)
+        a.y_dev = Y.data_ptr()
+        _call("convrot_linear_grouped", ctypes.byref(a), raw)
     return Y

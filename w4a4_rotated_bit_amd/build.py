@@ -16,8 +16,8 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB_PATH = os.path.join(HERE, "libconvrot.so")
 ARCH = "gfx950"
 
-HIP_SOURCES = ["kernels.hip", "api.hip"]
-CXX_SOURCES = ["host.cpp"]
+HIP_SOURCES = ["kernels.hip", "norm.hip", "rope.hip", "grouped.hip", "api.hip", "block_api.hip"]
+CXX_SOURCES = ["host.cpp", "block_host.cpp"]
 
 COMMON = ["-O3", "-fPIC", "-std=c++17", "-Wall", "-I", CSRC, "-I", INCLUDE]
 HIP_FLAGS = ["-x", "hip", f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

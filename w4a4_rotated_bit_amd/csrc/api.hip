@@ -22,6 +22,10 @@ namespace {
 // Per-device answer to "is this a gfx950?": 0 unknown, 1 yes, 2 no.
 std::atomic<int> g_arch_ok[64];
 
+}  // namespace
+
+namespace convrot {
+
 int check_device()
 {
     int dev = -1;
@@ -41,6 +45,10 @@ int launched()
 {
     return hipGetLastError() == hipSuccess ? CONVROT_OK : CONVROT_EHIP;
 }
+
+}  // namespace convrot
+
+namespace {
 
 hipStream_t as_stream(void* s) { return (hipStream_t)s; }
 

@@ -5,6 +5,10 @@
 
 namespace convrot {
 
+// Shared by the C entry points (api.hip).
+int check_device();  // CONVROT_OK when the current device is a gfx950
+int launched();      // CONVROT_OK unless the last launch reported an error
+
 enum PrepOut { OUT_IMAGE = 0, OUT_ROWMAJOR = 2, OUT_NK = 3, OUT_LDS = 4, OUT_ROTATED_BF16 = 5 };
 enum GemmOut { GEMM_OUT_BF16 = 0, GEMM_OUT_I32 = 1 };
 
