@@ -9,6 +9,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -16,7 +17,8 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB_PATH = os.path.join(HERE, "libconvrot.so")
 ARCH = "gfx950"
 
-HIP_SOURCES = ["kernels.hip", "norm.hip", "rope.hip", "grouped.hip", "api.hip", "block_api.hip"]
+HIP_SOURCES = ["kernels.hip", "grouped_bf16.hip", "grouped_f16.hip", "norm.hip", "rope.hip", "grouped.hip", "api.hip",
+               "block_api.hip"]
 CXX_SOURCES = ["host.cpp", "block_host.cpp"]
 
 COMMON = ["-O3", "-fPIC", "-std=c++17", "-Wall", "-I", CSRC, "-I", INCLUDE]
@@ -45,17 +47,13 @@ def build(verbose: bool = False) -> str:
     hipcc = _hipcc()
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
-    objs = []
-    for src in HIP_SOURCES:
-        obj = os.path.join(objdir, src + ".o")
-        out = _run([hipcc, *COMMON, *HIP_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj])
-        if verbose and out.strip():
-            print(out)
-        objs.append(obj)
-    for src in CXX_SOURCES:
-        obj = os.path.join(objdir, src + ".o")
-        _run([hipcc, *COMMON, "-c", os.path.join(CSRC, src), "-o", obj])
-        objs.append(obj)
+    objs = [os.path.join(objdir, src + ".o") for src in HIP_SOURCES + CXX_SOURCES]
+    cmds = [[hipcc, *COMMON, *(HIP_FLAGS if src in HIP_SOURCES else []), "-c", os.path.join(CSRC, src), "-o", obj]
+            for src, obj in zip(HIP_SOURCES + CXX_SOURCES, objs)]
+    with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as pool:
+        for out in pool.map(_run, cmds):
+            if verbose and out.strip():
+                print(out)
     tmp = LIB_PATH + ".tmp"
     _run([hipcc, "-shared", "-fPIC", f"--offload-arch={ARCH}", *objs, "-o", tmp])
     os.replace(tmp, LIB_PATH)

@@ -1,0 +1,431 @@
+// grouped_kernel.h -- y = x W^T + bias for a few rows of x and 4-bit weights with one
+// scale (and zero point) for every 32, 64 or 128 input channels of a row:
+//
+//   y[m][n] = sum_g s[n][g] (sum_{k in g} u[n][k] x[m][k] - z[n][g] sum_{k in g} x[m][k]) + bias[n]
+//
+// u in [0, 15] are the codes as stored (two's complement codes q are read as
+// u = q + 8 with z = 8).  Both inner sums run on the 16-bit matrix cores with
+// binary32 sums; the second one is the product with a matrix of ones, so it
+// comes out in the lanes that need it.  A code becomes a bf16 or f16 value
+// without rounding: the byte u is the FP8 e4m3 value u / 512 (denormals and
+// the first binade are one arithmetic progression), which one conversion
+// instruction widens two at a time, times 512.
+//
+// The codes are read as they are interchanged, N x packed-K.
+#pragma once
+#include "block_ops.h"
+
+namespace convrot {
+namespace grouped {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+template <typename D>
+struct Mat;
+template <>
+struct Mat<__bf16> {
+    typedef __bf16 Frag __attribute__((ext_vector_type(8)));
+    static __device__ __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+    template <bool HI>
+    static __device__ __forceinline__ uint32_t widen(uint32_t v)
+    {
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 512.f, HI));
+    }
+};
+template <>
+struct Mat<_Float16> {
+    typedef _Float16 Frag __attribute__((ext_vector_type(8)));
+    static __device__ __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+    }
+    template <bool HI>
+    static __device__ __forceinline__ uint32_t widen(uint32_t v)
+    {
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v, 512.f, HI));
+    }
+};
+
+struct GroupedParams {
+    const void *x, *scales, *bias;
+    const uint8_t *codes, *zeros;
+    void* y;
+    int M, N, K, groups, rows;   // rows: outputs a workgroup
+};
+
+// Eight codes of one word: the even ones lie in the low nibbles of its bytes,
+// the odd ones in the high nibbles.  IN_ORDER: k0 k1 .. k7, for two more
+// instructions a word; otherwise k0 k2 k4 k6 k1 k3 k5 k7, and x has to be so too.
+template <typename D, bool IN_ORDER>
+__device__ __forceinline__ typename Mat<D>::Frag widen8(uint32_t w)
+{
+    uint32_t a = w & 0x0F0F0F0Fu, b = (w >> 4) & 0x0F0F0F0Fu;
+    if constexpr (IN_ORDER) {
+        const uint32_t even = a, odd = b;
+        a = __builtin_amdgcn_perm(odd, even, 0x05010400u);
+        b = __builtin_amdgcn_perm(odd, even, 0x07030602u);
+    }
+    const u32x4 v = {Mat<D>::template widen<false>(a), Mat<D>::template widen<true>(a),
+                     Mat<D>::template widen<false>(b), Mat<D>::template widen<true>(b)};
+    return __builtin_bit_cast(typename Mat<D>::Frag, v);
+}
+
+// Eight consecutive values of x in that second order.
+__device__ __forceinline__ u32x4 reorder8(u32x4 x)
+{
+    return u32x4{__builtin_amdgcn_perm(x[1], x[0], 0x05040100u), __builtin_amdgcn_perm(x[3], x[2], 0x05040100u),
+                 __builtin_amdgcn_perm(x[1], x[0], 0x07060302u), __builtin_amdgcn_perm(x[3], x[2], 0x07060302u)};
+}
+
+// 4 x 4 transpose of (lane quarter, word): word j of quarter q becomes what
+// word q of quarter j was.  A group of 32 channels then lies in one word of
+// all four quarters, that is in one matrix instruction.
+__device__ __forceinline__ u32x4 transpose4(u32x4 w)
+{
+    auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+    auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+    auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+    auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+    return u32x4{c[0], c[1], d[0], d[1]};
+}
+
+template <int BYTES>
+struct UintOf;
+template <> struct UintOf<1> { typedef uint8_t type; };
+template <> struct UintOf<2> { typedef uint16_t type; };
+template <> struct UintOf<4> { typedef uint32_t type; };
+template <> struct UintOf<8> { typedef uint64_t type; };
+
+// The value that lane `from / 4` holds.
+__device__ __forceinline__ uint32_t fetch(int from, uint32_t v)
+{
+    return (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v);
+}
+// A workgroup of W waves makes p.rows outputs, at most 16 NT, for up to 16 MT
+// rows of x.  Its waves share the 128-K blocks, a run of consecutive ones each,
+// and add their parts in a fixed order at the end.
+//
+// In a matrix tile lane (r, q) = (lane % 16, lane / 16) owns row r and the
+// channels of quarter q.  Loads that way would touch a line of memory for every
+// lane (and a load costs the lines it touches: 157 against 85 us for 32 x 16384
+// -> 16384), so neighbouring lanes load neighbouring pieces of a row -- of the
+// codes lane / 4 is the row and lane % 4 the 16-byte piece, of x lane / 16 and
+// lane % 16 -- and a wave passes them on through its own part of shared memory.
+// Scales and zero points come for four blocks at a time, lane % 4 the block.
+// Codes are loaded four blocks ahead, x PX.
+//
+// Row m of x sits at row 4 (m % 4) + m / 4 of its matrix tile, so that the
+// first E of the four sums a lane holds are the ones in use for M <= 4 E.
+//
+// OCC: the waves of a SIMD that the registers have to leave room for.
+template <typename D, int GROUP, bool ZEROS, int MT, int E, int NT, int W, int PX, int OCC>
+__global__ __launch_bounds__(W * 64, OCC) void grouped_kernel(GroupedParams p)
+{
+    typedef typename Mat<D>::Frag Frag;
+    constexpr int kPer = 128 / GROUP;                // groups a block
+    constexpr int kSteps = GROUP / 32;               // matrix instructions a group
+    constexpr int kWords = (kPer + 1) / 2;           // words of a block's scales
+    constexpr bool kTurn = GROUP != 128;             // step j holds k = 32 j + 8 q, without it k = 32 q + 8 j
+    constexpr int kXLoads = E * MT;                  // four rows of x a load
+    constexpr bool kInOrder = kXLoads > 2 * NT;      // which of x and the codes is cheaper to reorder
+    typedef typename UintOf<kPer * 2>::type Scales __attribute__((aligned(2)));
+    typedef typename UintOf<kPer>::type Zeros __attribute__((aligned(1)));
+
+    union Shared {
+        u32x4 part[W][(kXLoads + NT) * 64];   // a wave's block of x and of codes, 16-byte pieces
+        float parts[W][MT * NT * E][64];
+    };
+    __shared__ Shared shared;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
+    const int r = lane % 16, q = lane / 16;
+    const int n0 = (int)blockIdx.x * p.rows, n_end = min(n0 + p.rows, p.N);
+    const int m_own = 4 * (r % 4 % E) + r / 4;   // row of x at row r of a matrix tile
+
+    const int blocks = p.K / 128, run = (blocks + W - 1) / W, first = wave * run, end = min(first + run, blocks);
+    f32x4 acc[MT][NT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    // one block, every operand with its owner
+    const auto multiply = [&](const u32x4 (&w)[NT], const u32x4 (&x)[MT][4], const uint32_t (&s)[NT][kWords],
+                              const uint32_t (&z)[NT]) {
+        // sums of x, negated and times the constant zero point
+        Frag offset;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) offset[i] = (D)(ZEROS ? -1.f : -8.f);
+        Frag xf[MT][4];
+        f32x4 sum[MT][kPer];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) xf[mt][j] = __builtin_bit_cast(Frag, x[mt][j]);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                sum[mt][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int j = i * kSteps; j < (i + 1) * kSteps; ++j) sum[mt][i] = Mat<D>::mma(xf[mt][j], offset, sum[mt][i]);
+            }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            u32x4 v = w[nt];
+            if constexpr (kTurn) v = transpose4(v);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                f32x4 part[MT];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) part[mt] = ZEROS ? f32x4{0.f, 0.f, 0.f, 0.f} : sum[mt][i];
+#pragma unroll
+                for (int j = i * kSteps; j < (i + 1) * kSteps; ++j) {
+                    const Frag wf = widen8<D, kInOrder>(ZEROS ? v[j] : v[j] ^ 0x88888888u);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) part[mt] = Mat<D>::mma(xf[mt][j], wf, part[mt]);
+                }
+                const float scale = (float)__builtin_bit_cast(D, (uint16_t)(s[nt][i / 2] >> (16 * (i % 2))));
+                const float zero = ZEROS ? (float)((z[nt] >> (8 * i)) & 0xFFu) : 0.f;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        acc[mt][nt][e] = fmaf(scale, ZEROS ? fmaf(zero, sum[mt][i][e], part[mt][e]) : part[mt][e], acc[mt][nt][e]);
+            }
+        }
+    };
+
+    if (first < end) {
+        // offsets of a lane from a base that is the same for the whole wave
+        const uint8_t* const codes = p.codes + (int64_t)n0 * (p.K / 2);
+        const uint16_t* const scales = (const uint16_t*)p.scales + (int64_t)n0 * p.groups;
+        const uint8_t* const zeros = p.zeros + (int64_t)n0 * p.groups;
+        uint32_t w_at[NT], s_at[NT], x_at[kXLoads];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const uint32_t n = min(16 * nt + lane / 4, n_end - 1 - n0);   // outputs past the end are computed and not stored
+            w_at[nt] = n * (uint32_t)(p.K / 2) + 16 * (lane % 4);
+            s_at[nt] = n * (uint32_t)p.groups;
+        }
+#pragma unroll
+        for (int i = 0; i < kXLoads; ++i) x_at[i] = (uint32_t)min(4 * i + lane / 16, p.M - 1) * (uint32_t)(2 * p.K) + 16 * (lane % 16);
+        u32x4 w[4][NT], x[PX][kXLoads];
+        uint32_t s[NT][kWords], z[NT];
+        const auto load_w = [&](u32x4 (&to)[NT], int b) {
+            const uint8_t* const base = codes + b * 64;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) to[nt] = *(const u32x4*)(base + w_at[nt]);
+        };
+        const auto load_x = [&](u32x4 (&to)[kXLoads], int b) {
+            const uint8_t* const base = (const uint8_t*)p.x + b * 256;
+#pragma unroll
+            for (int i = 0; i < kXLoads; ++i) to[i] = *(const u32x4*)(base + x_at[i]);
+        };
+        const auto load_s = [&](uint32_t (&to)[NT][kWords], uint32_t (&to_z)[NT], int b) {
+            const uint32_t at = (uint32_t)min(b + lane % 4, blocks - 1) * kPer;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const auto v = *(const Scales*)((const uint8_t*)scales + 2 * (s_at[nt] + at));
+                to[nt][0] = (uint32_t)v;
+                if constexpr (kPer == 4) to[nt][1] = (uint32_t)(v >> 32);
+                if constexpr (ZEROS) to_z[nt] = *(const Zeros*)(zeros + (s_at[nt] + at));
+            }
+        };
+        // The wave's own part of shared memory, whose accesses happen in order.
+        // Piece c of row m of x lies at 16 m + (c ^ m), piece c of row r of the
+        // codes at 4 r + (c ^ r / 4): the 16 lanes that read one piece of 16
+        // rows meet 16 different places.
+        u32x4* const part_x = shared.part[wave];
+        u32x4* const part_w = part_x + kXLoads * 64;
+        const auto take_x = [&](u32x4 (&to)[MT][4], const u32x4 (&from)[kXLoads]) {
+#pragma unroll
+            for (int i = 0; i < kXLoads; ++i) {
+                const int m = 4 * i + lane / 16;
+                part_x[16 * m + ((lane % 16) ^ (m % 16))] = kInOrder ? from[i] : reorder8(from[i]);
+            }
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) to[mt][i] = part_x[16 * (16 * mt + m_own) + ((kTurn ? 4 * i + q : 4 * q + i) ^ m_own)];
+            __builtin_amdgcn_wave_barrier();
+        };
+        const auto take_w = [&](u32x4 (&to)[NT], const u32x4 (&from)[NT]) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) part_w[64 * nt + (lane ^ lane / 16)] = from[nt];
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) to[nt] = part_w[64 * nt + 4 * r + (q ^ r / 4)];
+            __builtin_amdgcn_wave_barrier();
+        };
+        const auto take_s = [&](uint32_t (&so)[NT][kWords], uint32_t (&zo)[NT], int j) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int i = 0; i < kWords; ++i) so[nt][i] = fetch(4 * (4 * r + j), s[nt][i]);
+                zo[nt] = ZEROS ? fetch(4 * (4 * r + j), z[nt]) : 0;
+            }
+        };
+        // Loads return in order, so what is used first is asked for first: x of a
+        // block before its codes.
+        load_s(s, z, first);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (j < PX) load_x(x[j], min(first + j, end - 1));
+            load_w(w[j], min(first + j, end - 1));
+        }
+        u32x4 xo[MT][4];
+        int b = first;
+        for (; b + 4 < end; b += 4) {
+            uint32_t next_s[NT][kWords], next_z[NT];
+            load_s(next_s, next_z, b + 4);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                u32x4 wo[NT];
+                uint32_t so[NT][kWords], zo[NT];
+                take_x(xo, x[j % PX]);
+                load_x(x[j % PX], min(b + j + PX, end - 1));
+                take_s(so, zo, j);
+                take_w(wo, w[j]);
+                load_w(w[j], min(b + j + 4, end - 1));
+                __builtin_amdgcn_sched_barrier(0);
+                multiply(wo, xo, so, zo);
+                __builtin_amdgcn_sched_barrier(0);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int i = 0; i < kWords; ++i) s[nt][i] = next_s[nt][i];
+                if constexpr (ZEROS) z[nt] = next_z[nt];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (b + j < end) {
+                u32x4 wo[NT];
+                uint32_t so[NT][kWords], zo[NT];
+                take_x(xo, x[j % PX]);
+                if (j + PX < 4) load_x(x[j % PX], min(b + j + PX, end - 1));
+                take_s(so, zo, j);
+                take_w(wo, w[j]);
+                __builtin_amdgcn_sched_barrier(0);
+                multiply(wo, xo, so, zo);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+    }
+    if (wave == W - 1 && p.K % 128 != 0) {   // a row that ends inside a block: zeros behind it
+        u32x4 w[NT], x[MT][4];
+        uint32_t s[NT][kWords] = {}, z[NT] = {};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int64_t n = min(n0 + 16 * nt + r, n_end - 1);
+            w[nt] = u32x4{0u, 0u, 0u, 0u};
+            if (blocks * 128 + 32 * q < p.K) w[nt] = *(const u32x4*)(p.codes + n * (p.K / 2) + blocks * 64 + 16 * q);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (blocks * kPer + i < p.groups) {
+                    const int64_t g = n * p.groups + blocks * kPer + i;
+                    s[nt][i / 2] |= (uint32_t)((const uint16_t*)p.scales)[g] << (16 * (i % 2));
+                    if constexpr (ZEROS) z[nt] |= (uint32_t)p.zeros[g] << (8 * i);
+                }
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const int m = 16 * mt + m_own;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int k = blocks * 128 + (kTurn ? 32 * j + 8 * q : 32 * q + 8 * j);
+                x[mt][j] = u32x4{0u, 0u, 0u, 0u};
+                if (k < p.K) x[mt][j] = *(const u32x4*)((const uint16_t*)p.x + (int64_t)min(m, p.M - 1) * p.K + k);
+                if constexpr (!kInOrder) x[mt][j] = reorder8(x[mt][j]);
+            }
+        }
+        multiply(w, x, s, z);
+    }
+    __syncthreads();   // x is done with
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < E; ++e) shared.parts[wave][(mt * NT + nt) * E + e][lane] = acc[mt][nt][e];
+    __syncthreads();
+    for (int i = threadIdx.x; i < MT * NT * E * 64; i += W * 64) {
+        const int slot = i / 64, l = i % 64, mt = slot / (E * NT), nt = slot / E % NT, e = slot % E;
+        const int m = 16 * mt + 4 * e + l / 16, n = n0 + 16 * nt + l % 16;
+        if (m >= p.M || n >= n_end) continue;
+        float v = 0.f;
+#pragma unroll
+        for (int k = 0; k < W; ++k) v += shared.parts[k][slot][l];
+        if (p.bias) v += (float)((const D*)p.bias)[n];
+        ((D*)p.y)[(int64_t)m * p.N + n] = (D)v;
+    }
+}
+
+template <typename D, int GROUP, bool ZEROS, int MT, int E, int NT, int W, int PX, int OCC>
+void launch_one(GroupedParams p, hipStream_t s)
+{
+    hipLaunchKernelGGL((grouped_kernel<D, GROUP, ZEROS, MT, E, NT, W, PX, OCC>), dim3((p.N + p.rows - 1) / p.rows),
+                       dim3(W * 64), 0, s, p);
+}
+
+// Which variant, by M and N (times in a graph, us):
+// M <= 4: x is small, so one tile a workgroup and many workgroups; four waves
+//   from N > 8192 on (1 x 4096 -> 16384: 10.5 against 11.1 with eight; 4096 ->
+//   4096: 5.0 with eight); a long row of few outputs gets half-filled tiles, to
+//   have a workgroup for every unit (4 x 12288 -> 2048: 7.5 against 8.5).
+// M > 4: every workgroup reads all of x, so it takes as many outputs as one
+//   round (or several equal ones) over the units allows, up to 64 (16 x 4096 ->
+//   16384: 12.3 with 64 outputs, 16.8 with 32, 16.0 with 16).
+constexpr int kUnits = 256;   // compute units of an MI355X
+template <typename D, int GROUP, bool ZEROS>
+void launch_zeros(GroupedParams p, hipStream_t s)
+{
+    if (p.M <= 4) {
+        p.rows = p.N <= 2048 && p.K >= 8192 ? 8 : 16;
+        if (p.N > 8192) launch_one<D, GROUP, ZEROS, 1, 1, 1, 4, 4, 4>(p, s);
+        else launch_one<D, GROUP, ZEROS, 1, 1, 1, 8, 4, 4>(p, s);
+        return;
+    }
+    const int rounds = (p.N + 64 * kUnits - 1) / (64 * kUnits);
+    p.rows = (p.N + rounds * kUnits - 1) / (rounds * kUnits);
+    if (p.rows < 16) p.rows = 16;
+    const int tiles = (p.rows + 15) / 16;
+    if (p.M <= 8) {
+        if (tiles == 1) launch_one<D, GROUP, ZEROS, 1, 2, 1, 8, 2, 2>(p, s);
+        else if (tiles == 2) launch_one<D, GROUP, ZEROS, 1, 2, 2, 8, 4, 2>(p, s);
+        else if (tiles == 3) launch_one<D, GROUP, ZEROS, 1, 2, 3, 8, 4, 2>(p, s);
+        else launch_one<D, GROUP, ZEROS, 1, 2, 4, 8, 2, 2>(p, s);
+    } else if (p.M <= 16) {
+        if (tiles == 1) launch_one<D, GROUP, ZEROS, 1, 4, 1, 8, 1, 2>(p, s);
+        else if (tiles == 2) launch_one<D, GROUP, ZEROS, 1, 4, 2, 8, 2, 2>(p, s);
+        else if (tiles == 3) launch_one<D, GROUP, ZEROS, 1, 4, 3, 8, 2, 2>(p, s);
+        else launch_one<D, GROUP, ZEROS, 1, 4, 4, 8, 2, 2>(p, s);
+    } else {
+        if (tiles == 1) launch_one<D, GROUP, ZEROS, 2, 4, 1, 8, 1, 2>(p, s);
+        else if (tiles == 2) launch_one<D, GROUP, ZEROS, 2, 4, 2, 8, 1, 2>(p, s);
+        else if (tiles == 3) launch_one<D, GROUP, ZEROS, 2, 4, 3, 4, 1, 1>(p, s);
+        else launch_one<D, GROUP, ZEROS, 2, 4, 4, 4, 2, 1>(p, s);
+    }
+}
+
+template <typename D, int GROUP>
+void launch_group(const GroupedParams& p, hipStream_t s)
+{
+    p.zeros ? launch_zeros<D, GROUP, true>(p, s) : launch_zeros<D, GROUP, false>(p, s);
+}
+
+template <typename D>
+void launch_type(const GroupedParams& p, int group, hipStream_t s)
+{
+    if (group == 32) launch_group<D, 32>(p, s);
+    else if (group == 64) launch_group<D, 64>(p, s);
+    else launch_group<D, 128>(p, s);
+}
+
+}  // namespace grouped
+}  // namespace convrot
