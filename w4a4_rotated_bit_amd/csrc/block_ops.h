@@ -39,61 +39,62 @@ void launch_linear_grouped(const convrot_grouped_args& a, hipStream_t s);
 void launch_quantize_grouped(const void* W, int64_t N, int64_t K, int group, int dtype, uint8_t* codes, void* scales,
                              uint8_t* zeros, hipStream_t s);
 
+constexpr int kUnits = 256;   // compute units of an MI355X
+
 // ---- device helpers ---------------------------------------------------------
 
 template <typename T, int N>
 struct VecOf {
     typedef T type __attribute__((ext_vector_type(N)));
 };
-template <typename T>
-struct VecOf<T, 1> {
-    typedef T type;
-};
 
-// N consecutive elements at p, as one load (p aligned to the vector) widened to binary32.
-template <typename T, int N>
-__device__ __forceinline__ void load_f32(const T* p, float (&v)[N])
+// V consecutive elements, in one access whatever their alignment.
+template <typename T, int V>
+__device__ __forceinline__ typename VecOf<T, V>::type load_chunk(const T* p)
 {
-    if constexpr (N == 1) {
-        v[0] = (float)*p;
-    } else if constexpr (sizeof(T) * N > 16) {
-        constexpr int H = N / 2;
-        typedef typename VecOf<T, H>::type V;
-        const V a = *(const V*)p, b = *(const V*)(p + H);
-#pragma unroll
-        for (int i = 0; i < H; ++i) {
-            v[i] = (float)a[i];
-            v[H + i] = (float)b[i];
-        }
-    } else {
-        typedef typename VecOf<T, N>::type V;
-        const V a = *(const V*)p;
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = (float)a[i];
-    }
+    typedef typename VecOf<T, V>::type Any __attribute__((aligned(sizeof(T))));
+    return *(const Any*)p;
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_chunk(T* p, typename VecOf<T, V>::type v)
+{
+    typedef typename VecOf<T, V>::type Any __attribute__((aligned(sizeof(T))));
+    *(Any*)p = v;
 }
 
-// The same values rounded to T (nearest even) and stored.
-template <typename T, int N>
-__device__ __forceinline__ void store_f32(T* p, const float (&v)[N])
+// v of another lane of the same 16, by a lane permutation of the vector unit
+// (a shuffle through shared memory takes some ten times as long).
+template <int CTRL>
+__device__ __forceinline__ float lane_perm(float v)
 {
-    if constexpr (N == 1) {
-        *p = (T)v[0];
-    } else {
-        typedef typename VecOf<T, N>::type V;
-        V a;
-#pragma unroll
-        for (int i = 0; i < N; ++i) a[i] = (T)v[i];
-        *(V*)p = a;
-    }
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
 }
 
-// Sum over the W lanes of an aligned group (W a power of two, at most 64).
+// Sum over the W lanes of an aligned group (W a power of two, at most 64), the
+// same bits in all of them.
 template <int W>
 __device__ __forceinline__ float lane_sum(float v)
 {
-#pragma unroll
-    for (int d = 1; d < W; d *= 2) v += __shfl_xor(v, d, 64);
+    if constexpr (W >= 2) v += lane_perm<0xB1>(v);    // neighbour
+    if constexpr (W >= 4) v += lane_perm<0x4E>(v);    // other pair of four
+    if constexpr (W >= 8) v += lane_perm<0x141>(v);   // other four of eight, mirrored
+    if constexpr (W >= 16) v += lane_perm<0x140>(v);  // other eight of sixteen, mirrored
+    // rows of 16 lanes, then halves of 32, swapped between v and a copy of it (in
+    // a register of its own: swapped with itself a register stays as it is)
+    if constexpr (W >= 32) {
+        int i = __builtin_bit_cast(int, v), copy = i;
+        asm volatile("" : "+v"(copy));
+        const auto r = __builtin_amdgcn_permlane16_swap(i, copy, false, false);
+        const uint32_t a = r[0], b = r[1];
+        v = __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b);
+    }
+    if constexpr (W >= 64) {
+        int i = __builtin_bit_cast(int, v), copy = i;
+        asm volatile("" : "+v"(copy));
+        const auto r = __builtin_amdgcn_permlane32_swap(i, copy, false, false);
+        const uint32_t a = r[0], b = r[1];
+        v = __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b);
+    }
     return v;
 }
 

@@ -381,7 +381,6 @@ void launch_one(GroupedParams p, hipStream_t s)
 // M > 4: every workgroup reads all of x, so it takes as many outputs as one
 //   round (or several equal ones) over the units allows, up to 64 (16 x 4096 ->
 //   16384: 12.3 with 64 outputs, 16.8 with 32, 16.0 with 16).
-constexpr int kUnits = 256;   // compute units of an MI355X
 template <typename D, int GROUP, bool ZEROS>
 void launch_zeros(GroupedParams p, hipStream_t s)
 {

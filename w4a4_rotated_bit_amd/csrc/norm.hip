@@ -9,7 +9,7 @@
 // last store, so each of x, y, r and h crosses memory once; the statistics are
 // sums of binary32 in registers (LayerNorm: the mean first, then the squared
 // deviations, so that a large mean costs nothing), and N works on r as it is
-// before its rounding to the storage type.
+// before its rounding to the storage type.  
 #include "block_ops.h"
 
 namespace convrot {
@@ -23,11 +23,11 @@ struct NormParams {
     int rows, rows_per_vec, width;
     int norm, post_norm;
     float a, eps, inv_width;
+    bool in_place;   // r or h is x or y
 };
 
-// Sum over the T threads of a row.  `slot` alternates between calls, so that
-// one barrier a call is enough: a thread writes a slot again only after a
-// barrier that every thread reached after reading it.
+// Sum over the T threads of a row; every sum of a kernel has slots of its own,
+// so one barrier is enough.
 template <int T>
 __device__ __forceinline__ float row_sum(float v, float* slot)
 {
@@ -43,184 +43,170 @@ __device__ __forceinline__ float row_sum(float v, float* slot)
     return v;
 }
 
-// Row statistics of v: the factor and offset of v -> (v - mean) / sqrt(var + eps).
-template <int T, int V, int NV>
-__device__ __forceinline__ void row_stats(const float (&v)[NV][V], const bool (&in)[NV], int kind, float inv_width,
-                                          float eps, float* slots, float& mean, float& rstd)
-{
-    mean = 0.f;
-    if (kind == CONVROT_NORM_LAYER) {
-        float s = 0.f;
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int i = 0; i < V; ++i) s += v[j][i];   // zero outside the row
-        mean = row_sum<T>(s, slots) * inv_width;
-    }
-    float q = 0.f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-        if (in[j])
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float d = v[j][i] - mean;
-                q = fmaf(d, d, q);
-            }
-    rstd = 1.f / sqrtf(row_sum<T>(q, slots + T / 64) * inv_width + eps);
-}
-
-// T threads a row, NV chunks of V elements a thread.
-template <typename D, typename E, int T, int V, int NV>
+// D: type of the rows, E: of the vectors.  T threads a row, NV chunks of V
+// elements a thread.  EARLY: the vectors are loaded with the row, before its
+// sums, instead of where they are needed.
+//
+// TAIL: V does not divide the width.  The last chunk then ends where the row
+// ends and begins inside the chunk before it; the elements both have are left
+// out of its sums, and stored twice with the same value.
+template <typename D, typename E, int T, int V, int NV, bool TAIL, bool EARLY>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void residual_norm_kernel(NormParams p)
 {
-    constexpr int kRows = T < 256 ? 256 / T : 1;   // rows a workgroup
+    constexpr int kRows = T < 256 ? 256 / T : 1;   // rows at a time
     static_assert(T == 64 || kRows == 1, "several rows share a workgroup only where a row is one wave");
-    __shared__ float slots[T > 64 ? 4 * (T / 64) : 1];
+    typedef typename VecOf<D, V>::type Chunk;
+    typedef typename VecOf<E, V>::type Vector;
+    constexpr int kSlots = T > 64 ? 4 * (T / 64) : 1;
+    __shared__ float slots[kSlots];
     const int t = threadIdx.x % T;
     const int64_t row = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kRows + threadIdx.x / T;
-    if (row >= p.rows) return;   // whole waves; a workgroup with barriers has one row
-    const int64_t vec = row / p.rows_per_vec;
 
-    int at[NV];
+    int at[NV], skip[NV];   // a chunk's first element, and how many of its elements the chunk before it has
     bool in[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         at[j] = (j * T + t) * V;
         in[j] = at[j] < p.width;
-    }
-    const D* x = (const D*)p.x + row * p.x_stride;
-    float r[NV][V];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) r[j][i] = 0.f;
-        if (in[j]) load_f32<D, V>(x + at[j], r[j]);
-    }
-    if (p.y) {
-        const D* y = (const D*)p.y + row * p.y_stride;
-        float z[NV][V];
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) z[j][i] = 0.f;
-            if (in[j]) load_f32<D, V>(y + at[j], z[j]);
+        skip[j] = 0;
+        if (TAIL && at[j] + V > p.width) {
+            skip[j] = in[j] ? at[j] + V - p.width : V;
+            at[j] = p.width - V;
         }
+    }
+    const auto load_vector = [&](Vector (&to)[NV], const void* from) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (in[j]) to[j] = load_chunk<E, V>((const E*)from + at[j]);
+    };
+    // f(j, i) for every element
+    const auto all = [&](auto&& f) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i) f(j, i);
+    };
+    // v -> (v - mean) rstd, with the sums of the row in `slots`
+    const auto normalise = [&](float (&v)[NV][V], int kind, float* slots) {
+        float mean = 0.f, q = 0.f;
+        if (kind == CONVROT_NORM_LAYER) {
+            float sum = 0.f;
+            all([&](int j, int i) { sum += in[j] && (!TAIL || i >= skip[j]) ? v[j][i] : 0.f; });
+            mean = row_sum<T>(sum, slots) * p.inv_width;
+            all([&](int j, int i) { v[j][i] -= mean; });
+        }
+        all([&](int j, int i) { q = in[j] && (!TAIL || i >= skip[j]) ? fmaf(v[j][i], v[j][i], q) : q; });
+        const float rstd = 1.f / sqrtf(row_sum<T>(q, slots + T / 64) * p.inv_width + p.eps);
+        all([&](int j, int i) { v[j][i] *= rstd; });
+    };
+
+    if (row >= p.rows) return;   // whole waves; a workgroup with barriers has one row
+    Vector gate[NV], scale[NV], shift[NV], weight[NV], post_weight[NV];
+    const D* const xp = (const D*)p.x + row * p.x_stride;
+    const D* const yp = (const D*)p.y + row * p.y_stride;
+    Chunk x[NV], y[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+        if (in[j]) x[j] = load_chunk<D, V>(xp + at[j]);
+    if (p.y) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (in[j]) y[j] = load_chunk<D, V>(yp + at[j]);
+    }
+    const int64_t vec = row / p.rows_per_vec;
+    const E* const gate_p = (const E*)p.gate + vec * p.gate_stride;
+    const E* const scale_p = (const E*)p.scale + vec * p.scale_stride;
+    const E* const shift_p = (const E*)p.shift + vec * p.shift_stride;
+    if (EARLY) {
+        if (p.post_weight) load_vector(post_weight, p.post_weight);
+        if (p.weight) load_vector(weight, p.weight);
+        if (p.gate) load_vector(gate, gate_p);
+        if (p.scale) load_vector(scale, scale_p);
+        if (p.shift) load_vector(shift, shift_p);
+    }
+    if (TAIL && T > 64 && p.in_place) {   // every wave has read what the last chunk shares before it is written
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+    }
+    float r[NV][V];
+    all([&](int j, int i) { r[j][i] = p.a * (float)x[j][i]; });
+    if (p.y) {
+        float z[NV][V];
+        all([&](int j, int i) { z[j][i] = (float)y[j][i]; });
         if (p.post_norm != CONVROT_NORM_NONE) {
-            float mean, rstd;
-            row_stats<T, V, NV>(z, in, p.post_norm, p.inv_width, p.eps, slots, mean, rstd);
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                float w[V];
-#pragma unroll
-                for (int i = 0; i < V; ++i) w[i] = 1.f;
-                if (p.post_weight && in[j]) load_f32<E, V>((const E*)p.post_weight + at[j], w);
-#pragma unroll
-                for (int i = 0; i < V; ++i) z[j][i] = (z[j][i] - mean) * rstd * w[i];
+            normalise(z, p.post_norm, slots);
+            if (p.post_weight) {
+                if (!EARLY) load_vector(post_weight, p.post_weight);
+                all([&](int j, int i) { z[j][i] *= (float)post_weight[j][i]; });
             }
         }
+        if (p.gate) {
+            if (!EARLY) load_vector(gate, gate_p);
+            all([&](int j, int i) { r[j][i] = fmaf((float)gate[j][i], z[j][i], r[j][i]); });
+        } else {
+            all([&](int j, int i) { r[j][i] += z[j][i]; });
+        }
+    }
+    const auto store = [&](D* to) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            float g[V];
+            Chunk c;
 #pragma unroll
-            for (int i = 0; i < V; ++i) g[i] = 1.f;
-            if (p.gate && in[j]) load_f32<E, V>((const E*)p.gate + vec * p.gate_stride + at[j], g);
-#pragma unroll
-            for (int i = 0; i < V; ++i) r[j][i] = fmaf(g[i], z[j][i], p.a * r[j][i]);
+            for (int i = 0; i < V; ++i) c[i] = (D)r[j][i];
+            if (in[j]) store_chunk<D, V>(to + at[j], c);
         }
-    } else {
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int i = 0; i < V; ++i) r[j][i] *= p.a;
-    }
-    if (p.r) {
-        D* out = (D*)p.r + row * p.r_stride;
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if (in[j]) store_f32<D, V>(out + at[j], r[j]);
-    }
+    };
+    if (p.r) store((D*)p.r + row * p.r_stride);
     if (!p.h) return;
-
-    if (p.norm != CONVROT_NORM_NONE) {
-        // elements outside the row have to stay out of the sums
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if (!in[j])
-#pragma unroll
-                for (int i = 0; i < V; ++i) r[j][i] = 0.f;
-        float mean, rstd;
-        row_stats<T, V, NV>(r, in, p.norm, p.inv_width, p.eps, slots + (T > 64 ? 2 * (T / 64) : 0), mean, rstd);
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int i = 0; i < V; ++i) r[j][i] = (r[j][i] - mean) * rstd;
+    if (p.norm != CONVROT_NORM_NONE) normalise(r, p.norm, slots + (T > 64 ? 2 * (T / 64) : 0));
+    if (p.weight) {
+        if (!EARLY) load_vector(weight, p.weight);
+        all([&](int j, int i) { r[j][i] *= (float)weight[j][i]; });
     }
-    D* out = (D*)p.h + row * p.h_stride;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        if (!in[j]) continue;
-        float v[V];
-        if (p.weight) {
-            load_f32<E, V>((const E*)p.weight + at[j], v);
-#pragma unroll
-            for (int i = 0; i < V; ++i) r[j][i] *= v[i];
-        }
-        if (p.scale) {
-            load_f32<E, V>((const E*)p.scale + vec * p.scale_stride + at[j], v);
-#pragma unroll
-            for (int i = 0; i < V; ++i) r[j][i] = fmaf(r[j][i], v[i], r[j][i]);
-        }
-        if (p.shift) {
-            load_f32<E, V>((const E*)p.shift + vec * p.shift_stride + at[j], v);
-#pragma unroll
-            for (int i = 0; i < V; ++i) r[j][i] += v[i];
-        }
-        store_f32<D, V>(out + at[j], r[j]);
+    if (p.scale) {
+        if (!EARLY) load_vector(scale, scale_p);
+        all([&](int j, int i) { r[j][i] = fmaf(r[j][i], (float)scale[j][i], r[j][i]); });
     }
+    if (p.shift) {
+        if (!EARLY) load_vector(shift, shift_p);
+        all([&](int j, int i) { r[j][i] += (float)shift[j][i]; });
+    }
+    store((D*)p.h + row * p.h_stride);
 }
 
-template <typename D, typename E, int T, int V, int NV>
+template <typename D, typename E, int T, int V, int NV, bool TAIL>
 void launch_one(const NormParams& p, hipStream_t s)
 {
-    constexpr int kRows = T < 256 ? 256 / T : 1;
+    constexpr int kThreads = T < 256 ? 256 : T, kRows = kThreads / T;
     // a grid dimension holds fewer than 2^32 threads
     const unsigned blocks = (p.rows + kRows - 1) / kRows, gx = blocks < (1u << 20) ? blocks : 1u << 20;
-    hipLaunchKernelGGL((residual_norm_kernel<D, E, T, V, NV>), dim3(gx, (blocks + gx - 1) / gx),
-                       dim3(T < 256 ? 256 : T), 0, s, p);
+    // registers for the vectors too only where that leaves as many rows resident
+    hipLaunchKernelGGL((residual_norm_kernel<D, E, T, V, NV, TAIL, (NV == 1)>), dim3(gx, (blocks + gx - 1) / gx),
+                       dim3(kThreads), 0, s, p);
 }
 
-template <typename D, typename E, int V>
+template <typename D, typename E, bool TAIL>
 void launch_width(const NormParams& p, hipStream_t s)
 {
+    constexpr int V = 16 / sizeof(D);
     const int chunks = (p.width + V - 1) / V;
-    if (chunks <= 64) return launch_one<D, E, 64, V, 1>(p, s);
-    if (chunks <= 256) return launch_one<D, E, 256, V, 1>(p, s);
-    if (chunks <= 512) return launch_one<D, E, 256, V, 2>(p, s);
-    if (chunks <= 1024) return launch_one<D, E, 256, V, 4>(p, s);
-    if (chunks <= 2048) return launch_one<D, E, 1024, V, 2>(p, s);
-    if (chunks <= 4096) return launch_one<D, E, 1024, V, 4>(p, s);
-    if constexpr (V == 1) launch_one<D, E, 1024, V, 16>(p, s);   // up to 16384 scalars
-}
-
-bool vec_ok(const void* p, int64_t stride, int bytes, int V)
-{
-    return !p || ((uintptr_t)p % (V * bytes < 16 ? V * bytes : 16) == 0 && stride % V == 0);
+    if (chunks <= 64) launch_one<D, E, 64, V, 1, TAIL>(p, s);
+    else if (chunks <= 128) launch_one<D, E, 64, V, 2, TAIL>(p, s);
+    else if (chunks <= 256) launch_one<D, E, 256, V, 1, TAIL>(p, s);
+    else if (chunks <= 512 && p.rows <= kUnits) launch_one<D, E, 512, V, 1, TAIL>(p, s);
+    else if (chunks <= 512) launch_one<D, E, 256, V, 2, TAIL>(p, s);
+    else if (chunks <= 1024) launch_one<D, E, 512, V, 2, TAIL>(p, s);
+    else if (chunks <= 2048) launch_one<D, E, 1024, V, 2, TAIL>(p, s);
+    else if constexpr (V == 4) launch_one<D, E, 1024, V, 4, TAIL>(p, s);
 }
 
 template <typename D, typename E>
-void launch_types(const convrot_residual_norm_args& a, const NormParams& p, hipStream_t s)
+void launch_types(const NormParams& p, hipStream_t s)
 {
     constexpr int V = 16 / sizeof(D);
-    const int db = sizeof(D), eb = sizeof(E);
-    const bool wide = a.width % V == 0 && vec_ok(a.x_dev, a.x_stride, db, V) && vec_ok(a.y_dev, a.y_stride, db, V) &&
-                      vec_ok(a.r_dev, a.r_stride, db, V) && vec_ok(a.h_dev, a.h_stride, db, V) &&
-                      vec_ok(a.gate_dev, a.gate_stride, eb, V) && vec_ok(a.scale_dev, a.scale_stride, eb, V) &&
-                      vec_ok(a.shift_dev, a.shift_stride, eb, V) && vec_ok(a.weight_dev, 0, eb, V) &&
-                      vec_ok(a.post_weight_dev, 0, eb, V);
-    if (wide)
-        launch_width<D, E, V>(p, s);
-    else
-        launch_width<D, E, 1>(p, s);
+    if (p.width < V) launch_one<D, E, 64, 1, 1, false>(p, s);   // shorter than a chunk
+    else if (p.width % V == 0) launch_width<D, E, false>(p, s);
+    else launch_width<D, E, true>(p, s);
 }
 
 }  // namespace
@@ -252,13 +238,14 @@ void launch_residual_norm(const convrot_residual_norm_args& a, hipStream_t s)
     p.a = a.residual_scale;
     p.eps = a.eps;
     p.inv_width = 1.f / (float)a.width;
+    p.in_place = a.r_dev == a.x_dev || a.h_dev == a.x_dev || (a.y_dev && (a.r_dev == a.y_dev || a.h_dev == a.y_dev));
     const bool f32v = a.vec_dtype == CONVROT_F32;
     if (a.dtype == CONVROT_BF16)
-        f32v ? launch_types<__bf16, float>(a, p, s) : launch_types<__bf16, __bf16>(a, p, s);
+        f32v ? launch_types<__bf16, float>(p, s) : launch_types<__bf16, __bf16>(p, s);
     else if (a.dtype == CONVROT_F16)
-        f32v ? launch_types<_Float16, float>(a, p, s) : launch_types<_Float16, _Float16>(a, p, s);
+        f32v ? launch_types<_Float16, float>(p, s) : launch_types<_Float16, _Float16>(p, s);
     else
-        launch_types<float, float>(a, p, s);
+        launch_types<float, float>(p, s);
 }
 
 }  // namespace convrot
