@@ -17,7 +17,6 @@ namespace convrot {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRopeEach = 4;   // heads a group of lanes
 
 struct Heads {
     const void* in;
@@ -32,8 +31,7 @@ struct RopeParams {
     const void* pos;
     int64_t pos_batch, pos_token;
     int count, tokens, dim, pairs, pos_dtype, norm;
-    int tile, parts, slots;   // tokens a workgroup, workgroups a token, heads a workgroup and token
-    uint32_t per_slot;        // 65536 / slots, rounded up
+    int tile;   // rope_any_kernel: tokens a workgroup
     float eps, inv_dim;
     RopePlan plan;
 };
@@ -55,137 +53,143 @@ enum Exchange { PAIRS, CHUNKS, ELEMENTS };   // how a lane gets the other elemen
 
 // Even heads of at least one 16-byte chunk.  L lanes a head, lane c holding
 // chunk c (the last one ends where the head ends, and may share elements with
-// the one before it; both write the same values).  A workgroup takes `tile`
-// tokens, or some of the heads of one, at most kEach heads a lane group: it asks
-// for all of them first, then works out the angles while they arrive.
+// the one before it; both write the same values), so a wave holds 64 / L heads:
+// one item.  A wave takes IW items of one token: it asks for all of them, works
+// out the token's angles while they arrive, one or two a lane, and passes those
+// on through its own part of shared memory; nothing waits for another wave.
 //   PAIRS:    interleaved pairs, within the chunk
 //   CHUNKS:   halves of whole chunks: the pairs' other elements are one lane's
 //   ELEMENTS: halves of any size: through shared memory
-// Lanes of a head are in one wave, whose loads all precede its stores: the
-// output may be the input.
-template <typename D, int L, Exchange EX>
+// All loads of an item precede its stores: the output may be the input.
+template <typename D, int L, Exchange EX, int IW>
 __global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p)
 {
-    constexpr int V = 16 / sizeof(D), kGroups = kThreads / L, kEach = kRopeEach;
+    constexpr int V = 16 / sizeof(D), kHeads = 64 / L;
     typedef typename VecOf<D, V>::type Chunk;
     typedef uint32_t Words __attribute__((ext_vector_type(4)));
-    extern __shared__ __attribute__((aligned(16))) float shared[];
-    float2* const cs = (float2*)shared;                                // [tile][pairs]
-    float* const weights = shared + 2 * p.tile * p.pairs;              // [tensor][dim] where there are any
-    D* const rows = (D*)(weights + (p.norm ? p.count * p.dim : 0));    // ELEMENTS: [group][dim]
-    const int64_t b = blockIdx.y;
-    const int part = (int)blockIdx.z % p.parts;                        // of a token's heads
-    const int t0 = (int)(blockIdx.z / p.parts * gridDim.x + blockIdx.x) * p.tile, nt = min(p.tile, p.tokens - t0);
-    const int group = threadIdx.x / L, c = threadIdx.x % L;
-    if (nt <= 0) return;
-    const int slots = p.slots, items = nt * slots;                     // heads a token here, heads here
-
+    __shared__ float2 angles[kThreads / 64][kMaxRopePairs];
+    __shared__ __attribute__((aligned(16))) D rows[EX == ELEMENTS ? kThreads / 64 : 1][EX == ELEMENTS ? 64 * V : 1];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
+    const int64_t b = blockIdx.y, t = (int64_t)blockIdx.x * (kThreads / 64) + wave;
+    if (t >= p.tokens) return;
+    const int g = lane / L, c = lane % L;
     const bool in = c * V < p.dim;
     const int at = min(c * V, p.dim - V), skip = c * V - at;
-    int tensor[kEach], token[kEach], head[kEach];
-    Chunk x[kEach];
-#pragma unroll
-    for (int u = 0; u < kEach; ++u) {
-        const int item = group + u * kGroups;
-        token[u] = (int)((uint32_t)item * p.per_slot >> 16);           // item / slots
-        head[u] = item - token[u] * slots + part * slots;
-        tensor[u] = head[u] >= p.t[0].heads;
-        if (tensor[u]) head[u] -= p.t[0].heads;
-        if (item >= items || (tensor[u] && (p.count < 2 || head[u] >= p.t[1].heads))) token[u] = -1;
-        if (token[u] >= 0 && in) {
-            const Heads& h = p.t[tensor[u]];
-            x[u] = load_chunk<D, V>((const D*)h.in + b * h.in_batch + (t0 + token[u]) * h.in_token +
-                                    head[u] * h.in_head + at);
-        }
-    }
-    for (int i = threadIdx.x; i < nt * p.pairs; i += kThreads) {
-        const int t = i / p.pairs;
-        cs[i] = turn(p, b, t0 + t, i - t * p.pairs);
-    }
-    if (p.norm)
-        for (int i = threadIdx.x; i < p.count * p.dim; i += kThreads) {
-            const D* w = (const D*)p.t[i >= p.dim].weight;
-            weights[i] = w ? (float)w[i >= p.dim ? i - p.dim : i] : 1.f;
-        }
-    __syncthreads();
+    const int items0 = (p.t[0].heads + kHeads - 1) / kHeads;
+    const int items = items0 + (p.count > 1 ? (p.t[1].heads + kHeads - 1) / kHeads : 0);
+    const int first = (int)blockIdx.z * IW;
 
+    // lane offsets within an item; everything else about it is the same for the wave
+    const int64_t in0 = g * p.t[0].in_head + at, in1 = g * p.t[1].in_head + at;
+    Chunk x[IW];
+    bool has[IW];
 #pragma unroll
-    for (int u = 0; u < kEach; ++u) {
-        if (token[u] < 0) continue;   // the same for the lanes of a head
-        float v[V], rstd = 1.f;
+    for (int u = 0; u < IW; ++u) {
+        const bool second = first + u >= items0;
+        const int head = (first + u - (second ? items0 : 0)) * kHeads;
+        has[u] = first + u < items && in && head + g < (second ? p.t[1].heads : p.t[0].heads);
+        const D* const base = second ? (const D*)p.t[1].in + b * p.t[1].in_batch + t * p.t[1].in_token + head * p.t[1].in_head
+                                     : (const D*)p.t[0].in + b * p.t[0].in_batch + t * p.t[0].in_token + head * p.t[0].in_head;
+        x[u] = Chunk{};
+        if (has[u]) x[u] = load_chunk<D, V>(base + (second ? in1 : in0));
+    }
+    Chunk weight[kMaxRopeTensors];
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = in ? (float)x[u][i] : 0.f;
+    for (int k = 0; k < kMaxRopeTensors; ++k) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) weight[k][i] = (D)1.f;
+        if (p.t[k].weight && in) weight[k] = load_chunk<D, V>((const D*)p.t[k].weight + at);
+    }
+    float2* const cs = angles[wave];
+    for (int i = lane; i < p.pairs; i += 64) cs[i] = turn(p, b, t, i);
+    __builtin_amdgcn_wave_barrier();
+
+    // the lane's part of the angles, the other lane of its pairs, and its weights there
+    const int half = p.pairs / V;
+    const bool upper = c >= half;   // CHUNKS: of the second half
+    constexpr int kAngles = EX == PAIRS ? V / 2 : V;
+    float2 a[kAngles];
+    bool turned[kAngles];
+#pragma unroll
+    for (int i = 0; i < kAngles; ++i) {
+        const int e = EX == PAIRS ? at / 2 + i : at + i;   // of the pairs, of the elements
+        turned[i] = EX == PAIRS ? e < p.pairs : e < 2 * p.pairs;
+        a[i] = make_float2(1.f, 0.f);
+        if (turned[i]) a[i] = cs[EX == PAIRS || e < p.pairs ? e : e - p.pairs];
+        if (EX != PAIRS && e < p.pairs) a[i].y = -a[i].y;
+    }
+    const int other = 4 * ((lane & ~(L - 1)) + (upper ? c - half : c + half));
+    const auto exchanged = [&](Chunk v) {
+        if constexpr (EX == CHUNKS) {
+            Words w = __builtin_bit_cast(Words, v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t from = w[i];
+                w[i] = (uint32_t)__builtin_amdgcn_ds_bpermute(other, (int)from);
+            }
+            return __builtin_bit_cast(Chunk, w);
+        } else {
+            D* const row = rows[wave] + g * p.dim;
+            if (in) store_chunk<D, V>(row + at, v);
+            __builtin_amdgcn_wave_barrier();
+            Chunk o;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int e = at + i;
+                o[i] = row[in && e < 2 * p.pairs ? (e < p.pairs ? e + p.pairs : e - p.pairs) : 0];
+            }
+            __builtin_amdgcn_wave_barrier();
+            return o;
+        }
+    };
+    Chunk other_weight[kMaxRopeTensors];
+    if (EX != PAIRS && p.norm)
+#pragma unroll
+        for (int k = 0; k < kMaxRopeTensors; ++k) other_weight[k] = exchanged(weight[k]);
+
+    const int64_t out0 = g * p.t[0].out_head + at, out1 = g * p.t[1].out_head + at;
+#pragma unroll
+    for (int u = 0; u < IW; ++u) {
+        const bool second = first + u >= items0;
+        const int head = (first + u - (second ? items0 : 0)) * kHeads;
+        float v[V], o[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = (float)x[u][i];
+        if constexpr (EX != PAIRS) {
+            const Chunk other_x = exchanged(x[u]);
+#pragma unroll
+            for (int i = 0; i < V; ++i) o[i] = (float)other_x[i];
+        }
         if (p.norm) {
             float q = 0.f;
 #pragma unroll
             for (int i = 0; i < V; ++i) q = i >= skip ? fmaf(v[i], v[i], q) : q;
-            rstd = 1.f / sqrtf(lane_sum<L>(q) * p.inv_dim + p.eps);
-        }
-        const float* const w = weights + tensor[u] * p.dim;
-        const float2* const a = cs + token[u] * p.pairs;
-        float o[V];   // the other elements
-        const int half = p.pairs / V;
-        const bool second = c >= half;
-        if constexpr (EX == CHUNKS) {
-            Words raw = __builtin_bit_cast(Words, x[u]);
-            const int from = 4 * ((threadIdx.x & ~(L - 1) & 63) + (second ? c - half : c + half));
+            const float rstd = rsqrtf(lane_sum<L>(q) * p.inv_dim + p.eps);
+            const Chunk w = second ? weight[1] : weight[0];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) raw[i] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)raw[i]);
-            const Chunk other = __builtin_bit_cast(Chunk, raw);
+            for (int i = 0; i < V; ++i) v[i] *= rstd * (float)w[i];
+            if constexpr (EX != PAIRS) {
+                const Chunk ow = second ? other_weight[1] : other_weight[0];
 #pragma unroll
-            for (int i = 0; i < V; ++i) o[i] = (float)other[i];
-        }
-        if constexpr (EX == ELEMENTS) {
-            D* const row = rows + group * p.dim;
-            if (in) store_chunk<D, V>(row + at, x[u]);
-            __builtin_amdgcn_wave_barrier();
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int e = at + i;
-                o[i] = in && e < 2 * p.pairs ? (float)row[e < p.pairs ? e + p.pairs : e - p.pairs] : 0.f;
+                for (int i = 0; i < V; ++i) o[i] *= rstd * (float)ow[i];
             }
-            __builtin_amdgcn_wave_barrier();
         }
-        if (!in) continue;
-        if (p.norm)
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                v[i] = v[i] * rstd * w[at + i];
-                if constexpr (EX == CHUNKS)
-                    if (at < 2 * p.pairs) o[i] = o[i] * rstd * w[(second ? at - p.pairs : at + p.pairs) + i];
-                if constexpr (EX == ELEMENTS) {
-                    const int e = at + i;
-                    if (e < 2 * p.pairs) o[i] = o[i] * rstd * w[e < p.pairs ? e + p.pairs : e - p.pairs];
-                }
-            }
         Chunk y;
         if constexpr (EX == PAIRS) {
 #pragma unroll
             for (int i = 0; i < V; i += 2) {
-                float r0 = v[i], r1 = v[i + 1];
-                if (at + i < 2 * p.pairs) {
-                    const float2 t = a[(at + i) / 2];
-                    r0 = fmaf(v[i], t.x, -(v[i + 1] * t.y));
-                    r1 = fmaf(v[i], t.y, v[i + 1] * t.x);
-                }
-                y[i] = (D)r0;
-                y[i + 1] = (D)r1;
+                const float2 t = a[i / 2];
+                const float r0 = fmaf(v[i], t.x, -(v[i + 1] * t.y)), r1 = fmaf(v[i], t.y, v[i + 1] * t.x);
+                y[i] = (D)(turned[i / 2] ? r0 : v[i]);
+                y[i + 1] = (D)(turned[i / 2] ? r1 : v[i + 1]);
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int e = at + i;
-                float r = v[i];
-                if (EX == CHUNKS ? at < 2 * p.pairs : e < 2 * p.pairs) {
-                    const bool two = EX == CHUNKS ? second : e >= p.pairs;
-                    const float2 t = a[two ? e - p.pairs : e];
-                    r = fmaf(v[i], t.x, o[i] * (two ? t.y : -t.y));
-                }
-                y[i] = (D)r;
-            }
+            for (int i = 0; i < V; ++i) y[i] = (D)(turned[i] ? fmaf(v[i], a[i].x, o[i] * a[i].y) : v[i]);
         }
-        const Heads& h = p.t[tensor[u]];
-        store_chunk<D, V>((D*)h.out + b * h.out_batch + (t0 + token[u]) * h.out_token + head[u] * h.out_head + at, y);
+        D* const base = second ? (D*)p.t[1].out + b * p.t[1].out_batch + t * p.t[1].out_token + head * p.t[1].out_head
+                               : (D*)p.t[0].out + b * p.t[0].out_batch + t * p.t[0].out_token + head * p.t[0].out_head;
+        if (has[u]) store_chunk<D, V>(base + (second ? out1 : out0), y);
     }
 }
 
@@ -245,29 +249,28 @@ __global__ __launch_bounds__(kThreads) void rope_any_kernel(RopeParams p, int ha
     }
 }
 
-template <typename D, int L>
-void launch_lanes(RopeParams p, bool halves, int batch, hipStream_t s)
+template <typename D, int L, Exchange EX>
+void launch_items(const RopeParams& p, int batch, hipStream_t s)
 {
-    constexpr int V = 16 / sizeof(D), kHeads = kThreads / L * kRopeEach;   // heads a workgroup
-    const int heads = p.t[0].heads + (p.count > 1 ? p.t[1].heads : 0);
-    p.parts = (heads + kHeads - 1) / kHeads;
-    p.slots = (heads + p.parts - 1) / p.parts;
-    p.tile = p.parts > 1 ? 1 : kHeads / heads;
-    // fewer tokens a workgroup while there are units without one
-    while (p.tile > 1 && (int64_t)((p.tokens + p.tile - 1) / p.tile) * batch < 2 * kUnits) p.tile = (p.tile + 1) / 2;
-    p.per_slot = (65536 + p.slots - 1) / p.slots;
-    // a grid dimension holds fewer than 2^32 threads
-    const unsigned tiles = (p.tokens + p.tile - 1) / p.tile, gx = tiles < (1u << 20) ? tiles : 1u << 20;
-    const dim3 grid(gx, batch, (tiles + gx - 1) / gx * p.parts);
-    const bool chunks = halves && p.dim % V == 0 && p.pairs % V == 0;
-    const size_t lds = sizeof(float2) * p.tile * p.pairs + (p.norm ? sizeof(float) * p.count * p.dim : 0) +
-                       (halves && !chunks ? sizeof(D) * (kThreads / L) * p.dim : 0);
-    if (!halves)
-        hipLaunchKernelGGL((rope_kernel<D, L, PAIRS>), grid, dim3(kThreads), lds, s, p);
-    else if (chunks)
-        hipLaunchKernelGGL((rope_kernel<D, L, CHUNKS>), grid, dim3(kThreads), lds, s, p);
+    constexpr int kHeads = 64 / L, kWaves = kThreads / 64;
+    const int items = (p.t[0].heads + kHeads - 1) / kHeads + (p.count > 1 ? (p.t[1].heads + kHeads - 1) / kHeads : 0);
+    const int64_t all = (int64_t)p.tokens * batch * items;
+    const auto grid = [&](int each) { return dim3((p.tokens + kWaves - 1) / kWaves, batch, (items + each - 1) / each); };
+    if (all >= 64 * kUnits && items > 4)
+        hipLaunchKernelGGL((rope_kernel<D, L, EX, 8>), grid(8), dim3(kThreads), 0, s, p);
+    else if (all >= 16 * kUnits && items > 1)
+        hipLaunchKernelGGL((rope_kernel<D, L, EX, 4>), grid(4), dim3(kThreads), 0, s, p);
     else
-        hipLaunchKernelGGL((rope_kernel<D, L, ELEMENTS>), grid, dim3(kThreads), lds, s, p);
+        hipLaunchKernelGGL((rope_kernel<D, L, EX, 1>), grid(1), dim3(kThreads), 0, s, p);
+}
+
+template <typename D, int L>
+void launch_lanes(const RopeParams& p, bool halves, int batch, hipStream_t s)
+{
+    constexpr int V = 16 / sizeof(D);
+    if (!halves) launch_items<D, L, PAIRS>(p, batch, s);
+    else if (p.dim % V == 0 && p.pairs % V == 0) launch_items<D, L, CHUNKS>(p, batch, s);
+    else launch_items<D, L, ELEMENTS>(p, batch, s);
 }
 
 template <typename D>
