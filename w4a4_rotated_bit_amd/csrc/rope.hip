@@ -36,13 +36,16 @@ struct RopeParams {
     RopePlan plan;
 };
 
-// cos and sin of pair i at the position of (batch b, token t)
-__device__ __forceinline__ float2 turn(const RopeParams& p, int64_t b, int64_t t, int i)
+// Position of (batch b, token t) on the axis of pair i.
+__device__ __forceinline__ double place_of(const RopeParams& p, int64_t b, int64_t t, int i)
 {
     const int64_t at = b * p.pos_batch + t * p.pos_token + p.plan.axis[i];
-    const double place = p.pos_dtype == CONVROT_F32 ? (double)((const float*)p.pos)[at]
-                                                    : (double)((const int32_t*)p.pos)[at];
-    double turns = place * p.plan.turns[i];
+    return p.pos_dtype == CONVROT_F32 ? (double)((const float*)p.pos)[at] : (double)((const int32_t*)p.pos)[at];
+}
+
+// cos and sin of the angle of `turns` turns.
+__device__ __forceinline__ float2 turned_by(double turns)
+{
     turns -= rint(turns);
     float2 cs;
     sincospif(2.f * (float)turns, &cs.y, &cs.x);
@@ -79,6 +82,14 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p)
     const int items = items0 + (p.count > 1 ? (p.t[1].heads + kHeads - 1) / kHeads : 0);
     const int first = (int)blockIdx.z * IW;
 
+    // Loads return in order: the positions are asked for before the heads, so
+    // that the angles need not wait for those.
+    constexpr int kPairs = kMaxRopePairs / 64;
+    double turns[kPairs];
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j)
+        if (lane + 64 * j < p.pairs) turns[j] = p.plan.turns[lane + 64 * j] * place_of(p, b, t, lane + 64 * j);
+
     // lane offsets within an item; everything else about it is the same for the wave
     const int64_t in0 = g * p.t[0].in_head + at, in1 = g * p.t[1].in_head + at;
     Chunk x[IW];
@@ -93,15 +104,19 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p)
         x[u] = Chunk{};
         if (has[u]) x[u] = load_chunk<D, V>(base + (second ? in1 : in0));
     }
-    Chunk weight[kMaxRopeTensors];
+    constexpr int kKinds = IW == 1 ? 1 : kMaxRopeTensors;   // tensors a wave may meet
+    Chunk weight[kKinds];
 #pragma unroll
-    for (int k = 0; k < kMaxRopeTensors; ++k) {
+    for (int k = 0; k < kKinds; ++k) {
+        const D* const w = (const D*)(k == 1 || (IW == 1 && first >= items0) ? p.t[1].weight : p.t[0].weight);
 #pragma unroll
         for (int i = 0; i < V; ++i) weight[k][i] = (D)1.f;
-        if (p.t[k].weight && in) weight[k] = load_chunk<D, V>((const D*)p.t[k].weight + at);
+        if (w && in) weight[k] = load_chunk<D, V>(w + at);
     }
     float2* const cs = angles[wave];
-    for (int i = lane; i < p.pairs; i += 64) cs[i] = turn(p, b, t, i);
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j)
+        if (lane + 64 * j < p.pairs) cs[lane + 64 * j] = turned_by(turns[j]);
     __builtin_amdgcn_wave_barrier();
 
     // the lane's part of the angles, the other lane of its pairs, and its weights there
@@ -142,10 +157,10 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p)
             return o;
         }
     };
-    Chunk other_weight[kMaxRopeTensors];
+    Chunk other_weight[kKinds];
     if (EX != PAIRS && p.norm)
 #pragma unroll
-        for (int k = 0; k < kMaxRopeTensors; ++k) other_weight[k] = exchanged(weight[k]);
+        for (int k = 0; k < kKinds; ++k) other_weight[k] = exchanged(weight[k]);
 
     const int64_t out0 = g * p.t[0].out_head + at, out1 = g * p.t[1].out_head + at;
 #pragma unroll
@@ -165,11 +180,11 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p)
 #pragma unroll
             for (int i = 0; i < V; ++i) q = i >= skip ? fmaf(v[i], v[i], q) : q;
             const float rstd = rsqrtf(lane_sum<L>(q) * p.inv_dim + p.eps);
-            const Chunk w = second ? weight[1] : weight[0];
+            const Chunk w = second ? weight[kKinds - 1] : weight[0];
 #pragma unroll
             for (int i = 0; i < V; ++i) v[i] *= rstd * (float)w[i];
             if constexpr (EX != PAIRS) {
-                const Chunk ow = second ? other_weight[1] : other_weight[0];
+                const Chunk ow = second ? other_weight[kKinds - 1] : other_weight[0];
 #pragma unroll
                 for (int i = 0; i < V; ++i) o[i] *= rstd * (float)ow[i];
             }
@@ -205,7 +220,7 @@ __global__ __launch_bounds__(kThreads) void rope_any_kernel(RopeParams p, int ha
     const int t0 = (int)blockIdx.x * p.tile, nt = min(p.tile, p.tokens - t0);
     for (int i = threadIdx.x; i < nt * p.pairs; i += kThreads) {
         const int t = i / p.pairs;
-        cs[i] = turn(p, b, t0 + t, i - t * p.pairs);
+        cs[i] = turned_by(place_of(p, b, t0 + t, i - t * p.pairs) * p.plan.turns[i - t * p.pairs]);
     }
     __syncthreads();
     const int lane = threadIdx.x % 64;
