@@ -5,8 +5,6 @@ axes, and the product with group-scaled 4-bit weights.
 Tolerances are sums of what the arithmetic may lose.  u = 2^-24 is half a step
 of binary32 relative to the value; an output stored in type t adds half a step
 of t, finfo(t).eps / 2 of it (and half the smallest subnormal)."""
-import ctypes
-
 import numpy as np
 import pytest
 import torch
@@ -208,15 +206,18 @@ def test_norm_leaves_the_gaps_of_its_outputs(gpu):
     assert (buf[keep] == 5.0).all()
 
 
+def packed(layout, defaults, kw):
+    """The bytes of an argument struct: `defaults` in the order of its fields, some replaced."""
+    assert set(kw) <= set(defaults)
+    return layout.pack(*[v or 0 for v in {**defaults, **kw}.values()])
+
+
 def norm_args(**kw):
-    p = 1 << 30
-    a = B._NormArgs(x_dev=p, y_dev=p + (1 << 24), r_dev=p + (2 << 24), h_dev=p + (3 << 24), rows=4, width=64, x_stride=64,
-                    y_stride=64, r_stride=64, h_stride=64, rows_per_vec=1, residual_scale=1.0, eps=1e-6,
-                    dtype=B.CONVROT_BF16, vec_dtype=B.CONVROT_BF16, norm=B.CONVROT_NORM_LAYER,
-                    post_norm=B.CONVROT_NORM_NONE)
-    for k, v in kw.items():
-        setattr(a, k, v)
-    return a
+    return packed(B.NORM_ARGS, dict(
+        x_dev=P, y_dev=P + (1 << 24), gate_dev=0, scale_dev=0, shift_dev=0, weight_dev=0, post_weight_dev=0,
+        r_dev=P + (2 << 24), h_dev=P + (3 << 24), rows=4, width=64, x_stride=64, y_stride=64, r_stride=64, h_stride=64,
+        gate_stride=0, scale_stride=0, shift_stride=0, rows_per_vec=1, residual_scale=1.0, eps=1e-6,
+        dtype=B.CONVROT_BF16, vec_dtype=B.CONVROT_BF16, norm=B.CONVROT_NORM_LAYER, post_norm=B.CONVROT_NORM_NONE), kw)
 
 
 P = 1 << 30
@@ -241,10 +242,10 @@ P = 1 << 30
     ({"h_dev": P + (2 << 24) + 128}, False),
 ])
 def test_norm_refusals(kw, ok):
-    rc = B.load().convrot_validate_residual_norm(ctypes.byref(norm_args(**kw)))
+    rc = B.load().convrot_validate_residual_norm(norm_args(**kw))
     assert rc == (B.CONVROT_OK if ok else B.CONVROT_EINVAL)
     if not ok:
-        assert B.load().convrot_residual_norm(ctypes.byref(norm_args(**kw)), None) == B.CONVROT_EINVAL
+        assert B.load().convrot_residual_norm(norm_args(**kw), None) == B.CONVROT_EINVAL
 
 
 # ---- rotary positions ----------------------------------------------------------
@@ -376,28 +377,22 @@ def test_rope_frequencies():
             B.rope_frequencies(bad)
 
 
+FREQ, AXIS = np.ones(32), np.zeros(32, np.int32)
+
+
 def rope_args(q=None, k=None, **kw):
-    freq, axis = np.ones(32), np.zeros(32, np.int32)
-    a = B._RopeArgs(count=2, batch=2, tokens=3, head_dim=64, pos_dev=P, pos_batch_stride=9, pos_token_stride=3,
-                    pos_dtype=B.CONVROT_F32, axes=3, pairs=32, layout=1, norm=B.CONVROT_NORM_RMS, dtype=B.CONVROT_BF16,
-                    eps=1e-6)
+    FREQ[5], AXIS[5] = kw.pop("freq", 1.0), kw.pop("axis", 0)
+    fields = {}
     for i, extra in ((0, q), (1, k)):
-        h = a.heads[i]
-        h.in_dev, h.out_dev, h.weight_dev, h.heads = P + (4 * i + 1 << 20), P + (4 * i + 2 << 20), P, 4
-        h.in_batch_stride = h.out_batch_stride = 768
-        h.in_token_stride = h.out_token_stride = 256
-        h.in_head_stride = h.out_head_stride = 64
-        for key, v in (extra or {}).items():
-            setattr(h, key, v)
-    if "freq" in kw:
-        freq[5] = kw.pop("freq")
-    if "axis" in kw:
-        axis[5] = kw.pop("axis")
-    a.freq_host, a.axis_host = freq.ctypes.data, axis.ctypes.data
-    for key, v in kw.items():
-        setattr(a, key, v)
-    a._hold = (freq, axis)
-    return a
+        heads = dict(in_dev=P + (4 * i + 1 << 20), out_dev=P + (4 * i + 2 << 20), weight_dev=P, heads=4,
+                     in_batch_stride=768, in_token_stride=256, in_head_stride=64, out_batch_stride=768,
+                     out_token_stride=256, out_head_stride=64)
+        assert set(extra or {}) <= set(heads)
+        fields |= {f"{key}{i}": v for key, v in {**heads, **(extra or {})}.items()}
+    return packed(B.ROPE_ARGS, {**fields, **dict(
+        count=2, batch=2, tokens=3, head_dim=64, pos_dev=P, pos_batch_stride=9, pos_token_stride=3,
+        pos_dtype=B.CONVROT_F32, axes=3, pairs=32, freq_host=FREQ.ctypes.data, axis_host=AXIS.ctypes.data, layout=1,
+        norm=B.CONVROT_NORM_RMS, dtype=B.CONVROT_BF16, eps=1e-6)}, kw)
 
 
 Q, QO, K_ = P + (1 << 20), P + (2 << 20), P + (5 << 20)
@@ -428,11 +423,11 @@ Q, QO, K_ = P + (1 << 20), P + (2 << 20), P + (5 << 20)
       "k": {"out_dev": QO + 510, "out_token_stride": 512, "out_batch_stride": 1536}}, False),
 ])
 def test_rope_refusals(kw, ok):
-    a = rope_args(**kw)
-    rc = B.load().convrot_validate_rope(ctypes.byref(a))
+    a = rope_args(**dict(kw))
+    rc = B.load().convrot_validate_rope(a)
     assert rc == (B.CONVROT_OK if ok else B.CONVROT_EINVAL)
     if not ok:
-        assert B.load().convrot_rope(ctypes.byref(a), None) == B.CONVROT_EINVAL
+        assert B.load().convrot_rope(a, None) == B.CONVROT_EINVAL
 
 
 # ---- group-scaled 4-bit weights --------------------------------------------------
@@ -586,14 +581,12 @@ def test_quantize_grouped_matches_its_definition(gpu, dtype, group, asymmetric):
     ({"zeros_dev": P + 1}, True), ({"y_dev": P + (9 << 20) + 1}, False), ({"y_dev": P + 256}, False),
 ])
 def test_grouped_refusals(kw, ok):
-    a = B._GroupedArgs(x_dev=P, codes_dev=P + (1 << 22), scales_dev=P + (1 << 23), y_dev=P + (9 << 20), M=4, N=48, K=256,
-                       group=64, dtype=B.CONVROT_BF16)
-    for key, v in kw.items():
-        setattr(a, key, v)
-    rc = B.load().convrot_validate_linear_grouped(ctypes.byref(a))
+    a = packed(B.GROUPED_ARGS, dict(x_dev=P, codes_dev=P + (1 << 22), scales_dev=P + (1 << 23), zeros_dev=0, bias_dev=0,
+                                    y_dev=P + (9 << 20), M=4, N=48, K=256, group=64, dtype=B.CONVROT_BF16), kw)
+    rc = B.load().convrot_validate_linear_grouped(a)
     assert rc == (B.CONVROT_OK if ok else B.CONVROT_EINVAL)
     if not ok:
-        assert B.load().convrot_linear_grouped(ctypes.byref(a), None) == B.CONVROT_EINVAL
+        assert B.load().convrot_linear_grouped(a, None) == B.CONVROT_EINVAL
 
 
 def test_quantize_grouped_refusals():

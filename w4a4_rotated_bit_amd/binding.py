@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import numpy as np
@@ -63,33 +64,6 @@ _I = ctypes.c_int
 _SZ = ctypes.c_size_t
 
 
-class _NormArgs(ctypes.Structure):      # convrot_residual_norm_args
-    _fields_ = ([(n, _P) for n in ("x_dev", "y_dev", "gate_dev", "scale_dev", "shift_dev", "weight_dev",
-                                   "post_weight_dev", "r_dev", "h_dev")] +
-                [(n, _I64) for n in ("rows", "width", "x_stride", "y_stride", "r_stride", "h_stride", "gate_stride",
-                                     "scale_stride", "shift_stride", "rows_per_vec")] +
-                [("residual_scale", ctypes.c_float), ("eps", ctypes.c_float)] +
-                [(n, _I) for n in ("dtype", "vec_dtype", "norm", "post_norm")])
-
-
-class _Heads(ctypes.Structure):         # convrot_heads
-    _fields_ = ([(n, _P) for n in ("in_dev", "out_dev", "weight_dev")] +
-                [(n, _I64) for n in ("heads", "in_batch_stride", "in_token_stride", "in_head_stride",
-                                     "out_batch_stride", "out_token_stride", "out_head_stride")])
-
-
-class _RopeArgs(ctypes.Structure):      # convrot_rope_args
-    _fields_ = [("heads", _Heads * 2), ("count", _I), ("batch", _I64), ("tokens", _I64), ("head_dim", _I),
-                ("pos_dev", _P), ("pos_batch_stride", _I64), ("pos_token_stride", _I64), ("pos_dtype", _I),
-                ("axes", _I), ("pairs", _I), ("freq_host", _P), ("axis_host", _P), ("layout", _I), ("norm", _I),
-                ("dtype", _I), ("eps", ctypes.c_float)]
-
-
-class _GroupedArgs(ctypes.Structure):   # convrot_grouped_args
-    _fields_ = ([(n, _P) for n in ("x_dev", "codes_dev", "scales_dev", "zeros_dev", "bias_dev", "y_dev")] +
-                [("M", _I64), ("N", _I64), ("K", _I64), ("group", _I), ("dtype", _I)])
-
-
 _SIGNATURES = {
     "convrot_status_string": ([_I], ctypes.c_char_p),
     "convrot_version": ([], ctypes.c_char_p),
@@ -117,12 +91,12 @@ _SIGNATURES = {
                                 ctypes.POINTER(_SZ)], _I),
     "convrot_matrix_core_probe_bytes": ([ctypes.POINTER(_SZ)], _I),
     "convrot_matrix_core_probe": ([_I, _I, _P, _SZ, ctypes.POINTER(_I64), _P], _I),
-    "convrot_residual_norm": ([ctypes.POINTER(_NormArgs), _P], _I),
-    "convrot_validate_residual_norm": ([ctypes.POINTER(_NormArgs)], _I),
-    "convrot_rope": ([ctypes.POINTER(_RopeArgs), _P], _I),
-    "convrot_validate_rope": ([ctypes.POINTER(_RopeArgs)], _I),
-    "convrot_linear_grouped": ([ctypes.POINTER(_GroupedArgs), _P], _I),
-    "convrot_validate_linear_grouped": ([ctypes.POINTER(_GroupedArgs)], _I),
+    "convrot_residual_norm": ([_P, _P], _I),
+    "convrot_validate_residual_norm": ([_P], _I),
+    "convrot_rope": ([_P, _P], _I),
+    "convrot_validate_rope": ([_P], _I),
+    "convrot_linear_grouped": ([_P, _P], _I),
+    "convrot_validate_linear_grouped": ([_P], _I),
     "convrot_quantize_weight_grouped": ([_P, _I64, _I64, _I, _I, _P, _P, _P, _P], _I),
     "convrot_host_pack_nk": ([_P, _I64, _I64, _P], _I),
     "convrot_host_unpack_nk": ([_P, _I64, _I64, _P], _I),
@@ -160,7 +134,7 @@ def load():
 
 
 def _call(name, *args):
-    rc = getattr(load(), name)(*args)
+    rc = getattr(_lib or load(), name)(*args)
     if rc != CONVROT_OK:
         raise ConvRotError(rc, name)
 
@@ -553,20 +527,24 @@ CONVROT_NORM_RMS = 2
 CONVROT_ROPE_INTERLEAVED = 1
 CONVROT_ROPE_HALVES = 2
 
+# The argument structs of the C calls, in their order (native alignment).
+NORM_ARGS = struct.Struct("@9P10q2f4i")
+ROPE_ARGS = struct.Struct("@" + 2 * "3P7q" + "i2qi" + "P2q3i2P3if0P")
+GROUPED_ARGS = struct.Struct("@6P3q2i")
+
 _NORMS = {None: CONVROT_NORM_NONE, "layer": CONVROT_NORM_LAYER, "rms": CONVROT_NORM_RMS}
 _LAYOUTS = {"interleaved": CONVROT_ROPE_INTERLEAVED, "halves": CONVROT_ROPE_HALVES}
-_types = None   # torch dtype -> storage type, filled on first use
+_GROUPS = (32, 64, 128)
+_torch = None   # the module and its types' codes, from the first call on
+_types = {}
 
 
-def _type_of(t, name, allowed=None):
-    global _types
-    if _types is None:
-        import torch
-        _types = {torch.bfloat16: CONVROT_BF16, torch.float16: CONVROT_F16, torch.float32: CONVROT_F32}
-    code = _types.get(t.dtype)
-    if code is None or (allowed is not None and code not in allowed):
-        raise TypeError(f"{name} has an unsupported type {t.dtype}")
-    return code
+def _use_torch():
+    global _torch
+    import torch
+    _types.update({torch.bfloat16: CONVROT_BF16, torch.float16: CONVROT_F16, torch.float32: CONVROT_F32})
+    _torch = torch
+    return torch
 
 
 def _choice(table, key, what):
@@ -576,64 +554,76 @@ def _choice(table, key, what):
         raise ValueError(f"unknown {what} {key!r}") from None
 
 
-def _check_tensor(t, name, device):
-    """A tensor of this call: on its device, and one that asks for no gradient here."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.requires_grad and torch.is_grad_enabled():
-        raise RuntimeError(f"{name} requires a gradient, and this operator has none: call it under torch.no_grad()")
-
-
 def _on_gpu(t, name):
-    import torch
-    if not isinstance(t, torch.Tensor):
+    """The index of the device of a call's first tensor."""
+    if not isinstance(t, (_torch or _use_torch()).Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    return t.device
+    return t.get_device()
 
 
-class _Launch:
-    """The device and stream of a call: work and the outputs it allocates go to
-    ``stream`` (or the device's current stream), whatever device is current."""
-
-    def __init__(self, device, stream):
-        import torch
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
-        other = device.index != torch.cuda.current_device()
-        self._scope = torch.cuda.stream(stream) if stream is not None else torch.cuda.device(device) if other else None
-        self._raw = (stream or torch.cuda.current_stream(device)).cuda_stream
-
-    def __enter__(self):
-        if self._scope is not None:
-            self._scope.__enter__()
-        return self._raw
-
-    def __exit__(self, *exc):
-        if self._scope is not None:
-            self._scope.__exit__(*exc)
+def _check_tensor(t, name, device):
+    """A tensor of this call: on its device, and one that asks for no gradient here."""
+    if not isinstance(t, _torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda or t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
+    if t.requires_grad and _torch.is_grad_enabled():
+        raise RuntimeError(f"{name} requires a gradient, and this operator has none: call it under torch.no_grad()")
 
 
-def _rows(t, name, width=None):
+def _type_of(t, name):
+    code = _types.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} has an unsupported type {t.dtype}")
+    return code
+
+
+def _raw_stream(device):
+    """The handle of the device's current stream (torch.cuda.current_stream
+    builds an object around it, which takes longer than a launch)."""
+    get = getattr(_torch._C, "_cuda_getCurrentRawStream", None)
+    return get(device) if get is not None else _torch.cuda.current_stream(device).cuda_stream
+
+
+def _launch(device, stream, call):
+    """call(raw stream) with the device current, and with ``stream`` (or the
+    device's current stream) the one that its allocations belong to."""
+    cuda = _torch.cuda
+    if stream is None:
+        if cuda.current_device() == device:
+            return call(_raw_stream(device))
+        with cuda.device(device):
+            return call(_raw_stream(device))
+    if stream.device.index != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on cuda:{device}")
+    with cuda.stream(stream):
+        return call(stream.cuda_stream)
+
+
+def _rows(t, name, width):
     """(rows, row stride) of a tensor seen as rows of its dense last dimension."""
-    if t.dim() == 0 or (width is not None and t.shape[-1] != width):
-        raise ValueError(f"{name} must have rows of {width} values, got shape {tuple(t.shape)}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    shape = t.shape
+    if not shape or shape[-1] != width:
+        raise ValueError(f"{name} must have rows of {width} values, got shape {tuple(shape)}")
+    strides = t.stride()
+    if width > 1 and strides[-1] != 1:
         raise ValueError(f"{name} must be dense in its last dimension")
+    if len(shape) == 2:
+        return shape[0], strides[0]
+    if t.is_contiguous():
+        return (t.numel() // width, width) if width else (0, 0)
     if t.numel() == 0:
         return 0, 0
     rows, stride = 1, 0
-    for n, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+    for n, s in zip(reversed(shape[:-1]), reversed(strides[:-1])):
         if n == 1:
             continue
         if rows == 1:
             stride = s
         elif s != rows * stride:
-            raise ValueError(f"the rows of {name} are not evenly spaced: strides {t.stride()}")
+            raise ValueError(f"the rows of {name} are not evenly spaced: strides {strides}")
         rows *= n
     return rows, stride
 
@@ -650,68 +640,72 @@ def convrot_residual_norm(x, y=None, *, gate=None, scale=None, shift=None, weigh
     vector for every rows / V rows.  weight, post_weight: [width], of the
     vectors' type.  Returns (r, h) of x's shape; r or h given is written (x or
     y itself may be), and one not wanted is None."""
-    import torch
     device = _on_gpu(x, "x")
-    width = x.shape[-1] if x.dim() else 0
-    a = _NormArgs()
-    a.dtype = _type_of(x, "x")
-    a.norm, a.post_norm = _choice(_NORMS, norm, "norm"), _choice(_NORMS, post_norm, "norm")
-    a.residual_scale, a.eps, a.width = residual_scale, eps, width
-    rows, a.x_stride = _rows(x, "x", width)
-    a.rows, a.x_dev = rows, x.data_ptr()
     _check_tensor(x, "x", device)
+    shape, dtype = x.shape, x.dtype
+    width = shape[-1] if shape else 0
+    code = _type_of(x, "x")
+    norms = _choice(_NORMS, norm, "norm"), _choice(_NORMS, post_norm, "norm")
+    rows, x_stride = _rows(x, "x", width)
+    y_ptr = y_stride = 0
     if y is not None:
         _check_tensor(y, "y", device)
-        if y.shape != x.shape or y.dtype != x.dtype:
+        if y.shape != shape or y.dtype != dtype:
             raise ValueError(f"y must have the shape and type of x, got {tuple(y.shape)} {y.dtype}")
-        a.y_stride, a.y_dev = _rows(y, "y", width)[1], y.data_ptr()
-    per, a.vec_dtype = 0, 0
+        y_ptr, y_stride = y.data_ptr(), _rows(y, "y", width)[1]
+    vec_code, per = 0, 0
+    pointers, strides = [], []
     for name, v in (("gate", gate), ("scale", scale), ("shift", shift), ("weight", weight),
                     ("post_weight", post_weight)):
         if v is None:
+            pointers.append(0)
+            strides.append(0)
             continue
-        _check_tensor(v, name, device)
-        code = _type_of(v, name, (a.dtype, CONVROT_F32))
-        if a.vec_dtype and code != a.vec_dtype:
-            raise TypeError("the vectors and weights must have one type")
-        a.vec_dtype = code
+        if not isinstance(v, _torch.Tensor) or v.get_device() != device or v.requires_grad:
+            _check_tensor(v, name, device)
+        v_code = _types.get(v.dtype) or _type_of(v, name)
+        if v_code not in (code, CONVROT_F32) or vec_code not in (0, v_code):
+            raise TypeError("the vectors and weights must have one type, that of x or float32")
+        vec_code = v_code
         n, step = _rows(v, name, width)
-        setattr(a, name + "_dev", v.data_ptr())
-        if name in ("weight", "post_weight"):
-            if n != 1:
+        if n != 1:
+            lead = v.shape[:-1]
+            while lead and lead[-1] == 1:
+                lead = lead[:-1]
+            if "weight" in name:
                 raise ValueError(f"{name} must be one vector of {width} values")
-            continue
-        lead = list(v.shape[:-1])
-        while lead and lead[-1] == 1:
-            lead.pop()
-        if n == 1:
+            if rows % n if len(shape) == 2 and len(lead) == 1 and n else lead != shape[:len(lead)]:
+                raise ValueError(f"{name} of shape {tuple(v.shape)} does not fit x of shape {tuple(shape)}")
+            if rows:
+                if per not in (0, rows // n):
+                    raise ValueError("gate, scale and shift must have one vector, or as many as one another")
+                per = rows // n
+        else:
             step = 0
-        elif (rows % n if x.dim() == 2 and len(lead) == 1 and n else tuple(lead) != tuple(x.shape[:len(lead)])):
-            raise ValueError(f"{name} of shape {tuple(v.shape)} does not fit x of shape {tuple(x.shape)}")
-        elif rows:
-            if per and per != rows // n:
-                raise ValueError("gate, scale and shift must have one vector, or as many as one another")
-            per = rows // n
-        setattr(a, name + "_stride", step)
-    a.vec_dtype = a.vec_dtype or a.dtype
-    a.rows_per_vec = max(per, 1)
-    with _Launch(device, stream) as raw:
-        outs = []
-        for name, out, wanted in (("r", r, want_r), ("h", h, want_h)):
-            if out is None and not wanted:
-                outs.append(None)
-                continue
-            if out is None:
-                out = torch.empty(x.shape, dtype=x.dtype, device=device)
-            else:
-                _check_tensor(out, name, device)
-                if out.shape != x.shape or out.dtype != x.dtype:
-                    raise ValueError(f"{name} must have the shape and type of x")
-            setattr(a, name + "_stride", _rows(out, name, width)[1])
-            setattr(a, name + "_dev", out.data_ptr())
-            outs.append(out)
-        _call("convrot_residual_norm", ctypes.byref(a), raw)
-    return outs[0], outs[1]
+        pointers.append(v.data_ptr())
+        strides.append(step)
+
+    def output(out, name, wanted):
+        """The output given, or a new one: it, its address and row stride."""
+        if out is None:
+            if not wanted:
+                return None, 0, 0
+            out = x.new_empty(shape)
+            return out, out.data_ptr(), width
+        _check_tensor(out, name, device)
+        if out.shape != shape or out.dtype != dtype:
+            raise ValueError(f"{name} must have the shape and type of x")
+        return out, out.data_ptr(), _rows(out, name, width)[1]
+
+    def call(raw):
+        r_out, r_ptr, r_stride = output(r, "r", want_r)
+        h_out, h_ptr, h_stride = output(h, "h", want_h)
+        _call("convrot_residual_norm", NORM_ARGS.pack(
+            x.data_ptr(), y_ptr, *pointers, r_ptr, h_ptr, rows, width, x_stride, y_stride, r_stride, h_stride,
+            *strides[:3], per or 1, residual_scale, eps, code, vec_code or code, *norms), raw)
+        return r_out, h_out
+
+    return _launch(device, stream, call)
 
 
 def rope_frequencies(sizes, theta: float = 10000.0, shared: bool = False):
@@ -731,23 +725,25 @@ def rope_frequencies(sizes, theta: float = 10000.0, shared: bool = False):
     return freq, axis
 
 
-def _heads(slot, t, out, weight, name, a, device):
-    """Fill one convrot_heads; t and out are [batch, tokens, heads, head_dim]."""
-    if t.dim() != 4 or tuple(t.shape[:2]) != (a.batch, a.tokens) or t.shape[3] != a.head_dim:
-        raise ValueError(f"{name} must be [batch, tokens, heads, head_dim], got {tuple(t.shape)}")
-    if out.shape != t.shape or out.dtype != t.dtype:
+def _heads(t, out, weight, name, shape, device):
+    """The fields of one convrot_heads; t and out are [batch, tokens, heads, head_dim]."""
+    own = t.shape
+    if len(own) != 4 or own[0] != shape[0] or own[1] != shape[1] or own[3] != shape[3]:
+        raise ValueError(f"{name} must be [batch, tokens, heads, head_dim], got {tuple(own)}")
+    if out.shape != own or out.dtype != t.dtype:
         raise ValueError(f"{name}_out must have the shape and type of {name}")
-    for v in (t, out):
-        if v.shape[3] > 1 and v.stride(3) != 1:
-            raise ValueError(f"{name} and its output must be dense in their last dimension")
-    slot.in_dev, slot.out_dev, slot.heads = t.data_ptr(), out.data_ptr(), t.shape[2]
-    slot.in_batch_stride, slot.in_token_stride, slot.in_head_stride = t.stride()[:3]
-    slot.out_batch_stride, slot.out_token_stride, slot.out_head_stride = out.stride()[:3]
+    tb, tt, th, td = t.stride()
+    ob, ot, oh, od = out.stride()
+    if shape[3] > 1 and (td != 1 or od != 1):
+        raise ValueError(f"{name} and its output must be dense in their last dimension")
+    w = 0
     if weight is not None:
-        _check_tensor(weight, f"{name}_weight", device)
-        if weight.dtype != t.dtype or tuple(weight.shape) != (a.head_dim,) or not weight.is_contiguous():
+        if not isinstance(weight, _torch.Tensor) or weight.get_device() != device or weight.requires_grad:
+            _check_tensor(weight, f"{name}_weight", device)
+        if weight.dtype != t.dtype or weight.shape != own[3:] or not weight.is_contiguous():
             raise ValueError(f"{name}_weight must be one dense vector of head_dim values of {name}'s type")
-        slot.weight_dev = weight.data_ptr()
+        w = weight.data_ptr()
+    return t.data_ptr(), out.data_ptr(), w, own[2], tb, tt, th, ob, ot, oh
 
 
 def convrot_rope(q, k, positions, freq, axis, *, layout: str = "interleaved", qk_norm: bool = False, q_weight=None,
@@ -761,76 +757,84 @@ def convrot_rope(q, k, positions, freq, axis, *, layout: str = "interleaved", qk
     head by its root mean square first, times q_weight / k_weight [head_dim].
     Returns (q_out, k_out); given ones are written and may be q, k themselves or
     transposed views ([batch, heads, tokens, head_dim] storage)."""
-    import torch
     device = _on_gpu(q, "q")
     _check_tensor(q, "q", device)
-    if q.dim() != 4:
-        raise ValueError(f"q must be [batch, tokens, heads, head_dim], got {tuple(q.shape)}")
-    a = _RopeArgs()
-    a.dtype, a.layout, a.eps = _type_of(q, "q"), _choice(_LAYOUTS, layout, "layout"), eps
-    a.batch, a.tokens, a.head_dim = q.shape[0], q.shape[1], q.shape[3]
-    a.norm = CONVROT_NORM_RMS if qk_norm else CONVROT_NORM_NONE
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 4:
+        raise ValueError(f"q must be [batch, tokens, heads, head_dim], got {tuple(shape)}")
+    code, order = _type_of(q, "q"), _choice(_LAYOUTS, layout, "layout")
     freq, axis = np.ascontiguousarray(freq, np.float64), np.ascontiguousarray(axis, np.int32)
     if freq.ndim != 1 or freq.shape != axis.shape:
         raise ValueError("freq and axis must hold one value for every pair")
-    a.pairs, a.freq_host, a.axis_host = freq.shape[0], freq.ctypes.data, axis.ctypes.data
-    _check_tensor(positions, "positions", device)
-    if positions.dtype == torch.int32:
-        a.pos_dtype = CONVROT_I32
-    elif positions.dtype == torch.float32:
-        a.pos_dtype = CONVROT_F32
+    if not isinstance(positions, _torch.Tensor) or positions.get_device() != device or positions.requires_grad:
+        _check_tensor(positions, "positions", device)
+    if positions.dtype == _torch.int32:
+        pos_code = CONVROT_I32
+    elif positions.dtype == _torch.float32:
+        pos_code = CONVROT_F32
     else:
         raise TypeError(f"positions must be int32 or float32, got {positions.dtype}")
-    if positions.dim() != 3 or positions.shape[0] not in (1, a.batch) or positions.shape[1] != a.tokens:
-        raise ValueError(f"positions must be [batch or 1, tokens, axes], got {tuple(positions.shape)}")
-    if positions.shape[2] > 1 and positions.stride(2) != 1:
+    pos_shape = positions.shape
+    if len(pos_shape) != 3 or pos_shape[0] not in (1, shape[0]) or pos_shape[1] != shape[1]:
+        raise ValueError(f"positions must be [batch or 1, tokens, axes], got {tuple(pos_shape)}")
+    pos_strides = positions.stride()
+    if pos_shape[2] > 1 and pos_strides[2] != 1:
         raise ValueError("positions must be dense in their last dimension")
-    a.axes, a.pos_dev = positions.shape[2], positions.data_ptr()
-    a.pos_batch_stride = positions.stride(0) if positions.shape[0] > 1 else 0
-    a.pos_token_stride = positions.stride(1)
-    a.count = 1
     if k is not None:
         _check_tensor(k, "k", device)
-        if k.dtype != q.dtype:
+        if k.dtype != dtype:
             raise TypeError("k must have the type of q")
-        a.count = 2
     elif k_weight is not None or k_out is not None:
         raise ValueError("k_weight and k_out need k")
-    with _Launch(device, stream) as raw:
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=device)
-        else:
-            _check_tensor(q_out, "q_out", device)
-        _heads(a.heads[0], q, q_out, q_weight, "q", a, device)
-        if k is not None:
-            if k_out is None:
-                k_out = torch.empty(k.shape, dtype=k.dtype, device=device)
+
+    def call(raw):
+        outs, fields = [], []
+        for name, t, out, weight in (("q", q, q_out, q_weight), ("k", k, k_out, k_weight)):
+            if t is None:
+                outs.append(None)
+                fields.append((0,) * 10)
+                continue
+            if out is None:
+                out = t.new_empty(t.shape)
             else:
-                _check_tensor(k_out, "k_out", device)
-            _heads(a.heads[1], k, k_out, k_weight, "k", a, device)
-        _call("convrot_rope", ctypes.byref(a), raw)
-    return q_out, k_out
+                _check_tensor(out, name + "_out", device)
+            outs.append(out)
+            fields.append(_heads(t, out, weight, name, shape, device))
+        _call("convrot_rope", ROPE_ARGS.pack(
+            *fields[0], *fields[1], 1 if k is None else 2, shape[0], shape[1], shape[3], positions.data_ptr(),
+            pos_strides[0] if pos_shape[0] > 1 else 0, pos_strides[1], pos_code, pos_shape[2], freq.shape[0],
+            freq.__array_interface__["data"][0], axis.__array_interface__["data"][0], order, CONVROT_NORM_RMS if qk_norm else CONVROT_NORM_NONE, code, eps), raw)
+        return outs[0], outs[1]
+
+    return _launch(device, stream, call)
+
+
+def _check_group(group, K):
+    if group not in _GROUPS or K % group:
+        raise ValueError(f"group must be 32, 64 or 128 and divide K = {K}, got {group}")
 
 
 def convrot_quantize_weight_grouped(W, group: int, asymmetric: bool = False, stream=None):
     """W: bf16 or f16 [N, K] -> (codes uint8 [N, K/2], scales [N, K/group] of W's
     type, zeros uint8 [N, K/group], or None unless ``asymmetric``)."""
-    import torch
     device = _on_gpu(W, "W")
-    _check_tensor(W.detach(), "W", device)
     if W.dim() != 2 or not W.is_contiguous():
         raise ValueError("W must be a dense [N, K] tensor")
-    code = _type_of(W, "W", (CONVROT_BF16, CONVROT_F16))
+    code = _type_of(W, "W")
+    if code == CONVROT_F32:
+        raise TypeError("W must be bfloat16 or float16")
     N, K = W.shape
-    if group not in (32, 64, 128) or K % group:
-        raise ValueError(f"group must be 32, 64 or 128 and divide K = {K}, got {group}")
-    with _Launch(device, stream) as raw:
-        codes = torch.empty((N, K // 2), dtype=torch.uint8, device=device)
-        scales = torch.empty((N, K // group), dtype=W.dtype, device=device)
-        zeros = torch.empty((N, K // group), dtype=torch.uint8, device=device) if asymmetric else None
+    _check_group(group, K)
+
+    def call(raw):
+        codes = _torch.empty((N, K // 2), dtype=_torch.uint8, device=W.device)
+        scales = _torch.empty((N, K // group), dtype=W.dtype, device=W.device)
+        zeros = _torch.empty((N, K // group), dtype=_torch.uint8, device=W.device) if asymmetric else None
         _call("convrot_quantize_weight_grouped", W.data_ptr(), N, K, group, code, codes.data_ptr(),
               scales.data_ptr(), None if zeros is None else zeros.data_ptr(), raw)
-    return codes, scales, zeros
+        return codes, scales, zeros
+
+    return _launch(device, stream, call)
 
 
 def convrot_linear_grouped(X, codes, scales, zeros, bias, group: int, Y=None, stream=None):
@@ -838,33 +842,37 @@ def convrot_linear_grouped(X, codes, scales, zeros, bias, group: int, Y=None, st
     channels.  X: bf16 or f16 [M, K], M <= 32; codes: uint8 [N, K/2] (N x
     packed-K); scales: [N, K/group] of X's type; zeros: uint8 [N, K/group] with
     unsigned codes, None with two's complement ones; bias: [N] or None."""
-    import torch
     device = _on_gpu(X, "X")
-    a = _GroupedArgs()
-    a.dtype, a.group = _type_of(X, "X", (CONVROT_BF16, CONVROT_F16)), group
-    if X.dim() != 2 or codes.dim() != 2:
+    dtype = X.dtype
+    code = _type_of(X, "X")
+    if code == CONVROT_F32:
+        raise TypeError("X must be bfloat16 or float16")
+    if X.dim() != 2 or not isinstance(codes, _torch.Tensor) or codes.dim() != 2:
         raise ValueError("X and codes must be matrices")
     M, K = X.shape
     N = codes.shape[0]
-    if group not in (32, 64, 128) or K % group:
-        raise ValueError(f"group must be 32, 64 or 128 and divide K = {K}, got {group}")
-    a.M, a.N, a.K = M, N, K
-    for name, t, dtype, shape in (("X", X, X.dtype, (M, K)), ("codes", codes, torch.uint8, (N, K // 2)),
-                                  ("scales", scales, X.dtype, (N, K // group)),
-                                  ("zeros", zeros, torch.uint8, (N, K // group)), ("bias", bias, X.dtype, (N,)),
-                                  ("Y", Y, X.dtype, (M, N))):
-        if t is None and name in ("zeros", "bias", "Y"):
-            continue
-        _check_tensor(t, name, device)
-        if t.dtype != dtype or tuple(t.shape) != shape:
-            raise ValueError(f"{name} must be {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+    _check_group(group, K)
+    byte, groups = _torch.uint8, K // group
+
+    def place(t, name, kind, *shape):
+        if not isinstance(t, _torch.Tensor) or t.get_device() != device or t.requires_grad:
+            _check_tensor(t, name, device)
+        if t.dtype != kind or t.shape != shape:
+            raise ValueError(f"{name} must be {kind} {shape}, got {t.dtype} {tuple(t.shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-        if name != "Y":
-            setattr(a, name.lower() + "_dev", t.data_ptr())
-    with _Launch(device, stream) as raw:
-        if Y is None:
-            Y = torch.empty((M, N), dtype=X.dtype, device=device)
-        a.y_dev = Y.data_ptr()
-        _call("convrot_linear_grouped", ctypes.byref(a), raw)
-    return Y
+        return t.data_ptr()
+
+    x_ptr, codes_ptr = place(X, "X", dtype, M, K), place(codes, "codes", byte, N, K // 2)
+    scales_ptr = place(scales, "scales", dtype, N, groups)
+    zeros_ptr = 0 if zeros is None else place(zeros, "zeros", byte, N, groups)
+    bias_ptr = 0 if bias is None else place(bias, "bias", dtype, N)
+
+    def call(raw):
+        y = X.new_empty((M, N)) if Y is None else Y
+        y_ptr = y.data_ptr() if Y is None else place(Y, "Y", dtype, M, N)
+        _call("convrot_linear_grouped",
+              GROUPED_ARGS.pack(x_ptr, codes_ptr, scales_ptr, zeros_ptr, bias_ptr, y_ptr, M, N, K, group, code), raw)
+        return y
+
+    return _launch(device, stream, call)
