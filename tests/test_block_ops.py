@@ -744,3 +744,67 @@ def test_the_calls_follow_their_formulas_in_a_row(gpu):
     for got, t in ((q, h), (k, r)):
         want, e = rope_reference(t.view(2, 40, 4, 64), pos, freq, axis, "interleaved", None, False, 1e-6)
         close(got, want, e + half_step(torch.bfloat16, want.abs() + e), "rope")
+
+
+# ---- modules --------------------------------------------------------------------
+
+
+def test_conditioned_block_on_cpu():
+    """The plain form of the block, which needs no GPU, and its positions."""
+    from w4a4_rotated_bit_amd.flux_block import ConditionedBlock, picture, tokens
+    blk = ConditionedBlock(128, head_dim=64).to(torch.bfloat16)
+    pos = picture(30, 2)
+    assert pos.shape == (2, 30, 3) and (pos[:, :10] == 0).all() and pos[0, 10:].unique(dim=0).shape[0] == 20
+    assert len(blk.freq) == 32 and blk.axis.max() == 2
+    x = tokens(60, 128).view(2, 30, 128)
+    y = blk.plain(x, tokens(2, 128), pos)
+    assert y.shape == x.shape and y.dtype == torch.bfloat16 and torch.isfinite(y.float()).all()
+
+
+def test_grouped_linear_refusals():
+    from w4a4_rotated_bit_amd.module import GroupedLinear
+    codes, scales = torch.zeros((8, 64), dtype=torch.uint8), torch.zeros((8, 2), dtype=torch.bfloat16)
+    lin = GroupedLinear(128, 8, codes, scales, None, None, 64)
+    assert "group_size=64" in repr(lin)
+    with pytest.raises(ValueError):
+        GroupedLinear(128, 8, codes, scales, None, None, 128)
+    with pytest.raises(ValueError):
+        GroupedLinear(128, 8, codes, scales, scales[:4], None, 64)
+    with pytest.raises(ValueError):
+        GroupedLinear(100, 8, codes, scales, None, None, 64)
+    with pytest.raises(ValueError):
+        lin(torch.zeros(1, 64))
+    with pytest.raises(ValueError):
+        lin(torch.zeros(33, 128))
+    with pytest.raises(ValueError):
+        GroupedLinear.from_linear(torch.nn.Linear(128, 8), 64)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("asymmetric", [False, True])
+def test_grouped_linear_is_its_quantized_weight(gpu, asymmetric):
+    from w4a4_rotated_bit_amd.module import GroupedLinear
+    dense = torch.nn.Linear(256, 96).cuda().to(torch.float16)
+    lin = GroupedLinear.from_linear(dense, 64, asymmetric)
+    x = rand((2, 3, 256), 1, torch.float16).cuda()
+    y = lin(x)
+    assert y.shape == (2, 3, 96) and y.dtype == torch.float16
+    want = B.convrot_linear_grouped(x.view(6, 256), lin.codes, lin.scales, lin.zeros, lin.bias, 64)
+    assert torch.equal(y.view(6, 96), want)
+    # half a step of a weight is at most scale / 2, and the scale's own rounding moves it by 2^-11 of 7 (15) scales
+    step = lin.scales.float().max().item() * (0.5 + 15 * 2.0 ** -11)
+    off = (y.double().cpu() - dense(x).double().cpu()).abs().max()
+    assert off <= step * x.double().abs().sum(-1).max().item() + 2.0 ** -10 * y.double().abs().max().item() * 2
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("batch,T,hidden", [(1, 48, 256), (3, 33, 384)])
+def test_conditioned_block_runs(gpu, batch, T, hidden):
+    from w4a4_rotated_bit_amd.flux_block import run_conditioned
+    out = run_conditioned(T, hidden, batch, group_size=64, iters=0)
+    assert out["finite"]
+    # with dense linears the operators and the plain form round at the same six
+    # places (both h, q and k, the attended values' inputs, both sums); each may
+    # fall to the other side, a step of 2^-8 of the value
+    assert out["rel_err_operators"] <= 6 * 2.0 ** -8
+    assert out["rel_err_operators"] < out["rel_err_block"]

@@ -1,4 +1,5 @@
-"""ConvRotLinear: a torch module around the library's W4A4 (or W4A16) linear.
+"""ConvRotLinear: a torch module around the library's W4A4 (or W4A16) linear,
+and GroupedLinear: one around its group-scaled 4-bit linear for a few rows.
 
 The weight is rotated, quantized and packed once, on construction from an
 ``nn.Linear`` (the offline step; convrot-mlx README, "What is included": the
@@ -62,6 +63,57 @@ class ConvRotLinear(torch.nn.Module):
     def extra_repr(self) -> str:
         return (f"in_features={self.in_features}, out_features={self.out_features}, bias={self.bias is not None}, "
                 f"group_size={self.group_size}, rotation={self.rotation}, path={self.path}")
+
+
+class GroupedLinear(torch.nn.Module):
+    """y = x W^T + b for at most 32 rows, W in 4 bits with a scale (and zero
+    point) for every ``group_size`` input channels: the modulation linear of a
+    conditioned block, or a decoder's linear at a few tokens.
+
+    codes: uint8 [out_features, in_features / 2], the low nibble the even
+    channel, unsigned with zeros and two's complement without; scales: bf16 or
+    f16 [out_features, in_features / group_size]; zeros: uint8 of that shape."""
+
+    def __init__(self, in_features: int, out_features: int, codes: torch.Tensor, scales: torch.Tensor,
+                 zeros: torch.Tensor | None, bias: torch.Tensor | None, group_size: int = 128):
+        super().__init__()
+        if group_size not in (32, 64, 128) or in_features % group_size:
+            raise ValueError(f"group_size must be 32, 64 or 128 and divide {in_features}, got {group_size}")
+        shape = (out_features, in_features // group_size)
+        if tuple(codes.shape) != (out_features, in_features // 2) or tuple(scales.shape) != shape:
+            raise ValueError("codes and scales do not fit the features and the group size")
+        if zeros is not None and tuple(zeros.shape) != shape:
+            raise ValueError("zeros must have the shape of scales")
+        self.in_features, self.out_features, self.group_size = in_features, out_features, group_size
+        self.register_buffer("codes", codes)
+        self.register_buffer("scales", scales)
+        self.register_buffer("zeros", zeros)
+        self.register_buffer("bias", bias)
+
+    @classmethod
+    @torch.no_grad()
+    def from_linear(cls, linear: torch.nn.Linear, group_size: int = 128, asymmetric: bool = False) -> "GroupedLinear":
+        if not linear.weight.is_cuda:
+            raise ValueError("the linear must be on the GPU")
+        w = linear.weight.detach()
+        w = (w if w.dtype == torch.float16 else w.to(torch.bfloat16)).contiguous()
+        codes, scales, zeros = binding.convrot_quantize_weight_grouped(w, group_size, asymmetric)
+        b = None if linear.bias is None else linear.bias.detach().to(w.dtype).contiguous()
+        return cls(linear.in_features, linear.out_features, codes, scales, zeros, b, group_size)
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        if x.shape[-1] != self.in_features:
+            raise ValueError(f"last dimension {x.shape[-1]} != in_features {self.in_features}")
+        lead = x.shape[:-1]
+        x2 = x.reshape(-1, self.in_features).to(self.scales.dtype).contiguous()
+        if x2.shape[0] > 32:
+            raise ValueError(f"{x2.shape[0]} rows: a GroupedLinear takes at most 32")
+        y = binding.convrot_linear_grouped(x2, self.codes, self.scales, self.zeros, self.bias, self.group_size)
+        return y.reshape(*lead, self.out_features)
+
+    def extra_repr(self) -> str:
+        return (f"in_features={self.in_features}, out_features={self.out_features}, bias={self.bias is not None}, "
+                f"group_size={self.group_size}, asymmetric={self.zeros is not None}")
 
 
 def eligible(linear: torch.nn.Linear, group_size: int = 256) -> bool:
