@@ -240,6 +240,10 @@ P = 1 << 30
     ({"r_dev": P + 64}, False), ({"r_dev": P + 128, "x_stride": 128, "r_stride": 128}, True),
     ({"r_dev": P + 126, "x_stride": 128, "r_stride": 128}, False), ({"r_dev": P + 4 * 128}, True),
     ({"h_dev": P + (2 << 24) + 128}, False),
+    # vectors under an output: the second of two vectors, a weight
+    ({"gate_dev": P + (2 << 24) - 128, "gate_stride": 64, "rows_per_vec": 4}, True),
+    ({"gate_dev": P + (2 << 24) - 128, "gate_stride": 64, "rows_per_vec": 2}, False),
+    ({"weight_dev": P + (3 << 24) + 256}, False), ({"weight_dev": P + (3 << 24) + 512}, True),
 ])
 def test_norm_refusals(kw, ok):
     rc = B.load().convrot_validate_residual_norm(norm_args(**kw))
@@ -414,6 +418,7 @@ Q, QO, K_ = P + (1 << 20), P + (2 << 20), P + (5 << 20)
     ({"q": {"out_dev": Q}}, True), ({"q": {"out_dev": Q, "out_head_stride": 192, "out_token_stride": 64}}, False),
     ({"q": {"out_dev": Q + 128}}, False), ({"q": {"out_dev": K_}}, False),
     ({"q": {"out_dev": QO}, "k": {"out_dev": QO}}, False),
+    ({"pos_dev": QO + 1024}, False), ({"pos_dev": QO + 3072}, True), ({"k": {"weight_dev": QO + 3070}}, False),
     # heads first: [batch][heads][tokens][head_dim]
     ({"q": {"out_token_stride": 64, "out_head_stride": 192}}, True),
     # both outputs side by side in one packed buffer
@@ -578,7 +583,8 @@ def test_quantize_grouped_matches_its_definition(gpu, dtype, group, asymmetric):
     ({"group": 16}, False), ({"group": 256}, False), ({"group": 128}, True), ({"dtype": 3}, False), ({"dtype": 2}, True),
     ({"x_dev": None}, False), ({"codes_dev": None}, False), ({"scales_dev": None}, False), ({"y_dev": None}, False),
     ({"x_dev": P + 8}, False), ({"codes_dev": P + 8}, False), ({"scales_dev": P + 1}, False), ({"bias_dev": P + 1}, False),
-    ({"zeros_dev": P + 1}, True), ({"y_dev": P + (9 << 20) + 1}, False), ({"y_dev": P + 256}, False),
+    ({"zeros_dev": P + 1 - (1 << 20)}, True), ({"zeros_dev": P + (9 << 20)}, False), ({"bias_dev": P + (9 << 20) + 382}, False),
+    ({"bias_dev": P + (9 << 20) + 384}, True), ({"codes_dev": P + (9 << 20) - 16 * 383}, False), ({"y_dev": P + (9 << 20) + 1}, False), ({"y_dev": P + 256}, False),
 ])
 def test_grouped_refusals(kw, ok):
     a = packed(B.GROUPED_ARGS, dict(x_dev=P, codes_dev=P + (1 << 22), scales_dev=P + (1 << 23), zeros_dev=0, bias_dev=0,

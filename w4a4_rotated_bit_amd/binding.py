@@ -633,13 +633,13 @@ def convrot_residual_norm(x, y=None, *, gate=None, scale=None, shift=None, weigh
                           h=None, want_r: bool = True, want_h: bool = True, stream=None):
     """r = residual_scale x + gate * P(y);  h = N(r) * weight * (1 + scale) + shift.
 
-    x, y: bf16, f16 or f32 [..., width].  norm, post_norm: "layer", "rms" or
-    None.  gate, scale, shift: of the same type or f32, [width] for all rows, or
-    [..., width] with the leading dimensions of x, or the first of them (one
-    vector a batch entry; ones may follow); for a matrix x also [V, width], one
-    vector for every rows / V rows.  weight, post_weight: [width], of the
-    vectors' type.  Returns (r, h) of x's shape; r or h given is written (x or
-    y itself may be), and one not wanted is None."""
+    x, y: bf16, f16 or f32 [..., width], rows evenly spaced and dense.  norm,
+    post_norm: "layer", "rms" or None.  gate, scale, shift: of the same type or
+    f32, [width] for all rows, or [..., width] with the leading dimensions of x,
+    or the first of them (one vector a batch entry; ones may follow); for a
+    matrix x also [V, width], one vector for every rows / V rows.  weight,
+    post_weight: [width], of the vectors' type.  Returns (r, h) of x's shape; r
+    or h given is written (x or y itself may be), and one not wanted is None."""
     device = _on_gpu(x, "x")
     _check_tensor(x, "x", device)
     shape, dtype = x.shape, x.dtype
@@ -690,7 +690,7 @@ def convrot_residual_norm(x, y=None, *, gate=None, scale=None, shift=None, weigh
         if out is None:
             if not wanted:
                 return None, 0, 0
-            out = x.new_empty(shape)
+            out = _torch.empty_like(x, memory_format=_torch.contiguous_format)
             return out, out.data_ptr(), width
         _check_tensor(out, name, device)
         if out.shape != shape or out.dtype != dtype:
@@ -795,7 +795,7 @@ def convrot_rope(q, k, positions, freq, axis, *, layout: str = "interleaved", qk
                 fields.append((0,) * 10)
                 continue
             if out is None:
-                out = t.new_empty(t.shape)
+                out = _torch.empty_like(t, memory_format=_torch.contiguous_format)
             else:
                 _check_tensor(out, name + "_out", device)
             outs.append(out)

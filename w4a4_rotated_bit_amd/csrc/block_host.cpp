@@ -115,6 +115,18 @@ int convrot_validate_residual_norm(const convrot_residual_norm_args* args)
         if (y.at && !out.same(y) && !apart(y, out)) return CONVROT_EINVAL;
     }
     if (r.at && h.at && !apart(r, h)) return CONVROT_EINVAL;
+    const int64_t vectors = (a.rows + a.rows_per_vec - 1) / a.rows_per_vec;
+    const struct {
+        const void* at;
+        int64_t stride, count;
+    } vecs[] = {{a.gate_dev, a.gate_stride, vectors}, {a.scale_dev, a.scale_stride, vectors},
+                {a.shift_dev, a.shift_stride, vectors}, {a.weight_dev, 0, 1}, {a.post_weight_dev, 0, 1}};
+    for (const auto& g : vecs) {
+        if (!g.at) continue;
+        Block b(g.at, a.width, v);
+        b.add(g.count, g.stride, v);
+        if ((r.at && !apart(b, r)) || (h.at && !apart(b, h))) return CONVROT_EINVAL;
+    }
     return CONVROT_OK;
 }
 
@@ -154,13 +166,17 @@ int convrot_validate_rope(const convrot_rope_args* args)
         b.add(h.heads, out ? h.out_head_stride : h.in_head_stride, e);
         return b;
     };
+    Block places(a.pos_dev, a.axes, 4);
+    places.add(a.batch, a.pos_batch_stride, 4);
+    places.add(a.tokens, a.pos_token_stride, 4);
     for (int k = 0; k < a.count; ++k) {
         const Block out = block(a.heads[k], true);
-        if (!out.injective()) return CONVROT_EINVAL;
+        if (!out.injective() || !apart(places, out)) return CONVROT_EINVAL;
         for (int j = 0; j < a.count; ++j) {
             const Block in = block(a.heads[j], false);
             if (!(j == k && out.same(in)) && !apart(in, out)) return CONVROT_EINVAL;
             if (j < k && !apart(block(a.heads[j], true), out)) return CONVROT_EINVAL;
+            if (a.heads[j].weight_dev && !apart(Block(a.heads[j].weight_dev, a.head_dim, e), out)) return CONVROT_EINVAL;
         }
     }
     return CONVROT_OK;
@@ -178,8 +194,13 @@ int convrot_validate_linear_grouped(const convrot_grouped_args* args)
     if (!a.x_dev || !a.codes_dev || !a.scales_dev || !a.y_dev) return CONVROT_EINVAL;
     if (!aligned(a.x_dev, 16) || !aligned(a.codes_dev, 16)) return CONVROT_EINVAL;
     if (!aligned(a.scales_dev, 2) || !aligned(a.bias_dev, 2) || !aligned(a.y_dev, 2)) return CONVROT_EINVAL;
-    const Block x(a.x_dev, a.M * a.K, 2), y(a.y_dev, a.M * a.N, 2);
-    return apart(x, y) ? CONVROT_OK : CONVROT_EINVAL;
+    const Block y(a.y_dev, a.M * a.N, 2);
+    const int64_t groups = a.N * (a.K / a.group);
+    for (const Block& in : {Block(a.x_dev, a.M * a.K, 2), Block(a.codes_dev, a.N * (a.K / 2), 1), Block(a.scales_dev, groups, 2)})
+        if (!apart(in, y)) return CONVROT_EINVAL;
+    if (a.zeros_dev && !apart(Block(a.zeros_dev, groups, 1), y)) return CONVROT_EINVAL;
+    if (a.bias_dev && !apart(Block(a.bias_dev, a.N, 2), y)) return CONVROT_EINVAL;
+    return CONVROT_OK;
 }
 
 }  // extern "C"
