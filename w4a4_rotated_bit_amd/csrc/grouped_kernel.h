@@ -116,13 +116,14 @@ __device__ __forceinline__ uint32_t fetch(int from, uint32_t v)
 // codes lane / 4 is the row and lane % 4 the 16-byte piece, of x lane / 16 and
 // lane % 16 -- and a wave passes them on through its own part of shared memory.
 // Scales and zero points come for four blocks at a time, lane % 4 the block.
-// Codes are loaded four blocks ahead, x PX.
+// Codes are loaded two blocks ahead, x two or one: more
+// of them in flight costs registers and gains nothing.
 //
 // Row m of x sits at row 4 (m % 4) + m / 4 of its matrix tile, so that the
 // first E of the four sums a lane holds are the ones in use for M <= 4 E.
 //
 // OCC: the waves of a SIMD that the registers have to leave room for.
-template <typename D, int GROUP, bool ZEROS, int MT, int E, int NT, int W, int PX, int OCC>
+template <typename D, int GROUP, bool ZEROS, int MT, int E, int NT, int W, int OCC>
 __global__ __launch_bounds__(W * 64, OCC) void grouped_kernel(GroupedParams p)
 {
     typedef typename Mat<D>::Frag Frag;
@@ -131,6 +132,7 @@ __global__ __launch_bounds__(W * 64, OCC) void grouped_kernel(GroupedParams p)
     constexpr int kWords = (kPer + 1) / 2;           // words of a block's scales
     constexpr bool kTurn = GROUP != 128;             // step j holds k = 32 j + 8 q, without it k = 32 q + 8 j
     constexpr int kXLoads = E * MT;                  // four rows of x a load
+    constexpr int PW = 2, PX = E == 1 ? 2 : 1;       // blocks loaded ahead, of the codes and of x
     constexpr bool kInOrder = kXLoads > 2 * NT;      // which of x and the codes is cheaper to reorder
     typedef typename UintOf<kPer * 2>::type Scales __attribute__((aligned(2)));
     typedef typename UintOf<kPer>::type Zeros __attribute__((aligned(1)));
@@ -212,7 +214,7 @@ __global__ __launch_bounds__(W * 64, OCC) void grouped_kernel(GroupedParams p)
         }
 #pragma unroll
         for (int i = 0; i < kXLoads; ++i) x_at[i] = (uint32_t)min(4 * i + lane / 16, p.M - 1) * (uint32_t)(2 * p.K) + 16 * (lane % 16);
-        u32x4 w[4][NT], x[PX][kXLoads];
+        u32x4 w[PW][NT], x[PX][kXLoads];
         uint32_t s[NT][kWords], z[NT];
         const auto load_w = [&](u32x4 (&to)[NT], int b) {
             const uint8_t* const base = codes + b * 64;
@@ -273,7 +275,7 @@ __global__ __launch_bounds__(W * 64, OCC) void grouped_kernel(GroupedParams p)
         // block before its codes.
         load_s(s, z, first);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < PW; ++j) {
             if (j < PX) load_x(x[j], min(first + j, end - 1));
             load_w(w[j], min(first + j, end - 1));
         }
@@ -289,8 +291,8 @@ __global__ __launch_bounds__(W * 64, OCC) void grouped_kernel(GroupedParams p)
                 take_x(xo, x[j % PX]);
                 load_x(x[j % PX], min(b + j + PX, end - 1));
                 take_s(so, zo, j);
-                take_w(wo, w[j]);
-                load_w(w[j], min(b + j + 4, end - 1));
+                take_w(wo, w[j % PW]);
+                load_w(w[j % PW], min(b + j + PW, end - 1));
                 __builtin_amdgcn_sched_barrier(0);
                 multiply(wo, xo, so, zo);
                 __builtin_amdgcn_sched_barrier(0);
@@ -311,7 +313,8 @@ __global__ __launch_bounds__(W * 64, OCC) void grouped_kernel(GroupedParams p)
                 take_x(xo, x[j % PX]);
                 if (j + PX < 4) load_x(x[j % PX], min(b + j + PX, end - 1));
                 take_s(so, zo, j);
-                take_w(wo, w[j]);
+                take_w(wo, w[j % PW]);
+                if (j + PW < 4) load_w(w[j % PW], min(b + j + PW, end - 1));
                 __builtin_amdgcn_sched_barrier(0);
                 multiply(wo, xo, so, zo);
                 __builtin_amdgcn_sched_barrier(0);
@@ -366,10 +369,10 @@ __global__ __launch_bounds__(W * 64, OCC) void grouped_kernel(GroupedParams p)
     }
 }
 
-template <typename D, int GROUP, bool ZEROS, int MT, int E, int NT, int W, int PX, int OCC>
+template <typename D, int GROUP, bool ZEROS, int MT, int E, int NT, int W, int OCC>
 void launch_one(GroupedParams p, hipStream_t s)
 {
-    hipLaunchKernelGGL((grouped_kernel<D, GROUP, ZEROS, MT, E, NT, W, PX, OCC>), dim3((p.N + p.rows - 1) / p.rows),
+    hipLaunchKernelGGL((grouped_kernel<D, GROUP, ZEROS, MT, E, NT, W, OCC>), dim3((p.N + p.rows - 1) / p.rows),
                        dim3(W * 64), 0, s, p);
 }
 
@@ -386,8 +389,8 @@ void launch_zeros(GroupedParams p, hipStream_t s)
 {
     if (p.M <= 4) {
         p.rows = p.N <= 2048 && p.K >= 8192 ? 8 : 16;
-        if (p.N > 8192) launch_one<D, GROUP, ZEROS, 1, 1, 1, 4, 4, 4>(p, s);
-        else launch_one<D, GROUP, ZEROS, 1, 1, 1, 8, 4, 4>(p, s);
+        if (p.N > 8192) launch_one<D, GROUP, ZEROS, 1, 1, 1, 4, 4>(p, s);
+        else launch_one<D, GROUP, ZEROS, 1, 1, 1, 8, 4>(p, s);
         return;
     }
     const int rounds = (p.N + 64 * kUnits - 1) / (64 * kUnits);
@@ -395,20 +398,20 @@ void launch_zeros(GroupedParams p, hipStream_t s)
     if (p.rows < 16) p.rows = 16;
     const int tiles = (p.rows + 15) / 16;
     if (p.M <= 8) {
-        if (tiles == 1) launch_one<D, GROUP, ZEROS, 1, 2, 1, 8, 2, 2>(p, s);
-        else if (tiles == 2) launch_one<D, GROUP, ZEROS, 1, 2, 2, 8, 4, 2>(p, s);
-        else if (tiles == 3) launch_one<D, GROUP, ZEROS, 1, 2, 3, 8, 4, 2>(p, s);
-        else launch_one<D, GROUP, ZEROS, 1, 2, 4, 8, 2, 2>(p, s);
+        if (tiles == 1) launch_one<D, GROUP, ZEROS, 1, 2, 1, 8, 4>(p, s);
+        else if (tiles == 2) launch_one<D, GROUP, ZEROS, 1, 2, 2, 8, 2>(p, s);
+        else if (tiles == 3) launch_one<D, GROUP, ZEROS, 1, 2, 3, 8, 2>(p, s);
+        else launch_one<D, GROUP, ZEROS, 1, 2, 4, 8, 2>(p, s);
     } else if (p.M <= 16) {
-        if (tiles == 1) launch_one<D, GROUP, ZEROS, 1, 4, 1, 8, 1, 2>(p, s);
-        else if (tiles == 2) launch_one<D, GROUP, ZEROS, 1, 4, 2, 8, 2, 2>(p, s);
-        else if (tiles == 3) launch_one<D, GROUP, ZEROS, 1, 4, 3, 8, 2, 2>(p, s);
-        else launch_one<D, GROUP, ZEROS, 1, 4, 4, 8, 2, 2>(p, s);
+        if (tiles == 1) launch_one<D, GROUP, ZEROS, 1, 4, 1, 8, 2>(p, s);
+        else if (tiles == 2) launch_one<D, GROUP, ZEROS, 1, 4, 2, 8, 2>(p, s);
+        else if (tiles == 3) launch_one<D, GROUP, ZEROS, 1, 4, 3, 8, 2>(p, s);
+        else launch_one<D, GROUP, ZEROS, 1, 4, 4, 8, 2>(p, s);
     } else {
-        if (tiles == 1) launch_one<D, GROUP, ZEROS, 2, 4, 1, 8, 1, 2>(p, s);
-        else if (tiles == 2) launch_one<D, GROUP, ZEROS, 2, 4, 2, 8, 1, 2>(p, s);
-        else if (tiles == 3) launch_one<D, GROUP, ZEROS, 2, 4, 3, 4, 1, 1>(p, s);
-        else launch_one<D, GROUP, ZEROS, 2, 4, 4, 4, 2, 1>(p, s);
+        if (tiles == 1) launch_one<D, GROUP, ZEROS, 2, 4, 1, 8, 2>(p, s);
+        else if (tiles == 2) launch_one<D, GROUP, ZEROS, 2, 4, 2, 8, 2>(p, s);
+        else if (tiles == 3) launch_one<D, GROUP, ZEROS, 2, 4, 3, GROUP == 32 ? 4 : 8, GROUP == 32 ? 1 : 2>(p, s);
+        else launch_one<D, GROUP, ZEROS, 2, 4, 4, 4, 1>(p, s);   // fewer waves where eight would not fit the registers
     }
 }
 
