@@ -105,6 +105,7 @@ __device__ __forceinline__ uint32_t fetch(int from, uint32_t v)
 {
     return (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v);
 }
+
 // A workgroup of W waves makes p.rows outputs, at most 16 NT, for up to 16 MT
 // rows of x.  Its waves share the 128-K blocks, a run of consecutive ones each,
 // and add their parts in a fixed order at the end.
@@ -113,11 +114,13 @@ __device__ __forceinline__ uint32_t fetch(int from, uint32_t v)
 // channels of quarter q.  Loads that way would touch a line of memory for every
 // lane (and a load costs the lines it touches: 157 against 85 us for 32 x 16384
 // -> 16384), so neighbouring lanes load neighbouring pieces of a row -- of the
-// codes lane / 4 is the row and lane % 4 the 16-byte piece, of x lane / 16 and
-// lane % 16 -- and a wave passes them on through its own part of shared memory.
-// Scales and zero points come for four blocks at a time, lane % 4 the block.
-// Codes are loaded two blocks ahead, x two or one: more
-// of them in flight costs registers and gains nothing.
+// codes lane / 8 is the row and lane % 8 the 16-byte piece of two blocks, a
+// whole line, of x lane / 16 and lane % 16 -- and a wave passes them on through
+// its own part of shared memory.  Scales and zero points come for four blocks at
+// a time, lane % 4 the block.  Two blocks of codes are on their way while two
+// are multiplied, of x two blocks or one: more in flight costs registers and
+// time (four blocks of codes: 49.0 against 44.2 us, 16 x 4096 -> 16384 12.9
+// against 12.0).
 //
 // Row m of x sits at row 4 (m % 4) + m / 4 of its matrix tile, so that the
 // first E of the four sums a lane holds are the ones in use for M <= 4 E.
@@ -132,13 +135,13 @@ __global__ __launch_bounds__(W * 64, OCC) void grouped_kernel(GroupedParams p)
     constexpr int kWords = (kPer + 1) / 2;           // words of a block's scales
     constexpr bool kTurn = GROUP != 128;             // step j holds k = 32 j + 8 q, without it k = 32 q + 8 j
     constexpr int kXLoads = E * MT;                  // four rows of x a load
-    constexpr int PW = 2, PX = E == 1 ? 2 : 1;       // blocks loaded ahead, of the codes and of x
+    constexpr int PX = E == 1 ? 2 : 1;               // blocks of x loaded ahead
     constexpr bool kInOrder = kXLoads > 2 * NT;      // which of x and the codes is cheaper to reorder
     typedef typename UintOf<kPer * 2>::type Scales __attribute__((aligned(2)));
     typedef typename UintOf<kPer>::type Zeros __attribute__((aligned(1)));
 
     union Shared {
-        u32x4 part[W][(kXLoads + NT) * 64];   // a wave's block of x and of codes, 16-byte pieces
+        u32x4 part[W][(kXLoads + 2 * NT) * 64];   // a wave's block of x and two of codes, 16-byte pieces
         float parts[W][MT * NT * E][64];
     };
     __shared__ Shared shared;
@@ -147,7 +150,9 @@ __global__ __launch_bounds__(W * 64, OCC) void grouped_kernel(GroupedParams p)
     const int n0 = (int)blockIdx.x * p.rows, n_end = min(n0 + p.rows, p.N);
     const int m_own = 4 * (r % 4 % E) + r / 4;   // row of x at row r of a matrix tile
 
-    const int blocks = p.K / 128, run = (blocks + W - 1) / W, first = wave * run, end = min(first + run, blocks);
+    // a run of an even number of blocks, so that it begins with a line, unless that leaves waves without any
+    const int blocks = p.K / 128, least = (blocks + W - 1) / W, run = least < 4 ? least : (least + 1) / 2 * 2;
+    const int first = wave * run, end = min(first + run, blocks);
     f32x4 acc[MT][NT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
@@ -197,34 +202,45 @@ __global__ __launch_bounds__(W * 64, OCC) void grouped_kernel(GroupedParams p)
                     for (int e = 0; e < E; ++e)
                         acc[mt][nt][e] = fmaf(scale, ZEROS ? fmaf(zero, sum[mt][i][e], part[mt][e]) : part[mt][e], acc[mt][nt][e]);
             }
+            // The sums are made here and not where the loop ends, which would keep every part until then.
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) asm volatile("" : "+v"(acc[mt][nt]));
         }
     };
 
     if (first < end) {
-        // offsets of a lane from a base that is the same for the whole wave
-        const uint8_t* const codes = p.codes + (int64_t)n0 * (p.K / 2);
+        // Rows behind the last one read as zeros; their outputs are computed and not stored.
+        const auto codes = __builtin_amdgcn_make_buffer_rsrc((void*)(p.codes + (int64_t)n0 * (p.K / 2)), 0,
+                                                             (n_end - n0) * (p.K / 2), 0x20000);
+        const auto rows = __builtin_amdgcn_make_buffer_rsrc((void*)p.x, 0, 2 * p.M * p.K, 0x20000);
         const uint16_t* const scales = (const uint16_t*)p.scales + (int64_t)n0 * p.groups;
         const uint8_t* const zeros = p.zeros + (int64_t)n0 * p.groups;
-        uint32_t w_at[NT], s_at[NT], x_at[kXLoads];
+        const int half = lane % 8 / 4;   // which of the two blocks
+        const uint32_t w_at = (uint32_t)(lane / 8) * (uint32_t)(p.K / 2) + 16 * (lane % 4);
+        const uint32_t x_at = (uint32_t)(lane / 16) * (uint32_t)(2 * p.K) + 16 * (lane % 16);
+        uint32_t s_at[NT];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const uint32_t n = min(16 * nt + lane / 4, n_end - 1 - n0);   // outputs past the end are computed and not stored
-            w_at[nt] = n * (uint32_t)(p.K / 2) + 16 * (lane % 4);
-            s_at[nt] = n * (uint32_t)p.groups;
-        }
-#pragma unroll
-        for (int i = 0; i < kXLoads; ++i) x_at[i] = (uint32_t)min(4 * i + lane / 16, p.M - 1) * (uint32_t)(2 * p.K) + 16 * (lane % 16);
-        u32x4 w[PW][NT], x[PX][kXLoads];
+        for (int nt = 0; nt < NT; ++nt) s_at[nt] = (uint32_t)min(16 * nt + lane / 4, n_end - 1 - n0) * (uint32_t)p.groups;
+        u32x4 w[2 * NT], x[PX][kXLoads];
         uint32_t s[NT][kWords], z[NT];
-        const auto load_w = [&](u32x4 (&to)[NT], int b) {
-            const uint8_t* const base = codes + b * 64;
+        // With 32 rows an offset is worked out for each load: kept, those of all
+        // of them take registers that are not there.
+        const auto load_w = [&](int b) {   // blocks b and b + 1
+            const uint32_t at = w_at + (uint32_t)min(b + half, end - 1) * 64u;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) to[nt] = *(const u32x4*)(base + w_at[nt]);
+            for (int i = 0; i < 2 * NT; ++i) {
+                uint32_t row = (uint32_t)(8 * i) * (uint32_t)(p.K / 2);
+                if constexpr (MT > 1) asm volatile("" : "+s"(row));
+                w[i] = __builtin_amdgcn_raw_buffer_load_b128(codes, at + row, 0, 0);
+            }
         };
         const auto load_x = [&](u32x4 (&to)[kXLoads], int b) {
-            const uint8_t* const base = (const uint8_t*)p.x + b * 256;
 #pragma unroll
-            for (int i = 0; i < kXLoads; ++i) to[i] = *(const u32x4*)(base + x_at[i]);
+            for (int i = 0; i < kXLoads; ++i) {
+                uint32_t row = (uint32_t)(4 * i) * (uint32_t)(2 * p.K) + (uint32_t)b * 256u;
+                if constexpr (MT > 1) asm volatile("" : "+s"(row));
+                to[i] = __builtin_amdgcn_raw_buffer_load_b128(rows, x_at + row, 0, 0);
+            }
         };
         const auto load_s = [&](uint32_t (&to)[NT][kWords], uint32_t (&to_z)[NT], int b) {
             const uint32_t at = (uint32_t)min(b + lane % 4, blocks - 1) * kPer;
@@ -237,9 +253,10 @@ __global__ __launch_bounds__(W * 64, OCC) void grouped_kernel(GroupedParams p)
             }
         };
         // The wave's own part of shared memory, whose accesses happen in order.
-        // Piece c of row m of x lies at 16 m + (c ^ m), piece c of row r of the
-        // codes at 4 r + (c ^ r / 4): the 16 lanes that read one piece of 16
-        // rows meet 16 different places.
+        // Piece c of row m of x lies at 16 m + (c ^ m), piece c of row r of a
+        // block's codes at 4 r + (c ^ r / 4), in the second block with the rows
+        // swapped in pairs: the 16 lanes that read one piece of 16 rows, and the
+        // 8 that write a line, meet different places.
         u32x4* const part_x = shared.part[wave];
         u32x4* const part_w = part_x + kXLoads * 64;
         const auto take_x = [&](u32x4 (&to)[MT][4], const u32x4 (&from)[kXLoads]) {
@@ -255,12 +272,17 @@ __global__ __launch_bounds__(W * 64, OCC) void grouped_kernel(GroupedParams p)
                 for (int i = 0; i < 4; ++i) to[mt][i] = part_x[16 * (16 * mt + m_own) + ((kTurn ? 4 * i + q : 4 * q + i) ^ m_own)];
             __builtin_amdgcn_wave_barrier();
         };
-        const auto take_w = [&](u32x4 (&to)[NT], const u32x4 (&from)[NT]) {
+        const auto put_w = [&]() {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) part_w[64 * nt + (lane ^ lane / 16)] = from[nt];
+            for (int i = 0; i < 2 * NT; ++i) {
+                const int row = 8 * (i % 2) + lane / 8;
+                part_w[64 * NT * half + 64 * (i / 2) + 4 * (row ^ half) + (lane % 4 ^ row / 4)] = w[i];
+            }
             __builtin_amdgcn_wave_barrier();
+        };
+        const auto take_w = [&](u32x4 (&to)[NT], int h) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) to[nt] = part_w[64 * nt + 4 * r + (q ^ r / 4)];
+            for (int nt = 0; nt < NT; ++nt) to[nt] = part_w[64 * NT * h + 64 * nt + 4 * (r ^ h) + (q ^ r / 4)];
             __builtin_amdgcn_wave_barrier();
         };
         const auto take_s = [&](uint32_t (&so)[NT][kWords], uint32_t (&zo)[NT], int j) {
@@ -274,11 +296,9 @@ __global__ __launch_bounds__(W * 64, OCC) void grouped_kernel(GroupedParams p)
         // Loads return in order, so what is used first is asked for first: x of a
         // block before its codes.
         load_s(s, z, first);
-#pragma unroll
-        for (int j = 0; j < PW; ++j) {
-            if (j < PX) load_x(x[j], min(first + j, end - 1));
-            load_w(w[j], min(first + j, end - 1));
-        }
+        load_x(x[0], first);
+        load_w(first);
+        if constexpr (PX > 1) load_x(x[1], min(first + 1, end - 1));
         u32x4 xo[MT][4];
         int b = first;
         for (; b + 4 < end; b += 4) {
@@ -291,11 +311,13 @@ __global__ __launch_bounds__(W * 64, OCC) void grouped_kernel(GroupedParams p)
                 take_x(xo, x[j % PX]);
                 load_x(x[j % PX], min(b + j + PX, end - 1));
                 take_s(so, zo, j);
-                take_w(wo, w[j % PW]);
-                load_w(w[j % PW], min(b + j + PW, end - 1));
+                if (j % 2 == 0) {
+                    put_w();
+                    load_w(b + j + 2);
+                }
+                take_w(wo, j % 2);
                 __builtin_amdgcn_sched_barrier(0);
                 multiply(wo, xo, so, zo);
-                __builtin_amdgcn_sched_barrier(0);
                 __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
@@ -313,8 +335,9 @@ __global__ __launch_bounds__(W * 64, OCC) void grouped_kernel(GroupedParams p)
                 take_x(xo, x[j % PX]);
                 if (j + PX < 4) load_x(x[j % PX], min(b + j + PX, end - 1));
                 take_s(so, zo, j);
-                take_w(wo, w[j % PW]);
-                if (j + PW < 4) load_w(w[j % PW], min(b + j + PW, end - 1));
+                if (j % 2 == 0) put_w();
+                if (j == 0) load_w(b + 2);
+                take_w(wo, j % 2);
                 __builtin_amdgcn_sched_barrier(0);
                 multiply(wo, xo, so, zo);
                 __builtin_amdgcn_sched_barrier(0);
@@ -410,8 +433,8 @@ void launch_zeros(GroupedParams p, hipStream_t s)
     } else {
         if (tiles == 1) launch_one<D, GROUP, ZEROS, 2, 4, 1, 8, 2>(p, s);
         else if (tiles == 2) launch_one<D, GROUP, ZEROS, 2, 4, 2, 8, 2>(p, s);
-        else if (tiles == 3) launch_one<D, GROUP, ZEROS, 2, 4, 3, GROUP == 32 ? 4 : 8, GROUP == 32 ? 1 : 2>(p, s);
-        else launch_one<D, GROUP, ZEROS, 2, 4, 4, 4, 1>(p, s);   // fewer waves where eight would not fit the registers
+        else if (tiles == 3) launch_one<D, GROUP, ZEROS, 2, 4, 3, 8, 2>(p, s);
+        else launch_one<D, GROUP, ZEROS, 2, 4, 4, GROUP == 32 ? 4 : 8, GROUP == 32 ? 1 : 2>(p, s);   // eight waves do not have the registers
     }
 }
 
