@@ -12,6 +12,15 @@
 // instruction widens two at a time, times 512.
 //
 // The codes are read as they are interchanged, N x packed-K.
+//
+// Few rows are bound by memory: 1 x 4096 -> 12288 reads 26 MB in 8.0 us (3.3
+// TB/s, a kernel that only reads them 5.9 us), 1 x 1024 -> 1024 takes 2.4 us where
+// an empty kernel takes 1.9.  With more rows every compute unit reads all of x
+// and widens its share of the codes, some 60 vector instructions for each 16 x
+// 128 of them beside 8 or 16 matrix instructions: 32 x 16384 -> 16384 takes 45.5
+// us (143 MB, 3.1 TB/s), 34 with its codes in the cache and 26 for reading alone,
+// and 16 x 4128 -> 9001 with groups of 32 takes 13.9 us, 12.5 without its products
+// and 11.2 with rows of 4096, which begin with a line of memory.
 #pragma once
 #include "block_ops.h"
 
@@ -119,8 +128,8 @@ __device__ __forceinline__ uint32_t fetch(int from, uint32_t v)
 // its own part of shared memory.  Scales and zero points come for four blocks at
 // a time, lane % 4 the block.  Two blocks of codes are on their way while two
 // are multiplied, of x two blocks or one: more in flight costs registers and
-// time (four blocks of codes: 49.0 against 44.2 us, 16 x 4096 -> 16384 12.9
-// against 12.0).
+// time (four blocks of codes: 32 x 16384 -> 16384 49.0 against 44.2 us, 16 x 4096
+// -> 16384 12.9 against 12.0).
 //
 // Row m of x sits at row 4 (m % 4) + m / 4 of its matrix tile, so that the
 // first E of the four sums a lane holds are the ones in use for M <= 4 E.
@@ -401,12 +410,15 @@ void launch_one(GroupedParams p, hipStream_t s)
 
 // Which variant, by M and N (times in a graph, us):
 // M <= 4: x is small, so one tile a workgroup and many workgroups; four waves
-//   from N > 8192 on (1 x 4096 -> 16384: 10.5 against 11.1 with eight; 4096 ->
-//   4096: 5.0 with eight); a long row of few outputs gets half-filled tiles, to
-//   have a workgroup for every unit (4 x 12288 -> 2048: 7.5 against 8.5).
+//   from N > 8192 on (1 x 4096 -> 12288: 7.8, with eight 10.0; 4096 -> 4096: 5.9,
+//   with eight 5.3); a long row of few outputs gets half-filled tiles, to have a
+//   workgroup for every unit (4 x 12288 -> 2048: 7.7, with whole ones 8.0).
 // M > 4: every workgroup reads all of x, so it takes as many outputs as one
 //   round (or several equal ones) over the units allows, up to 64 (16 x 4096 ->
-//   16384: 12.3 with 64 outputs, 16.8 with 32, 16.0 with 16).
+//   16384: 11.9 with 64 outputs, 14.0 with 32, 15.1 with 16), with eight waves:
+//   two a SIMD cover each other's waits (32 x 16384 -> 16384: 42.8, with four
+//   46.4; 32 x 4096 -> 16384 in groups of 32: 18.7, with four 22.9, although
+//   eight have to keep some 25 of their registers in memory).
 template <typename D, int GROUP, bool ZEROS>
 void launch_zeros(GroupedParams p, hipStream_t s)
 {
@@ -434,7 +446,7 @@ void launch_zeros(GroupedParams p, hipStream_t s)
         if (tiles == 1) launch_one<D, GROUP, ZEROS, 2, 4, 1, 8, 2>(p, s);
         else if (tiles == 2) launch_one<D, GROUP, ZEROS, 2, 4, 2, 8, 2>(p, s);
         else if (tiles == 3) launch_one<D, GROUP, ZEROS, 2, 4, 3, 8, 2>(p, s);
-        else launch_one<D, GROUP, ZEROS, 2, 4, 4, GROUP == 32 ? 4 : 8, GROUP == 32 ? 1 : 2>(p, s);   // eight waves do not have the registers
+        else launch_one<D, GROUP, ZEROS, 2, 4, 4, 8, 2>(p, s);
     }
 }
 
