@@ -535,14 +535,20 @@ GROUPED_ARGS = struct.Struct("@6P3q2i")
 _NORMS = {None: CONVROT_NORM_NONE, "layer": CONVROT_NORM_LAYER, "rms": CONVROT_NORM_RMS}
 _LAYOUTS = {"interleaved": CONVROT_ROPE_INTERLEAVED, "halves": CONVROT_ROPE_HALVES}
 _GROUPS = (32, 64, 128)
-_torch = None   # the module and its types' codes, from the first call on
+_torch = None   # the module, its types' codes and its current device and stream, from the first call on
 _types = {}
+_current_device = _raw_stream = None
 
 
 def _use_torch():
-    global _torch
+    global _torch, _current_device, _raw_stream
     import torch
     _types.update({torch.bfloat16: CONVROT_BF16, torch.float16: CONVROT_F16, torch.float32: CONVROT_F32})
+    # The handles themselves: torch.cuda.current_stream builds an object around
+    # one, which takes longer than a launch.
+    _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda device: torch.cuda.current_stream(device).cuda_stream)
     _torch = torch
     return torch
 
@@ -580,25 +586,17 @@ def _type_of(t, name):
     return code
 
 
-def _raw_stream(device):
-    """The handle of the device's current stream (torch.cuda.current_stream
-    builds an object around it, which takes longer than a launch)."""
-    get = getattr(_torch._C, "_cuda_getCurrentRawStream", None)
-    return get(device) if get is not None else _torch.cuda.current_stream(device).cuda_stream
-
-
 def _launch(device, stream, call):
     """call(raw stream) with the device current, and with ``stream`` (or the
     device's current stream) the one that its allocations belong to."""
-    cuda = _torch.cuda
     if stream is None:
-        if cuda.current_device() == device:
+        if _current_device() == device:
             return call(_raw_stream(device))
-        with cuda.device(device):
+        with _torch.cuda.device(device):
             return call(_raw_stream(device))
     if stream.device.index != device:
         raise ValueError(f"stream is on {stream.device}, the tensors are on cuda:{device}")
-    with cuda.stream(stream):
+    with _torch.cuda.stream(stream):
         return call(stream.cuda_stream)
 
 
@@ -608,10 +606,12 @@ def _rows(t, name, width):
     if not shape or shape[-1] != width:
         raise ValueError(f"{name} must have rows of {width} values, got shape {tuple(shape)}")
     strides = t.stride()
-    if width > 1 and strides[-1] != 1:
+    if strides[-1] != 1 and width > 1:
         raise ValueError(f"{name} must be dense in its last dimension")
     if len(shape) == 2:
         return shape[0], strides[0]
+    if len(shape) == 1:
+        return 1, width
     if t.is_contiguous():
         return (t.numel() // width, width) if width else (0, 0)
     if t.numel() == 0:
@@ -653,22 +653,24 @@ def convrot_residual_norm(x, y=None, *, gate=None, scale=None, shift=None, weigh
         if y.shape != shape or y.dtype != dtype:
             raise ValueError(f"y must have the shape and type of x, got {tuple(y.shape)} {y.dtype}")
         y_ptr, y_stride = y.data_ptr(), _rows(y, "y", width)[1]
-    vec_code, per = 0, 0
-    pointers, strides = [], []
+    vec_type, vec_code, per = None, 0, 0
+    vectors = []   # addresses and strides of gate, scale, shift, weight, post_weight
     for name, v in (("gate", gate), ("scale", scale), ("shift", shift), ("weight", weight),
                     ("post_weight", post_weight)):
         if v is None:
-            pointers.append(0)
-            strides.append(0)
+            vectors.append((0, 0))
             continue
         if not isinstance(v, _torch.Tensor) or v.get_device() != device or v.requires_grad:
             _check_tensor(v, name, device)
-        v_code = _types.get(v.dtype) or _type_of(v, name)
-        if v_code not in (code, CONVROT_F32) or vec_code not in (0, v_code):
-            raise TypeError("the vectors and weights must have one type, that of x or float32")
-        vec_code = v_code
+        if v.dtype is not vec_type:
+            v_code = _type_of(v, name)
+            if vec_type is not None or v_code not in (code, CONVROT_F32):
+                raise TypeError("the vectors and weights must have one type, that of x or float32")
+            vec_type, vec_code = v.dtype, v_code
         n, step = _rows(v, name, width)
-        if n != 1:
+        if n == 1:
+            step = 0
+        else:
             lead = v.shape[:-1]
             while lead and lead[-1] == 1:
                 lead = lead[:-1]
@@ -680,10 +682,8 @@ def convrot_residual_norm(x, y=None, *, gate=None, scale=None, shift=None, weigh
                 if per not in (0, rows // n):
                     raise ValueError("gate, scale and shift must have one vector, or as many as one another")
                 per = rows // n
-        else:
-            step = 0
-        pointers.append(v.data_ptr())
-        strides.append(step)
+        vectors.append((v.data_ptr(), step))
+    (gate_ptr, gate_step), (scale_ptr, scale_step), (shift_ptr, shift_step), (w_ptr, _), (post_ptr, _) = vectors
 
     def output(out, name, wanted):
         """The output given, or a new one: it, its address and row stride."""
@@ -701,8 +701,9 @@ def convrot_residual_norm(x, y=None, *, gate=None, scale=None, shift=None, weigh
         r_out, r_ptr, r_stride = output(r, "r", want_r)
         h_out, h_ptr, h_stride = output(h, "h", want_h)
         _call("convrot_residual_norm", NORM_ARGS.pack(
-            x.data_ptr(), y_ptr, *pointers, r_ptr, h_ptr, rows, width, x_stride, y_stride, r_stride, h_stride,
-            *strides[:3], per or 1, residual_scale, eps, code, vec_code or code, *norms), raw)
+            x.data_ptr(), y_ptr, gate_ptr, scale_ptr, shift_ptr, w_ptr, post_ptr, r_ptr, h_ptr, rows, width, x_stride,
+            y_stride, r_stride, h_stride, gate_step, scale_step, shift_step, per or 1, residual_scale, eps, code,
+            vec_code or code, *norms), raw)
         return r_out, h_out
 
     return _launch(device, stream, call)
@@ -723,6 +724,13 @@ def rope_frequencies(sizes, theta: float = 10000.0, shared: bool = False):
     else:
         freq = np.concatenate([theta ** (-np.arange(s // 2) * 2.0 / s) for s in sizes])
     return freq, axis
+
+
+def _address(a):
+    """Of a host array; ndarray.ctypes, which takes twice as long, where it must be."""
+    if a.size and a.flags.writeable:
+        return ctypes.addressof(ctypes.c_char.from_buffer(a))
+    return a.ctypes.data
 
 
 def _heads(t, out, weight, name, shape, device):
@@ -803,7 +811,8 @@ def convrot_rope(q, k, positions, freq, axis, *, layout: str = "interleaved", qk
         _call("convrot_rope", ROPE_ARGS.pack(
             *fields[0], *fields[1], 1 if k is None else 2, shape[0], shape[1], shape[3], positions.data_ptr(),
             pos_strides[0] if pos_shape[0] > 1 else 0, pos_strides[1], pos_code, pos_shape[2], freq.shape[0],
-            freq.__array_interface__["data"][0], axis.__array_interface__["data"][0], order, CONVROT_NORM_RMS if qk_norm else CONVROT_NORM_NONE, code, eps), raw)
+            _address(freq), _address(axis), order, CONVROT_NORM_RMS if qk_norm else CONVROT_NORM_NONE, code,
+            eps), raw)
         return outs[0], outs[1]
 
     return _launch(device, stream, call)
