@@ -17,9 +17,9 @@
 // TB/s, a kernel that only reads them 5.9 us), 1 x 1024 -> 1024 takes 2.4 us where
 // an empty kernel takes 1.9.  With more rows every compute unit reads all of x
 // and widens its share of the codes, some 60 vector instructions for each 16 x
-// 128 of them beside 8 or 16 matrix instructions: 32 x 16384 -> 16384 takes 45.5
+// 128 of them beside 8 or 16 matrix instructions: 32 x 16384 -> 16384 takes 46
 // us (143 MB, 3.1 TB/s), 34 with its codes in the cache and 26 for reading alone,
-// and 16 x 4128 -> 9001 with groups of 32 takes 13.9 us, 12.5 without its products
+// and 16 x 4128 -> 9001 with groups of 32 takes 14 us, 12.5 without its products
 // and 11.2 with rows of 4096, which begin with a line of memory.
 #pragma once
 #include "block_ops.h"

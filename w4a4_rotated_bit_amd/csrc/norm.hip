@@ -12,7 +12,7 @@
 // before its rounding to the storage type.
 //
 // Bound by memory: 32768 rows of 4096 bf16 with both norms, every vector and
-// both outputs move 1.07 GB in 212 us (5.1 TB/s; a copy of that size reaches
+// both outputs move 1.07 GB in 215 us (5.0 TB/s; a copy of that size reaches
 // 5.0 TB/s, one of 256 MB 5.5), 1536 rows 50 MB in 12.5 us.  Short inputs are
 // bound by latency: one row of 4096 takes 2.4 us where an empty kernel takes
 // 1.9, and 999 rows of 1035 f16, two norms, 6.5 us: four sums across the
@@ -20,7 +20,7 @@
 //
 // One row a workgroup, and nothing else kept from row to row: workgroups that
 // went on to further rows, with the vectors in registers, held fewer rows in
-// flight (250 against 212 us for the 32768 rows).
+// flight (250 against 215 us for the 32768 rows).
 #include "block_ops.h"
 
 namespace convrot {

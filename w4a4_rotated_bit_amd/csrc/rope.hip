@@ -12,8 +12,8 @@
 // its token's angles once for all the heads it takes, up to 32 of 128 bf16.
 //
 // Bound by memory where there are many tokens: 32768 tokens of 16 + 16 heads of
-// 128 bf16 with norms, heads first, move 537 MB in 100 us (5.4 TB/s; a copy of
-// 256 MB reaches 5.5).  1536 such tokens (25 MB) take 9.6 us, of which the angles'
+// 128 bf16 with norms, heads first, move 537 MB in 98 to 106 us (5.1 TB/s and more;
+// a copy of 256 MB reaches 5.5).  1536 such tokens (25 MB) take 9.6 us, of which the angles'
 // binary64 and sincos, the norms and the launch are about half: the chip holds
 // every wave at once, so their latencies add up instead of hiding one another.
 // One token of each of four sequences takes 2.95 us where an empty kernel takes
