@@ -206,6 +206,18 @@ def test_norm_leaves_the_gaps_of_its_outputs(gpu):
     assert (buf[keep] == 5.0).all()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows_per_vec", [5, 6, 1 << 31, 1 << 32, (1 << 63) - 1])
+def test_norm_one_vector_for_any_number_of_rows(gpu, rows_per_vec):
+    x, gate = rand((5, 64), 1, torch.bfloat16).cuda(), rand((1, 64), 2, torch.bfloat16).cuda()
+    want = B.convrot_residual_norm(x, x, gate=gate)
+    r, h = torch.empty_like(x), torch.empty_like(x)
+    args = norm_args(x_dev=x.data_ptr(), y_dev=x.data_ptr(), gate_dev=gate.data_ptr(), gate_stride=64, r_dev=r.data_ptr(),
+                     h_dev=h.data_ptr(), rows=5, rows_per_vec=rows_per_vec)
+    assert B.load().convrot_residual_norm(args, torch.cuda.current_stream().cuda_stream) == B.CONVROT_OK
+    assert torch.equal(r, want[0]) and torch.equal(h, want[1])
+
+
 def packed(layout, defaults, kw):
     """The bytes of an argument struct: `defaults` in the order of its fields, some replaced."""
     assert set(kw) <= set(defaults)

@@ -115,7 +115,7 @@ int convrot_validate_residual_norm(const convrot_residual_norm_args* args)
         if (y.at && !out.same(y) && !apart(y, out)) return CONVROT_EINVAL;
     }
     if (r.at && h.at && !apart(r, h)) return CONVROT_EINVAL;
-    const int64_t vectors = (a.rows + a.rows_per_vec - 1) / a.rows_per_vec;
+    const int64_t vectors = (a.rows - 1) / a.rows_per_vec + 1;
     const struct {
         const void* at;
         int64_t stride, count;

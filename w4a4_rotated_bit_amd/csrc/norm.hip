@@ -249,7 +249,7 @@ void launch_residual_norm(const convrot_residual_norm_args& a, hipStream_t s)
     p.scale_stride = a.scale_stride;
     p.shift_stride = a.shift_stride;
     p.rows = (int)a.rows;
-    p.rows_per_vec = (int)a.rows_per_vec;
+    p.rows_per_vec = (int)(a.rows_per_vec < a.rows ? a.rows_per_vec : a.rows);
     p.width = (int)a.width;
     p.norm = a.norm;
     p.post_norm = a.y_dev ? a.post_norm : CONVROT_NORM_NONE;
