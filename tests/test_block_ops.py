@@ -264,6 +264,16 @@ def test_norm_refusals(kw, ok):
         assert B.load().convrot_residual_norm(norm_args(**kw), None) == B.CONVROT_EINVAL
 
 
+@pytest.mark.parametrize("name", ["x_stride", "y_stride", "r_stride", "h_stride", "gate_stride", "scale_stride", "shift_stride"])
+@pytest.mark.parametrize("rows,stride,ok", [(2, 1 << 40, True), (2, (1 << 40) + 1, False), (1 << 16, 1 << 40, True),
+                                            ((1 << 16) + 2, 1 << 40, False), (1 << 24, 1 << 40, False)])
+def test_norm_strides_that_reach_too_far(name, rows, stride, ok):
+    places = {"x_dev": 1, "y_dev": 2, "r_dev": 3, "h_dev": 4, "gate_dev": 5, "scale_dev": 5, "shift_dev": 5}
+    far = {key: i << 59 for key, i in places.items()}   # further from one another than any of them reaches
+    rc = B.load().convrot_validate_residual_norm(norm_args(**far, rows=rows, **{name: stride}))
+    assert rc == (B.CONVROT_OK if ok else B.CONVROT_EINVAL)
+
+
 # ---- rotary positions ----------------------------------------------------------
 
 
@@ -445,6 +455,25 @@ def test_rope_refusals(kw, ok):
     assert rc == (B.CONVROT_OK if ok else B.CONVROT_EINVAL)
     if not ok:
         assert B.load().convrot_rope(a, None) == B.CONVROT_EINVAL
+
+
+@pytest.mark.parametrize("sizes,strides,ok", [
+    ({"tokens": (1 << 16) + 1}, {"token_stride": 1 << 40}, True), ({"tokens": (1 << 16) + 2}, {"token_stride": 1 << 40}, False),
+    ({"tokens": 1 << 24}, {"token_stride": 1 << 40}, False), ({"batch": 65535}, {"batch_stride": 1 << 40}, True),
+    ({"heads": 65535}, {"head_stride": 1 << 40}, True), ({"heads": 4}, {"head_stride": (1 << 40) + 1}, False)])
+@pytest.mark.parametrize("side", ["in", "out", "pos"])
+def test_rope_strides_that_reach_too_far(side, sizes, strides, ok):
+    if side == "pos" and "heads" in sizes:
+        return
+    strides = {f"{side}_{key}": v for key, v in strides.items()}
+    n, tokens = sizes.get("heads", 4), sizes.get("tokens", 3)
+    heads = dict(in_dev=1 << 60, out_dev=2 << 60, heads=n)
+    for end in ("in", "out"):   # dense, but for the stride in question
+        heads |= {f"{end}_head_stride": 64, f"{end}_token_stride": 64 * n, f"{end}_batch_stride": 64 * n * tokens}
+    heads |= {key: v for key, v in strides.items() if side != "pos"}
+    rest = {key: v for key, v in strides.items() if side == "pos"}
+    a = rope_args(q=heads, count=1, pos_dev=3 << 60, tokens=tokens, batch=sizes.get("batch", 1), **rest)
+    assert B.load().convrot_validate_rope(a) == (B.CONVROT_OK if ok else B.CONVROT_EINVAL)
 
 
 # ---- group-scaled 4-bit weights --------------------------------------------------

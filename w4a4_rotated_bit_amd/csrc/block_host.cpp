@@ -73,8 +73,13 @@ bool apart(const Block& a, const Block& b, int64_t d, int level)
 }
 bool apart(const Block& a, const Block& b) { return apart(a, b, (int64_t)((intptr_t)b.at - (intptr_t)a.at), 0); }
 
-// largest stride taken: keeps every offset far inside 64 bits
-constexpr int64_t kMaxStride = (int64_t)1 << 40;
+// largest stride taken, and largest offset that a dimension may reach, in
+// elements: keeps every offset far inside 64 bits
+constexpr int64_t kMaxStride = (int64_t)1 << 40, kMaxReach = (int64_t)1 << 56;
+bool reaches(int64_t n, int64_t stride)
+{
+    return within(stride, 0, kMaxStride) && (n <= 1 || stride <= kMaxReach / (n - 1));
+}
 
 }  // namespace
 
@@ -88,8 +93,11 @@ int convrot_validate_residual_norm(const convrot_residual_norm_args* args)
     if (!within(a.rows, 0, kMaxRows) || !within(a.width, 1, kMaxNormWidth)) return CONVROT_EINVAL;
     if (!known_norm(a.norm) || !known_norm(a.post_norm)) return CONVROT_EINVAL;
     if (!(a.eps >= 0.f) || a.rows_per_vec < 1) return CONVROT_EINVAL;
-    for (int64_t s : {a.x_stride, a.y_stride, a.r_stride, a.h_stride, a.gate_stride, a.scale_stride, a.shift_stride})
-        if (!within(s, 0, kMaxStride)) return CONVROT_EINVAL;
+    const int64_t vectors = a.rows > 0 ? (a.rows - 1) / a.rows_per_vec + 1 : 0;
+    for (int64_t s : {a.x_stride, a.y_stride, a.r_stride, a.h_stride})
+        if (!reaches(a.rows, s)) return CONVROT_EINVAL;
+    for (int64_t s : {a.gate_stride, a.scale_stride, a.shift_stride})
+        if (!reaches(vectors, s)) return CONVROT_EINVAL;
     if (a.rows == 0) return CONVROT_OK;   // empty buffers may be NULL
     if (!a.y_dev && (a.gate_dev || a.post_norm != CONVROT_NORM_NONE)) return CONVROT_EINVAL;
     if (a.post_weight_dev && a.post_norm == CONVROT_NORM_NONE) return CONVROT_EINVAL;
@@ -115,7 +123,6 @@ int convrot_validate_residual_norm(const convrot_residual_norm_args* args)
         if (y.at && !out.same(y) && !apart(y, out)) return CONVROT_EINVAL;
     }
     if (r.at && h.at && !apart(r, h)) return CONVROT_EINVAL;
-    const int64_t vectors = (a.rows - 1) / a.rows_per_vec + 1;
     const struct {
         const void* at;
         int64_t stride, count;
@@ -143,16 +150,16 @@ int convrot_validate_rope(const convrot_rope_args* args)
     if (a.layout != CONVROT_ROPE_INTERLEAVED && a.layout != CONVROT_ROPE_HALVES) return CONVROT_EINVAL;
     if (a.norm != CONVROT_NORM_NONE && a.norm != CONVROT_NORM_RMS) return CONVROT_EINVAL;
     if (!(a.eps >= 0.f) || (a.pos_dtype != CONVROT_I32 && a.pos_dtype != CONVROT_F32)) return CONVROT_EINVAL;
-    if (!within(a.pos_batch_stride, 0, kMaxStride) || !within(a.pos_token_stride, 0, kMaxStride)) return CONVROT_EINVAL;
+    if (!reaches(a.batch, a.pos_batch_stride) || !reaches(a.tokens, a.pos_token_stride)) return CONVROT_EINVAL;
     const bool empty = a.batch == 0 || a.tokens == 0;
     if (!empty && (!a.pos_dev || !aligned(a.pos_dev, 4))) return CONVROT_EINVAL;
     const int e = elem_bytes(a.dtype);
     for (int k = 0; k < a.count; ++k) {
         const convrot_heads& h = a.heads[k];
         if (!within(h.heads, 1, kMaxHeads)) return CONVROT_EINVAL;
-        for (int64_t s : {h.in_batch_stride, h.in_token_stride, h.in_head_stride, h.out_batch_stride,
-                          h.out_token_stride, h.out_head_stride})
-            if (!within(s, 0, kMaxStride)) return CONVROT_EINVAL;
+        if (!reaches(a.batch, h.in_batch_stride) || !reaches(a.batch, h.out_batch_stride)) return CONVROT_EINVAL;
+        if (!reaches(a.tokens, h.in_token_stride) || !reaches(a.tokens, h.out_token_stride)) return CONVROT_EINVAL;
+        if (!reaches(h.heads, h.in_head_stride) || !reaches(h.heads, h.out_head_stride)) return CONVROT_EINVAL;
         if (h.weight_dev && a.norm == CONVROT_NORM_NONE) return CONVROT_EINVAL;
         if (empty) continue;
         if (!h.in_dev || !h.out_dev) return CONVROT_EINVAL;
