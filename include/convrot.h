@@ -287,7 +287,8 @@ int convrot_gemm(const void* workspace_dev, size_t ws_bytes, int64_t M, int64_t 
  *     before the call returns and not kept;
  *   - strides are in elements, inputs need only the alignment of their
  *     elements (16-byte aligned rows run faster; the grouped linear's X and
- *     codes have to be 16-byte aligned), and rows need not be dense;
+ *     codes have to be 16-byte aligned), and rows need not be dense; a stride is
+ *     at most 2^40, and the last row within 2^56 elements of the first;
  *   - no workspace: nothing is shared between calls, on any stream or graph;
  *   - outputs must not overlap inputs or one another, except where a field
  *     says so (CONVROT_EINVAL).
@@ -407,6 +408,8 @@ int convrot_validate_linear_grouped(const convrot_grouped_args* args_host);
  * finite makes its group's scale NaN. */
 int convrot_quantize_weight_grouped(const void* W_dev, int64_t N, int64_t K, int group, int dtype, uint8_t* codes_dev,
                                     void* scales_dev, uint8_t* zeros_dev, void* stream);
+int convrot_validate_quantize_weight_grouped(const void* W_dev, int64_t N, int64_t K, int group, int dtype,
+                                             const uint8_t* codes_dev, const void* scales_dev, const uint8_t* zeros_dev);
 
 /* ---- parity hooks (same kernels, exposed intermediate results) ---------- */
 

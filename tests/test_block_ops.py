@@ -647,6 +647,19 @@ def test_quantize_grouped_refusals():
     assert f(*([None, 0] + good[2:])) == B.CONVROT_OK
 
 
+@pytest.mark.parametrize("codes,scales,zeros,ok", [
+    (2048, 2560, 2592, True), (2047, 4096, None, False), (4096, 2046, None, False), (4096, 8192, 2047, False),
+    (4096, 4096 + 510, None, False), (4096, 4096 + 512, 4096 + 512 + 31, False), (4096, 4096 - 32, None, True),
+    (4096, 4096 - 30, None, False), (4096, 8192, 4096, False)])
+def test_quantize_grouped_refuses_overlaps(codes, scales, zeros, ok):
+    # W: 4 x 256 bf16, 2048 bytes; codes 512, scales 32, zeros 16
+    args = (P, 4, 256, 64, 1, P + codes, P + scales, zeros and P + zeros)
+    rc = B.load().convrot_validate_quantize_weight_grouped(*args)
+    assert rc == (B.CONVROT_OK if ok else B.CONVROT_EINVAL)
+    if not ok:
+        assert B.load().convrot_quantize_weight_grouped(*args, None) == B.CONVROT_EINVAL
+
+
 def test_host_tensors_are_refused():
     x = torch.zeros((2, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="device tensor"):

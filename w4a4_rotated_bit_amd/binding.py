@@ -98,6 +98,7 @@ _SIGNATURES = {
     "convrot_linear_grouped": ([_P, _P], _I),
     "convrot_validate_linear_grouped": ([_P], _I),
     "convrot_quantize_weight_grouped": ([_P, _I64, _I64, _I, _I, _P, _P, _P, _P], _I),
+    "convrot_validate_quantize_weight_grouped": ([_P, _I64, _I64, _I, _I, _P, _P, _P], _I),
     "convrot_host_pack_nk": ([_P, _I64, _I64, _P], _I),
     "convrot_host_unpack_nk": ([_P, _I64, _I64, _P], _I),
     "convrot_host_nk_to_kn": ([_P, _I64, _I64, _P], _I),

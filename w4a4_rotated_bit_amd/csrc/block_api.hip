@@ -47,13 +47,9 @@ int convrot_linear_grouped(const convrot_grouped_args* args, void* stream)
 int convrot_quantize_weight_grouped(const void* W, int64_t N, int64_t K, int group, int dtype, uint8_t* codes,
                                     void* scales, uint8_t* zeros, void* stream)
 {
-    if (dtype != CONVROT_BF16 && dtype != CONVROT_F16) return CONVROT_EINVAL;
-    if (group != 32 && group != 64 && group != 128) return CONVROT_EINVAL;
-    if (N < 0 || N > kMaxRows || K < group || K > kMaxGroupedK || K % group != 0) return CONVROT_EINVAL;
-    if (N == 0) return CONVROT_OK;
-    if (!W || !codes || !scales || !aligned(W, 2) || !aligned(scales, 2)) return CONVROT_EINVAL;
-    const int rc = check_device();
-    if (rc) return rc;
+    int rc = convrot_validate_quantize_weight_grouped(W, N, K, group, dtype, codes, scales, zeros);
+    if (rc || N == 0) return rc;
+    if ((rc = check_device())) return rc;
     launch_quantize_grouped(W, N, K, group, dtype, codes, scales, zeros, (hipStream_t)stream);
     return launched();
 }

@@ -210,4 +210,20 @@ int convrot_validate_linear_grouped(const convrot_grouped_args* args)
     return CONVROT_OK;
 }
 
+int convrot_validate_quantize_weight_grouped(const void* W, int64_t N, int64_t K, int group, int dtype,
+                                             const uint8_t* codes, const void* scales, const uint8_t* zeros)
+{
+    if (dtype != CONVROT_BF16 && dtype != CONVROT_F16) return CONVROT_EINVAL;
+    if (group != 32 && group != 64 && group != 128) return CONVROT_EINVAL;
+    if (!within(N, 0, kMaxRows) || !within(K, group, kMaxGroupedK) || K % group != 0) return CONVROT_EINVAL;
+    if (N == 0) return CONVROT_OK;
+    if (!W || !codes || !scales || !aligned(W, 2) || !aligned(scales, 2)) return CONVROT_EINVAL;
+    const int64_t groups = N * (K / group);
+    const Block all[] = {Block(W, N * K, 2), Block(codes, N * (K / 2), 1), Block(scales, groups, 2), Block(zeros, groups, 1)};
+    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < i; ++j)
+            if (all[i].at && !apart(all[i], all[j])) return CONVROT_EINVAL;
+    return CONVROT_OK;
+}
+
 }  // extern "C"
