@@ -134,8 +134,12 @@ __device__ __forceinline__ uint32_t fetch(int from, uint32_t v)
 // Row m of x sits at row 4 (m % 4) + m / 4 of its matrix tile, so that the
 // first E of the four sums a lane holds are the ones in use for M <= 4 E.
 //
+// LINES: every row of the codes is whole lines of memory, which are then loaded
+// with the hint that they are used once (1 x 4096 -> 12288 8.6 -> 8.0 us, 32 x 16384
+// -> 16384 47.4 -> 44.9); where rows begin inside a line, two loads want it (16 x
+// 4128 -> 9001 14.2 -> 15.2).
 // OCC: the waves of a SIMD that the registers have to leave room for.
-template <typename D, int GROUP, bool ZEROS, int MT, int E, int NT, int W, int OCC>
+template <typename D, int GROUP, bool ZEROS, bool LINES, int MT, int E, int NT, int W, int OCC>
 __global__ __launch_bounds__(W * 64, OCC) void grouped_kernel(GroupedParams p)
 {
     typedef typename Mat<D>::Frag Frag;
@@ -240,7 +244,7 @@ __global__ __launch_bounds__(W * 64, OCC) void grouped_kernel(GroupedParams p)
             for (int i = 0; i < 2 * NT; ++i) {
                 uint32_t row = (uint32_t)(8 * i) * (uint32_t)(p.K / 2);
                 if constexpr (MT > 1) asm volatile("" : "+s"(row));
-                w[i] = __builtin_amdgcn_raw_buffer_load_b128(codes, at + row, 0, 0);
+                w[i] = __builtin_amdgcn_raw_buffer_load_b128(codes, at + row, 0, LINES ? 2 : 0);
             }
         };
         const auto load_x = [&](u32x4 (&to)[kXLoads], int b) {
@@ -352,7 +356,7 @@ __global__ __launch_bounds__(W * 64, OCC) void grouped_kernel(GroupedParams p)
                 __builtin_amdgcn_sched_barrier(0);
             }
     }
-    if (wave == W - 1 && p.K % 128 != 0) {   // a row that ends inside a block: zeros behind it
+    if (!LINES && wave == W - 1 && p.K % 128 != 0) {   // a row that ends inside a block: zeros behind it
         u32x4 w[NT], x[MT][4];
         uint32_t s[NT][kWords] = {}, z[NT] = {};
 #pragma unroll
@@ -404,8 +408,11 @@ __global__ __launch_bounds__(W * 64, OCC) void grouped_kernel(GroupedParams p)
 template <typename D, int GROUP, bool ZEROS, int MT, int E, int NT, int W, int OCC>
 void launch_one(GroupedParams p, hipStream_t s)
 {
-    hipLaunchKernelGGL((grouped_kernel<D, GROUP, ZEROS, MT, E, NT, W, OCC>), dim3((p.N + p.rows - 1) / p.rows),
-                       dim3(W * 64), 0, s, p);
+    const dim3 grid((p.N + p.rows - 1) / p.rows), block(W * 64);
+    if (p.K % 256 == 0 && (uintptr_t)p.codes % 128 == 0)
+        hipLaunchKernelGGL((grouped_kernel<D, GROUP, ZEROS, true, MT, E, NT, W, OCC>), grid, block, 0, s, p);
+    else
+        hipLaunchKernelGGL((grouped_kernel<D, GROUP, ZEROS, false, MT, E, NT, W, OCC>), grid, block, 0, s, p);
 }
 
 // Which variant, by M and N (times in a graph, us):
