@@ -61,6 +61,20 @@ __device__ __forceinline__ void store_chunk(T* p, typename VecOf<T, V>::type v)
     typedef typename VecOf<T, V>::type Any __attribute__((aligned(sizeof(T))));
     *(Any*)p = v;
 }
+// The same with the hint that the data is used once: lines that are read or
+// written whole need not stay in the caches near the units.
+template <typename T, int V>
+__device__ __forceinline__ typename VecOf<T, V>::type load_once(const T* p)
+{
+    typedef typename VecOf<T, V>::type Any __attribute__((aligned(sizeof(T))));
+    return __builtin_nontemporal_load((const Any*)p);
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_once(T* p, typename VecOf<T, V>::type v)
+{
+    typedef typename VecOf<T, V>::type Any __attribute__((aligned(sizeof(T))));
+    __builtin_nontemporal_store((Any)v, (Any*)p);
+}
 
 // v of another lane of the same 16, by a lane permutation of the vector unit
 // (a shuffle through shared memory takes some ten times as long).

@@ -115,14 +115,15 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void residual_norm_kernel(NormPa
     Vector gate[NV], scale[NV], shift[NV], weight[NV], post_weight[NV];
     const D* const xp = (const D*)p.x + row * p.x_stride;
     const D* const yp = (const D*)p.y + row * p.y_stride;
+    const auto load = [](const D* p) { return TAIL ? load_chunk<D, V>(p) : load_once<D, V>(p); };
     Chunk x[NV], y[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-        if (in[j]) x[j] = load_chunk<D, V>(xp + at[j]);
+        if (in[j]) x[j] = load(xp + at[j]);
     if (p.y) {
 #pragma unroll
         for (int j = 0; j < NV; ++j)
-            if (in[j]) y[j] = load_chunk<D, V>(yp + at[j]);
+            if (in[j]) y[j] = load(yp + at[j]);
     }
     const int64_t vec = row / p.rows_per_vec;
     const E* const gate_p = (const E*)p.gate + vec * p.gate_stride;
@@ -164,7 +165,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void residual_norm_kernel(NormPa
             Chunk c;
 #pragma unroll
             for (int i = 0; i < V; ++i) c[i] = (D)r[j][i];
-            if (in[j]) store_chunk<D, V>(to + at[j], c);
+            if (in[j]) TAIL ? store_chunk<D, V>(to + at[j], c) : store_once<D, V>(to + at[j], c);
         }
     };
     if (p.r) store((D*)p.r + row * p.r_stride);

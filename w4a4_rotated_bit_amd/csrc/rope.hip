@@ -71,8 +71,9 @@ enum Exchange { PAIRS, CHUNKS, ELEMENTS };   // how a lane gets the other elemen
 //   PAIRS:    interleaved pairs, within the chunk
 //   CHUNKS:   halves of whole chunks: the pairs' other elements are one lane's
 //   ELEMENTS: halves of any size: through shared memory
+// WHOLE: a head is L chunks, none of them shared.
 // All loads of an item precede its stores: the output may be the input.
-template <typename D, int L, Exchange EX, int IW>
+template <typename D, int L, Exchange EX, int IW, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p)
 {
     constexpr int V = 16 / sizeof(D), kHeads = 64 / L;
@@ -84,8 +85,8 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p)
     const int64_t b = blockIdx.y, t = (int64_t)blockIdx.x * (kThreads / 64) + wave;
     if (t >= p.tokens) return;
     const int g = lane / L, c = lane % L;
-    const bool in = c * V < p.dim;
-    const int at = min(c * V, p.dim - V), skip = c * V - at;
+    const bool in = WHOLE || c * V < p.dim;
+    const int at = WHOLE ? c * V : min(c * V, p.dim - V), skip = c * V - at;
     const int items0 = (p.t[0].heads + kHeads - 1) / kHeads;
     const int items = items0 + (p.count > 1 ? (p.t[1].heads + kHeads - 1) / kHeads : 0);
     const int first = (int)blockIdx.z * IW;
@@ -110,7 +111,7 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p)
         const D* const base = second ? (const D*)p.t[1].in + b * p.t[1].in_batch + t * p.t[1].in_token + head * p.t[1].in_head
                                      : (const D*)p.t[0].in + b * p.t[0].in_batch + t * p.t[0].in_token + head * p.t[0].in_head;
         x[u] = Chunk{};
-        if (has[u]) x[u] = load_chunk<D, V>(base + (second ? in1 : in0));
+        if (has[u]) x[u] = load_once<D, V>(base + (second ? in1 : in0));
     }
     constexpr int kKinds = IW == 1 ? 1 : kMaxRopeTensors;   // tensors a wave may meet
     Chunk weight[kKinds];
@@ -212,7 +213,8 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p)
         }
         D* const base = second ? (D*)p.t[1].out + b * p.t[1].out_batch + t * p.t[1].out_token + head * p.t[1].out_head
                                : (D*)p.t[0].out + b * p.t[0].out_batch + t * p.t[0].out_token + head * p.t[0].out_head;
-        if (has[u]) store_chunk<D, V>(base + (second ? out1 : out0), y);
+        D* const to = base + (second ? out1 : out0);
+        if (has[u]) WHOLE ? store_once<D, V>(to, y) : store_chunk<D, V>(to, y);
     }
 }
 
@@ -272,7 +274,7 @@ __global__ __launch_bounds__(kThreads) void rope_any_kernel(RopeParams p, int ha
     }
 }
 
-template <typename D, int L, Exchange EX>
+template <typename D, int L, Exchange EX, bool WHOLE>
 void launch_items(const RopeParams& p, int batch, hipStream_t s)
 {
     constexpr int kHeads = 64 / L, kWaves = kThreads / 64;
@@ -284,20 +286,21 @@ void launch_items(const RopeParams& p, int batch, hipStream_t s)
     // of them 148, 110, 98).
     const auto grid = [&](int each) { return dim3((p.tokens + kWaves - 1) / kWaves, batch, (items + each - 1) / each); };
     if (all >= 64 * kUnits && items > 4)
-        hipLaunchKernelGGL((rope_kernel<D, L, EX, 8>), grid(8), dim3(kThreads), 0, s, p);
+        hipLaunchKernelGGL((rope_kernel<D, L, EX, 8, WHOLE>), grid(8), dim3(kThreads), 0, s, p);
     else if (all >= 16 * kUnits && items > 1)
-        hipLaunchKernelGGL((rope_kernel<D, L, EX, 4>), grid(4), dim3(kThreads), 0, s, p);
+        hipLaunchKernelGGL((rope_kernel<D, L, EX, 4, WHOLE>), grid(4), dim3(kThreads), 0, s, p);
     else
-        hipLaunchKernelGGL((rope_kernel<D, L, EX, 1>), grid(1), dim3(kThreads), 0, s, p);
+        hipLaunchKernelGGL((rope_kernel<D, L, EX, 1, WHOLE>), grid(1), dim3(kThreads), 0, s, p);
 }
 
 template <typename D, int L>
 void launch_lanes(const RopeParams& p, bool halves, int batch, hipStream_t s)
 {
     constexpr int V = 16 / sizeof(D);
-    if (!halves) launch_items<D, L, PAIRS>(p, batch, s);
-    else if (p.dim % V == 0 && p.pairs % V == 0) launch_items<D, L, CHUNKS>(p, batch, s);
-    else launch_items<D, L, ELEMENTS>(p, batch, s);
+    const bool whole = p.dim == L * V, chunks = p.dim % V == 0 && p.pairs % V == 0;
+    if (halves && !chunks) launch_items<D, L, ELEMENTS, false>(p, batch, s);
+    else if (halves) whole ? launch_items<D, L, CHUNKS, true>(p, batch, s) : launch_items<D, L, CHUNKS, false>(p, batch, s);
+    else whole ? launch_items<D, L, PAIRS, true>(p, batch, s) : launch_items<D, L, PAIRS, false>(p, batch, s);
 }
 
 template <typename D>
