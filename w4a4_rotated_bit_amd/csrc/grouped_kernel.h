@@ -13,12 +13,12 @@
 //
 // The codes are read as they are interchanged, N x packed-K.
 //
-// Few rows are bound by memory: 1 x 4096 -> 12288 reads 26 MB in 8.0 us (3.3
+// Few rows are bound by memory: 1 x 4096 -> 12288 reads 26 MB in 7.9 us (3.3
 // TB/s, a kernel that only reads them 5.9 us), 1 x 1024 -> 1024 takes 2.4 us where
 // an empty kernel takes 1.9.  With more rows every compute unit reads all of x
 // and widens its share of the codes, some 60 vector instructions for each 16 x
-// 128 of them beside 8 or 16 matrix instructions: 32 x 16384 -> 16384 takes 46
-// us (143 MB, 3.1 TB/s), 34 with its codes in the cache and 26 for reading alone,
+// 128 of them beside 8 or 16 matrix instructions: 32 x 16384 -> 16384 takes 44
+// us (143 MB, 3.2 TB/s), 34 with its codes in the cache and 26 for reading alone,
 // and 16 x 4128 -> 9001 with groups of 32 takes 14 us, 12.5 without its products
 // and 11.2 with rows of 4096, which begin with a line of memory.
 #pragma once
@@ -128,8 +128,8 @@ __device__ __forceinline__ uint32_t fetch(int from, uint32_t v)
 // its own part of shared memory.  Scales and zero points come for four blocks at
 // a time, lane % 4 the block.  Two blocks of codes are on their way while two
 // are multiplied, of x two blocks or one: more in flight costs registers and
-// time (four blocks of codes: 32 x 16384 -> 16384 49.0 against 44.2 us, 16 x 4096
-// -> 16384 12.9 against 12.0).
+// time (four blocks of codes: 32 x 16384 -> 16384 49 against 44 us, 16 x 4096 -> 16384
+// 12.9 against 12.0).
 //
 // Row m of x sits at row 4 (m % 4) + m / 4 of its matrix tile, so that the
 // first E of the four sums a lane holds are the ones in use for M <= 4 E.

@@ -12,12 +12,15 @@
 // its token's angles once for all the heads it takes, up to 32 of 128 bf16.
 //
 // Bound by memory where there are many tokens: 32768 tokens of 16 + 16 heads of
-// 128 bf16 with norms, heads first, move 537 MB in 98 to 106 us (5.1 TB/s and more;
-// a copy of 256 MB reaches 5.5).  1536 such tokens (25 MB) take 9.6 us, of which the angles'
-// binary64 and sincos, the norms and the launch are about half: the chip holds
-// every wave at once, so their latencies add up instead of hiding one another.
-// One token of each of four sequences takes 2.95 us where an empty kernel takes
-// 1.9; 3 x 333 tokens of 72, whose halves end inside a chunk, 6.2 us.
+// 128 bf16 with norms, heads first, move 537 MB in 96 us (5.6 TB/s; a copy of
+// 256 MB reaches 5.5).  1536 such tokens (25 MB) take 6.6 us (3.8 TB/s): the chip
+// holds every wave at once, so what a wave waits for -- its position, its heads,
+// sincos, the norm -- adds up instead of hiding behind other waves.  Heads are
+// loaded and stored with the hint that they are used once (without it 104 and
+// 9.6 us); the stores not where lanes are idle, which end inside lines (3 x 333
+// tokens of 72 6.5 against 6.2 us).  One token of each of four sequences takes
+// 3.0 us where an empty kernel takes 1.9; those tokens of 72, whose halves end
+// inside a chunk, 6.1 us.
 #include "block_ops.h"
 
 namespace convrot {
@@ -282,8 +285,8 @@ void launch_items(const RopeParams& p, int batch, hipStream_t s)
     const int64_t all = (int64_t)p.tokens * batch * items;
     // Items a wave takes, one, four or eight: more of them share the token's
     // angles, fewer spread few tokens over more waves (one token of each of four
-    // sequences 3.0, 3.7, 4.6 us; 1536 tokens of 32 heads 11.3, 9.7, 10.7; 32768
-    // of them 148, 110, 98).
+    // sequences 3.0, 3.7, 4.6 us; 1536 tokens of 32 heads 8.9, 6.6, 7.5; 32768 of
+    // them 141 with one, 96 with eight).
     const auto grid = [&](int each) { return dim3((p.tokens + kWaves - 1) / kWaves, batch, (items + each - 1) / each); };
     if (all >= 64 * kUnits && items > 4)
         hipLaunchKernelGGL((rope_kernel<D, L, EX, 8, WHOLE>), grid(8), dim3(kThreads), 0, s, p);
