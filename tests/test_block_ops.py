@@ -577,6 +577,35 @@ def test_grouped_every_channel_meets_its_own_code(gpu, group):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("k,group", [(32, 32), (96, 32), (160, 32), (192, 32), (224, 32), (544, 32), (1120, 32), (4128, 32),
+                                     (4192, 32), (6240, 32), (64, 64), (192, 64), (576, 64), (1088, 64), (4160, 64), (128, 32),
+                                     (1152, 64), (4224, 128)])
+def test_grouped_rows_that_end_inside_a_block(gpu, k, group, zeros):
+    """Whatever the next row holds stays out: every other output's scales are NaN,
+    and so is the second row of x.  The rest are integers times powers of two, so
+    that every sum (at most 6240 * 15 * 4 * 8 eighths, below 2^24) is exact."""
+    n = 37
+    g = torch.Generator().manual_seed(k)
+    codes = torch.randint(0, 256, (n, k // 2), generator=g, dtype=torch.uint8)
+    z = torch.randint(0, 16, (n, k // group), generator=g, dtype=torch.uint8) if zeros else None
+    s = 2.0 ** torch.randint(-3, 1, (n, k // group), generator=g).to(torch.bfloat16)
+    q = codes_of(codes, z, group) * s.double().repeat_interleave(group, 1)
+    s[1::2] = float("nan")
+    for m in (1, 3, 7, 16, 32):
+        x = torch.randint(-4, 5, (m, k), generator=g).to(torch.bfloat16)
+        want = (x.double() @ q.t()).to(torch.bfloat16)
+        if m > 1:
+            x[1] = float("nan")
+        y = B.convrot_linear_grouped(dev(x), dev(codes), dev(s), dev(z), None, group).cpu()
+        assert y[:, 1::2].isnan().all()
+        good = torch.arange(m) != 1
+        assert torch.equal(y[good][:, ::2], want[good][:, ::2]), m
+        if m > 1:
+            assert y[1].isnan().all()
+
+
+@pytest.mark.gpu
 def test_grouped_infinite_rows_stay_alone(gpu):
     x = rand((3, 256), 1, torch.bfloat16).cuda()
     codes = torch.randint(0, 256, (40, 128), generator=torch.Generator().manual_seed(1), dtype=torch.uint8).cuda()

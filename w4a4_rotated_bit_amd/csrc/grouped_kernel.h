@@ -19,8 +19,10 @@
 // and widens its share of the codes, some 60 vector instructions for each 16 x
 // 128 of them beside 8 or 16 matrix instructions: 32 x 16384 -> 16384 takes 44
 // us (143 MB, 3.2 TB/s), 34 with its codes in the cache and 26 for reading alone,
-// and 16 x 4128 -> 9001 with groups of 32 takes 14 us, 12.5 without its products
-// and 11.2 with rows of 4096, which begin with a line of memory.
+// and 16 x 4128 -> 9001 with groups of 32 takes 13.3 us: 4.3 for
+// launch, first loads and the joining of the waves, then 1.6 to 1.8 for each block
+// of a wave, bound by the widening (10.8 with rows of 4096, which begin with a
+// line of memory and need four blocks of a wave instead of five).
 #pragma once
 #include "block_ops.h"
 
@@ -149,6 +151,7 @@ __global__ __launch_bounds__(W * 64, OCC) void grouped_kernel(GroupedParams p)
     constexpr bool kTurn = GROUP != 128;             // step j holds k = 32 j + 8 q, without it k = 32 q + 8 j
     constexpr int kXLoads = E * MT;                  // four rows of x a load
     constexpr int PX = E == 1 ? 2 : 1;               // blocks of x loaded ahead
+    constexpr uint32_t kNowhere = 0x80000000u;       // an offset behind any buffer, whatever row is added
     constexpr bool kInOrder = kXLoads > 2 * NT;      // which of x and the codes is cheaper to reorder
     typedef typename UintOf<kPer * 2>::type Scales __attribute__((aligned(2)));
     typedef typename UintOf<kPer>::type Zeros __attribute__((aligned(1)));
@@ -163,9 +166,14 @@ __global__ __launch_bounds__(W * 64, OCC) void grouped_kernel(GroupedParams p)
     const int n0 = (int)blockIdx.x * p.rows, n_end = min(n0 + p.rows, p.N);
     const int m_own = 4 * (r % 4 % E) + r / 4;   // row of x at row r of a matrix tile
 
-    // a run of an even number of blocks, so that it begins with a line, unless that leaves waves without any
-    const int blocks = p.K / 128, least = (blocks + W - 1) / W, run = least < 4 ? least : (least + 1) / 2 * 2;
-    const int first = wave * run, end = min(first + run, blocks);
+    // Blocks of 128 K, the last one filled up with zeros (a row shorter than one
+    // comes at the end).  A wave's run begins with a line where rows do; where they
+    // do not, runs are as even as they can be (16 x 4224 -> 9001 in groups of 32:
+    // 12.5 us, with even numbers of blocks 14.0; 1 x 5120 -> 8192: 7.7 and 7.1).
+    const int blocks = p.K < 128 ? 0 : (p.K + 127) / 128, least = blocks / W, more = blocks % W;
+    const int most = least + (more > 0), run = most < 4 ? most : (most + 1) / 2 * 2;
+    const int first = LINES ? wave * run : wave * least + min(wave, more);
+    const int end = LINES ? min(first + run, blocks) : first + least + (wave < more);
     f32x4 acc[MT][NT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
@@ -222,7 +230,7 @@ __global__ __launch_bounds__(W * 64, OCC) void grouped_kernel(GroupedParams p)
     };
 
     if (first < end) {
-        // Rows behind the last one read as zeros; their outputs are computed and not stored.
+        // Rows behind the last one, and what is nowhere, read as zeros; their outputs are computed and not stored.
         const auto codes = __builtin_amdgcn_make_buffer_rsrc((void*)(p.codes + (int64_t)n0 * (p.K / 2)), 0,
                                                              (n_end - n0) * (p.K / 2), 0x20000);
         const auto rows = __builtin_amdgcn_make_buffer_rsrc((void*)p.x, 0, 2 * p.M * p.K, 0x20000);
@@ -239,7 +247,8 @@ __global__ __launch_bounds__(W * 64, OCC) void grouped_kernel(GroupedParams p)
         // With 32 rows an offset is worked out for each load: kept, those of all
         // of them take registers that are not there.
         const auto load_w = [&](int b) {   // blocks b and b + 1
-            const uint32_t at = w_at + (uint32_t)min(b + half, end - 1) * 64u;
+            const uint32_t of = (uint32_t)min(b + half, end - 1) * 64u;
+            const uint32_t at = LINES || of + 16 * (lane % 4) < (uint32_t)(p.K / 2) ? w_at + of : kNowhere;
 #pragma unroll
             for (int i = 0; i < 2 * NT; ++i) {
                 uint32_t row = (uint32_t)(8 * i) * (uint32_t)(p.K / 2);
@@ -248,15 +257,18 @@ __global__ __launch_bounds__(W * 64, OCC) void grouped_kernel(GroupedParams p)
             }
         };
         const auto load_x = [&](u32x4 (&to)[kXLoads], int b) {
+            const uint32_t at = LINES || b * 128 + 8 * (lane % 16) < p.K ? x_at : kNowhere;
 #pragma unroll
             for (int i = 0; i < kXLoads; ++i) {
                 uint32_t row = (uint32_t)(4 * i) * (uint32_t)(2 * p.K) + (uint32_t)b * 256u;
                 if constexpr (MT > 1) asm volatile("" : "+s"(row));
-                to[i] = __builtin_amdgcn_raw_buffer_load_b128(rows, x_at + row, 0, 0);
+                to[i] = __builtin_amdgcn_raw_buffer_load_b128(rows, at + row, 0, 0);
             }
         };
         const auto load_s = [&](uint32_t (&to)[NT][kWords], uint32_t (&to_z)[NT], int b) {
-            const uint32_t at = (uint32_t)min(b + lane % 4, blocks - 1) * kPer;
+            // of the row's last groups where a block has fewer of its own
+            uint32_t at = (uint32_t)min(b + lane % 4, blocks - 1) * kPer;
+            if constexpr (!LINES) at = min(at, (uint32_t)(p.groups - kPer));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const auto v = *(const Scales*)((const uint8_t*)scales + 2 * (s_at[nt] + at));
@@ -340,6 +352,18 @@ __global__ __launch_bounds__(W * 64, OCC) void grouped_kernel(GroupedParams p)
                 if constexpr (ZEROS) z[nt] = next_z[nt];
             }
         }
+        if (!LINES && kPer > 1 && end == blocks && lane % 4 == blocks - 1 - b) {
+            const int before = blocks * kPer - p.groups;   // groups in front of the last block's own
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                uint64_t v = s[nt][0];
+                if constexpr (kPer == 4) v |= (uint64_t)s[nt][1] << 32;
+                v >>= 16 * before;
+                s[nt][0] = (uint32_t)v;
+                if constexpr (kPer == 4) s[nt][1] = (uint32_t)(v >> 32);
+                if constexpr (ZEROS) z[nt] >>= 8 * before;
+            }
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if (b + j < end) {
@@ -356,18 +380,18 @@ __global__ __launch_bounds__(W * 64, OCC) void grouped_kernel(GroupedParams p)
                 __builtin_amdgcn_sched_barrier(0);
             }
     }
-    if (!LINES && wave == W - 1 && p.K % 128 != 0) {   // a row that ends inside a block: zeros behind it
+    if (!LINES && kPer > 1 && wave == W - 1 && p.K < 128) {   // a row shorter than a block: zeros behind it
         u32x4 w[NT], x[MT][4];
         uint32_t s[NT][kWords] = {}, z[NT] = {};
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int64_t n = min(n0 + 16 * nt + r, n_end - 1);
             w[nt] = u32x4{0u, 0u, 0u, 0u};
-            if (blocks * 128 + 32 * q < p.K) w[nt] = *(const u32x4*)(p.codes + n * (p.K / 2) + blocks * 64 + 16 * q);
+            if (32 * q < p.K) w[nt] = *(const u32x4*)(p.codes + n * (p.K / 2) + 16 * q);
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
-                if (blocks * kPer + i < p.groups) {
-                    const int64_t g = n * p.groups + blocks * kPer + i;
+                if (i < p.groups) {
+                    const int64_t g = n * p.groups + i;
                     s[nt][i / 2] |= (uint32_t)((const uint16_t*)p.scales)[g] << (16 * (i % 2));
                     if constexpr (ZEROS) z[nt] |= (uint32_t)p.zeros[g] << (8 * i);
                 }
@@ -377,7 +401,7 @@ __global__ __launch_bounds__(W * 64, OCC) void grouped_kernel(GroupedParams p)
             const int m = 16 * mt + m_own;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int k = blocks * 128 + (kTurn ? 32 * j + 8 * q : 32 * q + 8 * j);
+                const int k = kTurn ? 32 * j + 8 * q : 32 * q + 8 * j;
                 x[mt][j] = u32x4{0u, 0u, 0u, 0u};
                 if (k < p.K) x[mt][j] = *(const u32x4*)((const uint16_t*)p.x + (int64_t)min(m, p.M - 1) * p.K + k);
                 if constexpr (!kInOrder) x[mt][j] = reorder8(x[mt][j]);
