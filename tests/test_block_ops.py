@@ -129,6 +129,13 @@ def test_norm_kinds_and_types(gpu, dtype, vec, norm, post):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,width", [("bf16", 2056), ("bf16", 4096), ("f16", 4091), ("f32", 2048), ("f32", 2045), ("f16", 1035)])
+def test_norm_more_rows_than_units(gpu, dtype, width):
+    check_norm(300, width, dtype, vectors=3, norm="layer", post="rms", seed=width)
+    check_norm(257, width, dtype, vec="f32", norm="rms", seed=width)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("rows", [1, 2, 3, 4, 5, 63, 1537])
 def test_norm_rows_and_per_row_vectors(gpu, rows):
     check_norm(rows, 256, vectors=rows, seed=rows)       # a vector of its own for every row
@@ -360,6 +367,18 @@ def test_rope_strides_and_in_place(gpu, dim, sizes, layout):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["interleaved", "halves"])
+@pytest.mark.parametrize("tokens,hq,hk,dim,sizes,dtype", [
+    (1101, 9, 3, 72, (22, 22, 20), "f16"), (1101, 9, 3, 72, (22, 22, 22), "f16"), (1100, 16, 5, 64, (64,), "bf16"),
+    (2801, 13, 11, 72, (24, 24), "bf16"), (2801, 13, 11, 72, (26, 24), "f16"), (2100, 20, 20, 128, (44, 42, 42), "bf16"),
+    (1701, 7, 3, 256, (256,), "f32"), (2801, 3, 3, 100, (50, 50), "f32")])
+def test_rope_many_tokens(gpu, tokens, hq, hk, dim, sizes, dtype, layout):
+    """A wave takes four or eight items, the last of them partly or of the other tensor."""
+    check_rope(1, tokens, hq, hk, dim, sizes, layout, dtype, norm=True, packed=True, in_place=True, seed=tokens + dim)
+    check_rope(2, (tokens + 1) // 2, hq, hk, dim, sizes, layout, dtype, head_major=True, seed=tokens + dim)
+
+
+@pytest.mark.gpu
 def test_rope_one_tensor_and_identity(gpu):
     freq, axis = B.rope_frequencies((32, 32))
     q = rand((1, 9, 4, 64), 1, torch.bfloat16).cuda()
@@ -541,6 +560,16 @@ def test_grouped_rows(gpu, m):
 def test_grouped_sizes(gpu, n, k, group):
     check_grouped(1, n, k, group, seed=n)
     check_grouped(19, n, k, group, zeros=True, dtype="f16", bias=False, seed=k)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m", [1, 4, 5, 8, 12, 27])
+@pytest.mark.parametrize("n", [300, 5000, 9001, 16000, 16500])
+def test_grouped_tiles(gpu, m, n):
+    """Every count of output tiles a workgroup, with one round of workgroups and two."""
+    check_grouped(m, n, 1280, 32, zeros=True, dtype="f16", seed=n)
+    check_grouped(m, n, 1152, 64, seed=n)
+    check_grouped(m, n, 1408, 128, zeros=n % 2 == 1, bias=False, seed=n)
 
 
 @pytest.mark.gpu
@@ -760,6 +789,43 @@ def test_binding_refusals(gpu):
 
 
 # ---- streams and graphs ------------------------------------------------------------
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits(gpu):
+    far = (1 << 30) + 64   # elements from row to row: the third begins beyond 2^32 bytes
+    buf = torch.empty(2 * far + 1024, dtype=torch.bfloat16, device="cuda")
+
+    def spread(t):
+        v = buf.as_strided(t.shape, (far, *t.stride()[1:]))
+        v.copy_(t)
+        return v
+
+    x = rand((3, 64), 1, torch.bfloat16).cuda()
+    want = B.convrot_residual_norm(x, x)
+    got = B.convrot_residual_norm(spread(x), x, r=spread(x))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    q = rand((3, 1, 2, 64), 2, torch.bfloat16).cuda()
+    pos = torch.arange(3, dtype=torch.int32, device="cuda").view(3, 1, 1)
+    freq, axis = B.rope_frequencies((64,))
+    want = B.convrot_rope(q, None, pos, freq, axis)[0]
+    places = spread(q)
+    assert torch.equal(B.convrot_rope(places, None, pos, freq, axis, q_out=places)[0], want)
+    flip = lambda v: v.transpose(0, 1)   # noqa: E731  tokens as the far dimension
+    places = spread(q)
+    assert torch.equal(flip(B.convrot_rope(flip(places), None, flip(pos), freq, axis, q_out=flip(places))[0]), want)
+    del buf, places, got
+    n, k, last = (1 << 17) + 5, 65536, 5   # codes of more than 2^32 bytes
+    codes = torch.empty((n, k // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.full((n, k // 128), 2.0 ** -7, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator().manual_seed(3)
+    own = torch.randint(0, 256, (last, k // 2), generator=g, dtype=torch.uint8)
+    codes[-last:] = own.cuda()
+    for m in (1, 17):
+        x = torch.randint(-1, 2, (m, k), generator=g).to(torch.bfloat16)   # sums below 2^24
+        y = B.convrot_linear_grouped(x.cuda(), codes, scales, None, None, 128)
+        want = x.double() @ codes_of(own, None, 128).t() * 2.0 ** -7
+        assert torch.equal(y[:, -last:].cpu(), want.to(torch.bfloat16))
 
 
 def block_calls():
