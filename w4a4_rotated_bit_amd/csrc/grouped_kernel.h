@@ -19,10 +19,10 @@
 // and widens its share of the codes, some 60 vector instructions for each 16 x
 // 128 of them beside 8 or 16 matrix instructions: 32 x 16384 -> 16384 takes 44
 // us (143 MB, 3.2 TB/s), 34 with its codes in the cache and 26 for reading alone,
-// and 16 x 4128 -> 9001 with groups of 32 takes 13.3 us: 4.3 for
-// launch, first loads and the joining of the waves, then 1.6 to 1.8 for each block
-// of a wave, bound by the widening (10.8 with rows of 4096, which begin with a
-// line of memory and need four blocks of a wave instead of five).
+// and 16 x 4128 -> 9001 with groups of 32 takes 13.3 us: 4.3 for launch, first
+// loads and the joining of the waves, then 1.6 to 1.8 for each block of a wave,
+// bound by the widening (10.8 with rows of 4096, which begin with a line of memory
+// and give a wave four blocks instead of five).
 #pragma once
 #include "block_ops.h"
 
@@ -130,16 +130,16 @@ __device__ __forceinline__ uint32_t fetch(int from, uint32_t v)
 // its own part of shared memory.  Scales and zero points come for four blocks at
 // a time, lane % 4 the block.  Two blocks of codes are on their way while two
 // are multiplied, of x two blocks or one: more in flight costs registers and
-// time (four blocks of codes: 32 x 16384 -> 16384 49 against 44 us, 16 x 4096 -> 16384
-// 12.9 against 12.0).
+// time (four blocks of codes: 32 x 16384 -> 16384 49 against 44 us, 16 x 4096 ->
+// 16384 12.9 against 12.0).
 //
 // Row m of x sits at row 4 (m % 4) + m / 4 of its matrix tile, so that the
 // first E of the four sums a lane holds are the ones in use for M <= 4 E.
 //
 // LINES: every row of the codes is whole lines of memory, which are then loaded
-// with the hint that they are used once (1 x 4096 -> 12288 8.6 -> 8.0 us, 32 x 16384
-// -> 16384 47.4 -> 44.9); where rows begin inside a line, two loads want it (16 x
-// 4128 -> 9001 14.2 -> 15.2).
+// with the hint that they are used once (1 x 4096 -> 12288 8.6 -> 8.0 us, 32 x
+// 16384 -> 16384 47.4 -> 44.9); where rows begin inside a line, two loads want it
+// (16 x 4128 -> 9001 14.2 -> 15.2).
 // OCC: the waves of a SIMD that the registers have to leave room for.
 template <typename D, int GROUP, bool ZEROS, bool LINES, int MT, int E, int NT, int W, int OCC>
 __global__ __launch_bounds__(W * 64, OCC) void grouped_kernel(GroupedParams p)
