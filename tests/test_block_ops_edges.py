@@ -1,0 +1,77 @@
+"""The operators around the linears of a block where they are easily wrong.
+
+u = 2^-24 is half a step of binary32 relative to the value; an output stored in
+type t adds half a step of t, finfo(t).eps / 2 of it."""
+import pytest
+import torch
+
+from w4a4_rotated_bit_amd import binding as B
+
+U = 2.0 ** -24
+TYPES = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+# additions one after the other in a row's sum: at most 64 elements a thread, 6
+# steps across a wave, 16 waves, and a few roundings of the statistics
+SUM = 64 + 6 + 16 + 10
+
+
+def rand(shape, seed, dtype=torch.float32, std=1.0, mean=0.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * std + mean).to(dtype)
+
+
+def half_step(dtype, value):
+    info = torch.finfo(dtype)
+    return info.eps / 2 * value.abs() + info.smallest_normal * info.eps / 2
+
+
+# ---- LayerNorm far from zero -----------------------------------------------------
+
+
+def layer_norm(v, eps):
+    """LayerNorm of the exact rows v in binary64, and the error of a binary32
+    evaluation in which a mean far from zero costs nothing: a first mean is off
+    by no more than e = (SUM + 2) u mean|v|; what is left of the row is rounded
+    once, has a mean of its own no larger than e that is found to SUM + 4 of its
+    roundings, and that mean leaves both the row and the mean square.  The mean
+    square is then off by SUM + 8 roundings of itself and of e^2."""
+    d = v - v.mean(-1, keepdim=True)
+    e = (SUM + 2) * U * v.abs().mean(-1, keepdim=True)
+    size = d.abs().mean(-1, keepdim=True) + e
+    var = (d * d).mean(-1, keepdim=True) + eps
+    rstd = 1 / torch.sqrt(var)
+    off = (2 * U * (d.abs() + e) + (SUM + 4) * U * size) * rstd
+    # the root halves what the mean square is off by, through its own sum and
+    # through the square of the second mean
+    square = ((SUM + 8) * U * (1 + e * e / var) + 2 * (SUM + 4) * U * size * e / var + ((SUM + 4) * U * size) ** 2 / var)
+    return d * rstd, off + (d * rstd).abs() * (square + 4 * U)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("width", [3, 65, 255, 768, 1000, 1035, 2048, 4091, 8200, 16383])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_layer_norm_of_rows_of_one_value_is_zero(gpu, dtype, width):
+    """(v - mean) is 0 whatever the value is and however its sum rounds; the norm's
+    factor is 1 / sqrt(eps) = 1000 at most."""
+    values = torch.tensor([20.0, 100.0, 1000.0, -1000.0, 7.7, 333.3, 60000.0]).to(TYPES[dtype])
+    x = values.unsqueeze(1).expand(-1, width).contiguous().cuda()
+    _, off = layer_norm(x.cpu().double(), 1e-6)
+    _, h = B.convrot_residual_norm(x, norm="layer", want_r=False)
+    off = off + half_step(TYPES[dtype], off)
+    assert (h.cpu().double().abs() <= off).all(), h[:, 0]
+    r, _ = B.convrot_residual_norm(torch.zeros_like(x), x, norm=None, post_norm="layer", want_h=False)
+    assert (r.cpu().double().abs() <= off).all(), r[:, 0]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("width", [255, 1000, 1024, 1035, 4091, 4096, 16383])
+@pytest.mark.parametrize("mean,std", [(1000.0, 1.0), (-300.0, 0.1), (1e5, 3.0), (5.0, 1e-3), (0.0, 1.0)])
+def test_layer_norm_far_from_zero(gpu, width, mean, std):
+    x = rand((5, width), width, torch.float32, std, mean)
+    want, off = layer_norm(x.double(), 1e-6)
+    off = off + want.abs() * U
+    for rows in (5, 300):   # fewer and more rows than units: other workgroups
+        c = x.repeat(rows // 5, 1).cuda()
+        _, h = B.convrot_residual_norm(c, norm="layer", want_r=False)
+        r, _ = B.convrot_residual_norm(torch.zeros_like(c), c, norm=None, post_norm="layer", want_h=False)
+        for got in (h, r):
+            assert ((got.cpu().double() - want.repeat(rows // 5, 1)).abs() <= off.repeat(rows // 5, 1)).all()

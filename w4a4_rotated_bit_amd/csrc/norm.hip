@@ -7,18 +7,21 @@
 //
 // One row is held in the registers of T threads from its first load to its
 // last store, so each of x, y, r and h crosses memory once; the statistics are
-// sums of binary32 in registers (LayerNorm: the mean first, then the squared
-// deviations, so that a large mean costs nothing), and N works on r as it is
-// before its rounding to the storage type.
+// sums of binary32 in registers, and N works on r as it is before its rounding
+// to the storage type.  LayerNorm's mean is found twice: a first one, off by the
+// roundings of a sum of the row's full size, is taken away from the row, and the
+// mean of what is left, found in the same pass as its squares, is taken out of
+// both.  Its roundings are those of the deviations, so a mean far from zero costs
+// nothing (in rows of one value, 1000, the first mean alone left up to 0.06 in h).
 //
 // Bound by memory: 32768 rows of 4096 bf16 with both norms, every vector and
-// both outputs move 1.07 GB in 202 us (5.3 TB/s; a copy of that size reaches
+// both outputs move 1.07 GB in 194 us (5.5 TB/s; a copy of that size reaches
 // 5.0 TB/s, one of 256 MB 5.5), 1536 rows 50 MB in 10.2 us (4.9 TB/s).  Rows are
 // loaded and stored with the hint that they are used once, without it 215 and
 // 12.4 us; not where a chunk does not divide the width, whose chunks share lines
 // (999 rows of 1035 7.0 against 6.6 us).  Short inputs are
 // bound by latency: one row of 4096 takes 2.4 us where an empty kernel takes
-// 1.9, and 999 rows of 1035 f16, two norms, 6.5 us: four sums across the
+// 1.9, and 999 rows of 1035 f16, two norms, 6.8 us: four sums across the
 // workgroup one after the other, and chunks that cross lines of memory.
 //
 // One row a workgroup, and nothing else kept from row to row: workgroups that
@@ -40,21 +43,27 @@ struct NormParams {
     bool in_place;   // r or h is x or y
 };
 
-// Sum over the T threads of a row; every sum of a kernel has slots of its own,
-// so one barrier is enough.
-template <int T>
-__device__ __forceinline__ float row_sum(float v, float* slot)
+// Sums of C values over the T threads of a row; every exchange of a kernel has
+// slots of its own, so one barrier is enough.
+template <int T, int C>
+__device__ __forceinline__ void row_sums(float (&v)[C], float* slot)
 {
-    v = lane_sum<64>(v);
+#pragma unroll
+    for (int c = 0; c < C; ++c) v[c] = lane_sum<64>(v[c]);
     if constexpr (T > 64) {
         const int wave = threadIdx.x / 64;
-        if (threadIdx.x % 64 == 0) slot[wave] = v;
-        __syncthreads();
-        v = 0.f;
+        if (threadIdx.x % 64 == 0) {
 #pragma unroll
-        for (int w = 0; w < T / 64; ++w) v += slot[w];
+            for (int c = 0; c < C; ++c) slot[C * wave + c] = v[c];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            v[c] = 0.f;
+#pragma unroll
+            for (int w = 0; w < T / 64; ++w) v[c] += slot[C * w + c];
+        }
     }
-    return v;
 }
 
 // D: type of the rows, E: of the vectors.  T threads a row, NV chunks of V
@@ -71,8 +80,8 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void residual_norm_kernel(NormPa
     static_assert(T == 64 || kRows == 1, "several rows share a workgroup only where a row is one wave");
     typedef typename VecOf<D, V>::type Chunk;
     typedef typename VecOf<E, V>::type Vector;
-    constexpr int kSlots = T > 64 ? 4 * (T / 64) : 1;
-    __shared__ float slots[kSlots];
+    constexpr int kSlots = T > 64 ? 3 * (T / 64) : 0;   // of one norm: a sum, then a pair
+    __shared__ float slots[T > 64 ? 2 * kSlots : 1];
     const int t = threadIdx.x % T;
     const int64_t row = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kRows + threadIdx.x / T;
 
@@ -102,16 +111,31 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void residual_norm_kernel(NormPa
     };
     // v -> (v - mean) rstd, with the sums of the row in `slots`
     const auto normalise = [&](float (&v)[NV][V], int kind, float* slots) {
-        float mean = 0.f, q = 0.f;
+        const auto own = [&](int j, int i) { return in[j] && (!TAIL || i >= skip[j]) ? v[j][i] : 0.f; };
         if (kind == CONVROT_NORM_LAYER) {
-            float sum = 0.f;
-            all([&](int j, int i) { sum += in[j] && (!TAIL || i >= skip[j]) ? v[j][i] : 0.f; });
-            mean = row_sum<T>(sum, slots) * p.inv_width;
+            float first[1] = {0.f}, rest[2] = {0.f, 0.f};
+            all([&](int j, int i) { first[0] += own(j, i); });
+            row_sums<T>(first, slots);
+            float mean = first[0] * p.inv_width;
+            asm volatile("" : "+v"(mean));   // rounded, for every element: some subtractions would take the product in
             all([&](int j, int i) { v[j][i] -= mean; });
+            all([&](int j, int i) {
+                const float d = own(j, i);
+                rest[0] += d;
+                rest[1] = fmaf(d, d, rest[1]);
+            });
+            row_sums<T>(rest, slots + T / 64);
+            const float left = rest[0] * p.inv_width;
+            const float var = fmaxf(fmaf(-left, left, rest[1] * p.inv_width), 0.f);
+            const float rstd = 1.f / sqrtf(var + p.eps);
+            all([&](int j, int i) { v[j][i] = fmaf(v[j][i], rstd, -left * rstd); });
+        } else {
+            float q[1] = {0.f};
+            all([&](int j, int i) { q[0] = fmaf(own(j, i), own(j, i), q[0]); });
+            row_sums<T>(q, slots);
+            const float rstd = 1.f / sqrtf(q[0] * p.inv_width + p.eps);
+            all([&](int j, int i) { v[j][i] *= rstd; });
         }
-        all([&](int j, int i) { q = in[j] && (!TAIL || i >= skip[j]) ? fmaf(v[j][i], v[j][i], q) : q; });
-        const float rstd = 1.f / sqrtf(row_sum<T>(q, slots + T / 64) * p.inv_width + p.eps);
-        all([&](int j, int i) { v[j][i] *= rstd; });
     };
 
     if (row >= p.rows) return;   // whole waves; a workgroup with barriers has one row
@@ -173,7 +197,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void residual_norm_kernel(NormPa
     };
     if (p.r) store((D*)p.r + row * p.r_stride);
     if (!p.h) return;
-    if (p.norm != CONVROT_NORM_NONE) normalise(r, p.norm, slots + (T > 64 ? 2 * (T / 64) : 0));
+    if (p.norm != CONVROT_NORM_NONE) normalise(r, p.norm, slots + kSlots);
     if (p.weight) {
         if (!EARLY) load_vector(weight, p.weight);
         all([&](int j, int i) { r[j][i] *= (float)weight[j][i]; });
