@@ -75,3 +75,40 @@ def test_layer_norm_far_from_zero(gpu, width, mean, std):
         r, _ = B.convrot_residual_norm(torch.zeros_like(c), c, norm=None, post_norm="layer", want_h=False)
         for got in (h, r):
             assert ((got.cpu().double() - want.repeat(rows // 5, 1)).abs() <= off.repeat(rows // 5, 1)).all()
+
+
+# ---- the binding's own checks, without a GPU --------------------------------------
+
+
+@pytest.fixture
+def host_calls(monkeypatch):
+    """The binding on host tensors: its checks run, the C call is recorded instead of made."""
+    B._use_torch()
+    calls = []
+    monkeypatch.setattr(B, "_on_gpu", lambda t, name: -1)
+    monkeypatch.setattr(B, "_check_tensor", lambda t, name, device: None)
+    monkeypatch.setattr(B, "_launch", lambda device, stream, call: call(0))
+    monkeypatch.setattr(B, "_call", lambda name, *args: calls.append((name, args)))
+    return calls
+
+
+@pytest.mark.parametrize("x,v,rows_per_vec", [
+    ((8,), (8,), 1), ((3, 8), (8,), 1), ((3, 8), (1, 1, 8), 1), ((6, 8), (2, 8), 3), ((6, 8), (3, 1, 8), 2), ((6, 8), (6, 8), 1),
+    ((2, 3, 8), (2, 8), 3), ((2, 3, 8), (2, 1, 8), 3), ((2, 3, 8), (2, 3, 8), 1), ((2, 3, 8), (2, 3, 1, 8), 1), ((8, 8), (8, 8), 1),
+    # more leading dimensions than x has, reaching into its width
+    ((8,), (8, 8), None), ((3, 8), (3, 8, 8), None), ((2, 3, 8), (2, 3, 8, 8), None), ((8, 8), (8, 8, 8), None),
+    ((8,), (8, 1, 8), None), ((1, 8), (8, 8), None), ((3, 8), (6, 8), None), ((3, 8), (2, 8), None), ((2, 3, 8), (3, 8), None),
+    ((2, 3, 8), (6, 8), None), ((2, 3, 8), (2, 2, 8), None), ((3, 8), (0, 8), None)])
+@pytest.mark.parametrize("name", ["gate", "scale", "shift"])
+def test_norm_vectors_have_the_leading_dimensions_of_x(host_calls, name, x, v, rows_per_vec):
+    x, v = torch.zeros(x), torch.zeros(v)
+    if rows_per_vec is None:
+        with pytest.raises(ValueError, match=name):
+            B.convrot_residual_norm(x, x, **{name: v})
+        assert not host_calls
+        return
+    B.convrot_residual_norm(x, x, **{name: v})
+    fields = B.NORM_ARGS.unpack(host_calls[0][1][0])
+    assert fields[18] == rows_per_vec
+    step = fields[{"gate": 15, "scale": 16, "shift": 17}[name]]
+    assert step == (8 if v.numel() > 8 else 0)

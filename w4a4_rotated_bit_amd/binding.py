@@ -677,7 +677,7 @@ def convrot_residual_norm(x, y=None, *, gate=None, scale=None, shift=None, weigh
                 lead = lead[:-1]
             if "weight" in name:
                 raise ValueError(f"{name} must be one vector of {width} values")
-            if rows % n if len(shape) == 2 and len(lead) == 1 and n else lead != shape[:len(lead)]:
+            if rows % n if len(shape) == 2 and len(lead) == 1 and n else lead != shape[:-1][:len(lead)]:
                 raise ValueError(f"{name} of shape {tuple(v.shape)} does not fit x of shape {tuple(shape)}")
             if rows:
                 if per not in (0, rows // n):
