@@ -112,3 +112,29 @@ def test_norm_vectors_have_the_leading_dimensions_of_x(host_calls, name, x, v, r
     assert fields[18] == rows_per_vec
     step = fields[{"gate": 15, "scale": 16, "shift": 17}[name]]
     assert step == (8 if v.numel() > 8 else 0)
+
+
+def test_tensors_with_a_tangent_are_refused(host_calls):
+    """A tangent of forward differentiation would be lost as a gradient would be."""
+    import torch.autograd.forward_ad as fwd
+    x, q, pos = torch.zeros((2, 8)), torch.zeros((1, 2, 1, 8)), torch.zeros((1, 2, 1))
+    X, codes, scales, bias = (torch.zeros(s, dtype=t) for s, t in (
+        ((2, 32), torch.bfloat16), ((4, 16), torch.uint8), ((4, 1), torch.bfloat16), ((4,), torch.bfloat16)))
+    freq, axis = B.rope_frequencies((8,))
+    norm = dict(x=x, y=x, gate=x, scale=x, shift=x, weight=x[0], post_weight=x[0], post_norm="rms", r=torch.empty_like(x),
+                h=torch.empty_like(x))
+    rope = dict(q=q, k=q, positions=pos, freq=freq, axis=axis, qk_norm=True, q_weight=q[0, 0, 0], k_weight=q[0, 0, 0],
+                q_out=torch.empty_like(q), k_out=torch.empty_like(q))
+    grouped = dict(X=X, codes=codes, scales=scales, zeros=None, bias=bias, group=32, Y=torch.empty((2, 4), dtype=X.dtype))
+    for call, args, dual in ((B.convrot_residual_norm, norm, [k for k in norm if k != "post_norm"]),
+                             (B.convrot_rope, rope, ["q", "k", "positions", "q_weight", "k_weight", "q_out", "k_out"]),
+                             (B.convrot_linear_grouped, grouped, ["X", "scales", "bias", "Y"])):
+        with fwd.dual_level():
+            call(**args)     # none of them has one
+            made = len(host_calls)
+            for key in dual:
+                t = args[key]
+                with pytest.raises(RuntimeError, match="tangent"):
+                    call(**{**args, key: fwd.make_dual(t.clone(), torch.ones_like(t))})
+            assert len(host_calls) == made
+        call(**args)

@@ -537,13 +537,15 @@ _NORMS = {None: CONVROT_NORM_NONE, "layer": CONVROT_NORM_LAYER, "rms": CONVROT_N
 _LAYOUTS = {"interleaved": CONVROT_ROPE_INTERLEAVED, "halves": CONVROT_ROPE_HALVES}
 _GROUPS = (32, 64, 128)
 _torch = None   # the module, its types' codes and its current device and stream, from the first call on
+_forward = None   # its forward differentiation
 _types = {}
 _current_device = _raw_stream = None
 
 
 def _use_torch():
-    global _torch, _current_device, _raw_stream
+    global _torch, _forward, _current_device, _raw_stream
     import torch
+    import torch.autograd.forward_ad as _forward
     _types.update({torch.bfloat16: CONVROT_BF16, torch.float16: CONVROT_F16, torch.float32: CONVROT_F32})
     # The handles themselves: torch.cuda.current_stream builds an object around
     # one, which takes longer than a launch.
@@ -578,6 +580,17 @@ def _check_tensor(t, name, device):
         raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
     if t.requires_grad and _torch.is_grad_enabled():
         raise RuntimeError(f"{name} requires a gradient, and this operator has none: call it under torch.no_grad()")
+
+
+def _check_tangents(*tensors):
+    """No tensor of this call carries a tangent of forward differentiation, which
+    ``requires_grad`` does not tell."""
+    if getattr(_forward, "_current_level", 0) < 0:   # outside of any dual level
+        return
+    for t in tensors:
+        if isinstance(t, _torch.Tensor) and _forward.unpack_dual(t).tangent is not None:
+            raise RuntimeError("a tensor of this call has a tangent, and this operator has no derivative: "
+                               "call it on the primal of torch.autograd.forward_ad.unpack_dual")
 
 
 def _type_of(t, name):
@@ -643,6 +656,7 @@ def convrot_residual_norm(x, y=None, *, gate=None, scale=None, shift=None, weigh
     or h given is written (x or y itself may be), and one not wanted is None."""
     device = _on_gpu(x, "x")
     _check_tensor(x, "x", device)
+    _check_tangents(x, y, gate, scale, shift, weight, post_weight, r, h)
     shape, dtype = x.shape, x.dtype
     width = shape[-1] if shape else 0
     code = _type_of(x, "x")
@@ -768,6 +782,7 @@ def convrot_rope(q, k, positions, freq, axis, *, layout: str = "interleaved", qk
     transposed views ([batch, heads, tokens, head_dim] storage)."""
     device = _on_gpu(q, "q")
     _check_tensor(q, "q", device)
+    _check_tangents(q, k, positions, q_weight, k_weight, q_out, k_out)
     shape, dtype = q.shape, q.dtype
     if len(shape) != 4:
         raise ValueError(f"q must be [batch, tokens, heads, head_dim], got {tuple(shape)}")
@@ -853,6 +868,7 @@ def convrot_linear_grouped(X, codes, scales, zeros, bias, group: int, Y=None, st
     packed-K); scales: [N, K/group] of X's type; zeros: uint8 [N, K/group] with
     unsigned codes, None with two's complement ones; bias: [N] or None."""
     device = _on_gpu(X, "X")
+    _check_tangents(X, codes, scales, zeros, bias, Y)
     dtype = X.dtype
     code = _type_of(X, "X")
     if code == CONVROT_F32:
