@@ -138,3 +138,26 @@ def test_tensors_with_a_tangent_are_refused(host_calls):
                     call(**{**args, key: fwd.make_dual(t.clone(), torch.ones_like(t))})
             assert len(host_calls) == made
         call(**args)
+
+
+def test_given_outputs_count_as_written(host_calls):
+    """Autograd tells a saved tensor that was written since by its version."""
+    x, q, pos = torch.zeros((2, 8)), torch.zeros((1, 2, 1, 8)), torch.zeros((1, 2, 1))
+    X, codes, scales = (torch.zeros(s, dtype=t) for s, t in (
+        ((2, 32), torch.bfloat16), ((4, 16), torch.uint8), ((4, 1), torch.bfloat16)))
+    freq, axis = B.rope_frequencies((8,))
+    r, h, out, y = x.clone(), x.clone(), q.clone(), X.new_zeros((2, 4))
+    B.convrot_residual_norm(x, r=r, h=h)
+    B.convrot_rope(q, q, pos, freq, axis, q_out=q, k_out=out)
+    B.convrot_linear_grouped(X, codes, scales, None, None, 32, Y=y)
+    assert [t._version for t in (r, h, q, out, y)] == [1] * 5
+    assert [t._version for t in (x, pos, X, codes, scales)] == [0] * 5
+    with torch.inference_mode():
+        t = torch.zeros((2, 8))
+        B.convrot_residual_norm(t, r=t)
+    weight = torch.ones((2, 8), requires_grad=True)
+    z = (weight * x).sum()      # saves x
+    with torch.no_grad():
+        B.convrot_residual_norm(x, r=x)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        z.backward()

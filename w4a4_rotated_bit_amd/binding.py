@@ -593,6 +593,13 @@ def _check_tangents(*tensors):
                                "call it on the primal of torch.autograd.forward_ad.unpack_dual")
 
 
+def _written(*tensors):
+    """Outputs that the caller gave: autograd is told that they changed."""
+    for t in tensors:
+        if t is not None:
+            _torch.autograd.graph.increment_version(t)
+
+
 def _type_of(t, name):
     code = _types.get(t.dtype)
     if code is None:
@@ -719,6 +726,7 @@ def convrot_residual_norm(x, y=None, *, gate=None, scale=None, shift=None, weigh
             x.data_ptr(), y_ptr, gate_ptr, scale_ptr, shift_ptr, w_ptr, post_ptr, r_ptr, h_ptr, rows, width, x_stride,
             y_stride, r_stride, h_stride, gate_step, scale_step, shift_step, per or 1, residual_scale, eps, code,
             vec_code or code, *norms), raw)
+        _written(r, h)
         return r_out, h_out
 
     return _launch(device, stream, call)
@@ -829,6 +837,7 @@ def convrot_rope(q, k, positions, freq, axis, *, layout: str = "interleaved", qk
             pos_strides[0] if pos_shape[0] > 1 else 0, pos_strides[1], pos_code, pos_shape[2], freq.shape[0],
             _address(freq), _address(axis), order, CONVROT_NORM_RMS if qk_norm else CONVROT_NORM_NONE, code,
             eps), raw)
+        _written(q_out, k_out)
         return outs[0], outs[1]
 
     return _launch(device, stream, call)
@@ -899,6 +908,7 @@ def convrot_linear_grouped(X, codes, scales, zeros, bias, group: int, Y=None, st
         y_ptr = y.data_ptr() if Y is None else place(Y, "Y", dtype, M, N)
         _call("convrot_linear_grouped",
               GROUPED_ARGS.pack(x_ptr, codes_ptr, scales_ptr, zeros_ptr, bias_ptr, y_ptr, M, N, K, group, code), raw)
+        _written(Y)
         return y
 
     return _launch(device, stream, call)
