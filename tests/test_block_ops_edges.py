@@ -87,7 +87,7 @@ def host_calls(monkeypatch):
     calls = []
     monkeypatch.setattr(B, "_on_gpu", lambda t, name: -1)
     monkeypatch.setattr(B, "_check_tensor", lambda t, name, device: None)
-    monkeypatch.setattr(B, "_launch", lambda device, stream, call: call(0))
+    monkeypatch.setattr(B, "_launch", lambda device, stream, call, tensors: call(0))
     monkeypatch.setattr(B, "_call", lambda name, *args: calls.append((name, args)))
     return calls
 
@@ -161,3 +161,56 @@ def test_given_outputs_count_as_written(host_calls):
         B.convrot_residual_norm(x, r=x)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         z.backward()
+
+
+def test_tensors_of_a_call_on_another_stream_are_recorded_there(monkeypatch):
+    """Memory that is freed while the stream still reads it must not be given out again."""
+    from contextlib import nullcontext
+    from types import SimpleNamespace
+    B._use_torch()
+    monkeypatch.setattr(B, "_on_gpu", lambda t, name: 0)
+    monkeypatch.setattr(B, "_check_tensor", lambda t, name, device: None)
+    monkeypatch.setattr(B, "_call", lambda name, *args: None)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: nullcontext())
+    seen = []
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: seen.append((t.data_ptr(), s)))
+    side = SimpleNamespace(device=SimpleNamespace(index=0), cuda_stream=7)
+    x, y, w, q, pos = torch.zeros((2, 8)), torch.zeros((2, 8)), torch.zeros(8), torch.zeros((1, 2, 1, 8)), torch.zeros((1, 2, 1))
+    X, codes, scales, zeros, bias = (torch.zeros(s, dtype=t) for s, t in (
+        ((2, 32), torch.bfloat16), ((4, 16), torch.uint8), ((4, 1), torch.bfloat16), ((4, 1), torch.uint8), ((4,), torch.bfloat16)))
+    freq, axis = B.rope_frequencies((8,))
+    r, out, Y = x.clone(), q.clone(), X.new_zeros((2, 4))
+    mods = dict(gate=w.clone(), scale=w.clone(), shift=w.clone(), weight=w.clone(), post_weight=w.clone())
+    k, qw = q.clone(), w.clone()
+    for call, own in (
+            (lambda s: B.convrot_residual_norm(x, y, post_norm="rms", r=r, stream=s, **mods), (x, y, r, *mods.values())),
+            (lambda s: B.convrot_rope(q, k, pos, freq, axis, qk_norm=True, q_weight=qw, k_weight=w, q_out=out, stream=s),
+             (q, k, pos, qw, w, out)),
+            (lambda s: B.convrot_linear_grouped(X, codes, scales, zeros, bias, 32, Y=Y, stream=s),
+             (X, codes, scales, zeros, bias, Y)),
+            (lambda s: B.convrot_quantize_weight_grouped(X, 32, stream=s), (X,))):
+        seen.clear()
+        call(side)
+        assert {at for at, _ in seen} == {t.data_ptr() for t in own} and all(s is side for _, s in seen)
+
+
+@pytest.mark.gpu
+def test_inputs_freed_while_another_stream_reads_them(gpu):
+    side = torch.cuda.Stream()
+    x = rand((64, 4096), 1, torch.bfloat16).cuda()
+    want = B.convrot_residual_norm(x, x)
+    torch.full_like(x, 7.0)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)   # the call's kernel starts after what follows here
+    got = B.convrot_residual_norm(x, x, stream=side)
+    at = x.data_ptr()
+    del x
+    others = [torch.empty((64, 4096), dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    assert side.query() or all(t.data_ptr() != at for t in others)
+    for t in others:
+        t.fill_(7.0)
+    side.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)

@@ -607,9 +607,12 @@ def _type_of(t, name):
     return code
 
 
-def _launch(device, stream, call):
+def _launch(device, stream, call, tensors):
     """call(raw stream) with the device current, and with ``stream`` (or the
-    device's current stream) the one that its allocations belong to."""
+    device's current stream) the one that its allocations belong to.  The
+    memory of the call's own ``tensors`` is kept until a ``stream`` given has run
+    it, whenever they are freed; that the stream waits for what makes them, and
+    others for its outputs, is the caller's to order."""
     if stream is None:
         if _current_device() == device:
             return call(_raw_stream(device))
@@ -618,7 +621,11 @@ def _launch(device, stream, call):
     if stream.device.index != device:
         raise ValueError(f"stream is on {stream.device}, the tensors are on cuda:{device}")
     with _torch.cuda.stream(stream):
-        return call(stream.cuda_stream)
+        out = call(stream.cuda_stream)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+    return out
 
 
 def _rows(t, name, width):
@@ -660,7 +667,9 @@ def convrot_residual_norm(x, y=None, *, gate=None, scale=None, shift=None, weigh
     or the first of them (one vector a batch entry; ones may follow); for a
     matrix x also [V, width], one vector for every rows / V rows.  weight,
     post_weight: [width], of the vectors' type.  Returns (r, h) of x's shape; r
-    or h given is written (x or y itself may be), and one not wanted is None."""
+    or h given is written (x or y itself may be), and one not wanted is None.
+    ``stream``: where to run, if not on the current stream; it has to wait for what
+    makes the inputs, and their memory is kept until it is done."""
     device = _on_gpu(x, "x")
     _check_tensor(x, "x", device)
     _check_tangents(x, y, gate, scale, shift, weight, post_weight, r, h)
@@ -729,7 +738,7 @@ def convrot_residual_norm(x, y=None, *, gate=None, scale=None, shift=None, weigh
         _written(r, h)
         return r_out, h_out
 
-    return _launch(device, stream, call)
+    return _launch(device, stream, call, (x, y, gate, scale, shift, weight, post_weight, r, h))
 
 
 def rope_frequencies(sizes, theta: float = 10000.0, shared: bool = False):
@@ -787,7 +796,8 @@ def convrot_rope(q, k, positions, freq, axis, *, layout: str = "interleaved", qk
     host arrays, one value a pair (``rope_frequencies``).  qk_norm: divide each
     head by its root mean square first, times q_weight / k_weight [head_dim].
     Returns (q_out, k_out); given ones are written and may be q, k themselves or
-    transposed views ([batch, heads, tokens, head_dim] storage)."""
+    transposed views ([batch, heads, tokens, head_dim] storage).  ``stream``: as in
+    ``convrot_residual_norm``."""
     device = _on_gpu(q, "q")
     _check_tensor(q, "q", device)
     _check_tangents(q, k, positions, q_weight, k_weight, q_out, k_out)
@@ -840,7 +850,7 @@ def convrot_rope(q, k, positions, freq, axis, *, layout: str = "interleaved", qk
         _written(q_out, k_out)
         return outs[0], outs[1]
 
-    return _launch(device, stream, call)
+    return _launch(device, stream, call, (q, k, positions, q_weight, k_weight, q_out, k_out))
 
 
 def _check_group(group, K):
@@ -850,7 +860,8 @@ def _check_group(group, K):
 
 def convrot_quantize_weight_grouped(W, group: int, asymmetric: bool = False, stream=None):
     """W: bf16 or f16 [N, K] -> (codes uint8 [N, K/2], scales [N, K/group] of W's
-    type, zeros uint8 [N, K/group], or None unless ``asymmetric``)."""
+    type, zeros uint8 [N, K/group], or None unless ``asymmetric``).  ``stream``:
+    as in ``convrot_residual_norm``."""
     device = _on_gpu(W, "W")
     if W.dim() != 2 or not W.is_contiguous():
         raise ValueError("W must be a dense [N, K] tensor")
@@ -868,14 +879,15 @@ def convrot_quantize_weight_grouped(W, group: int, asymmetric: bool = False, str
               scales.data_ptr(), None if zeros is None else zeros.data_ptr(), raw)
         return codes, scales, zeros
 
-    return _launch(device, stream, call)
+    return _launch(device, stream, call, (W,))
 
 
 def convrot_linear_grouped(X, codes, scales, zeros, bias, group: int, Y=None, stream=None):
     """Y = X W^T + bias, W = scales * (codes - zeros) in groups of ``group``
     channels.  X: bf16 or f16 [M, K], M <= 32; codes: uint8 [N, K/2] (N x
     packed-K); scales: [N, K/group] of X's type; zeros: uint8 [N, K/group] with
-    unsigned codes, None with two's complement ones; bias: [N] or None."""
+    unsigned codes, None with two's complement ones; bias: [N] or None.
+    ``stream``: as in ``convrot_residual_norm``."""
     device = _on_gpu(X, "X")
     _check_tangents(X, codes, scales, zeros, bias, Y)
     dtype = X.dtype
@@ -911,4 +923,4 @@ def convrot_linear_grouped(X, codes, scales, zeros, bias, group: int, Y=None, st
         _written(Y)
         return y
 
-    return _launch(device, stream, call)
+    return _launch(device, stream, call, (X, codes, scales, zeros, bias, Y))
