@@ -214,3 +214,17 @@ def test_inputs_freed_while_another_stream_reads_them(gpu):
     side.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+# ---- sources ------------------------------------------------------------------------
+
+
+def test_lanes_pass_values_on_behind_a_fence():
+    """A wave barrier alone orders nothing for the compiler's memory accesses."""
+    from pathlib import Path
+    csrc = Path(B.__file__).parent / "csrc"
+    for name in ("norm.hip", "rope.hip", "grouped.hip", "grouped_kernel.h"):
+        assert "__builtin_amdgcn_wave_barrier" not in (csrc / name).read_text(), name
+    body = (csrc / "block_ops.h").read_text().split("void wave_exchange()")[1].split("}")[0]
+    order = [body.index(s) for s in ("__ATOMIC_RELEASE", "__builtin_amdgcn_wave_barrier", "__ATOMIC_ACQUIRE")]
+    assert order == sorted(order)

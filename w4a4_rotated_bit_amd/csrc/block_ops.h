@@ -76,6 +76,17 @@ __device__ __forceinline__ void store_once(T* p, typename VecOf<T, V>::type v)
     __builtin_nontemporal_store((Any)v, (Any*)p);
 }
 
+// Where lanes of a wave pass values on through shared memory: what they wrote
+// before it is what they read after it, and no write behind it comes before a
+// read in front of it.  A wave's accesses to shared memory happen in their
+// order, so this is no instruction, only the order that the compiler has to keep.
+__device__ __forceinline__ void wave_exchange()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 // v of another lane of the same 16, by a lane permutation of the vector unit
 // (a shuffle through shared memory takes some ten times as long).
 template <int CTRL>

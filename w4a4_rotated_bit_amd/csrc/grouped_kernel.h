@@ -290,12 +290,12 @@ __global__ __launch_bounds__(W * 64, OCC) void grouped_kernel(GroupedParams p)
                 const int m = 4 * i + lane / 16;
                 part_x[16 * m + ((lane % 16) ^ (m % 16))] = kInOrder ? from[i] : reorder8(from[i]);
             }
-            __builtin_amdgcn_wave_barrier();
+            wave_exchange();
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) to[mt][i] = part_x[16 * (16 * mt + m_own) + ((kTurn ? 4 * i + q : 4 * q + i) ^ m_own)];
-            __builtin_amdgcn_wave_barrier();
+            wave_exchange();
         };
         const auto put_w = [&]() {
 #pragma unroll
@@ -303,12 +303,12 @@ __global__ __launch_bounds__(W * 64, OCC) void grouped_kernel(GroupedParams p)
                 const int row = 8 * (i % 2) + lane / 8;
                 part_w[64 * NT * half + 64 * (i / 2) + 4 * (row ^ half) + (lane % 4 ^ row / 4)] = w[i];
             }
-            __builtin_amdgcn_wave_barrier();
+            wave_exchange();
         };
         const auto take_w = [&](u32x4 (&to)[NT], int h) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) to[nt] = part_w[64 * NT * h + 64 * nt + 4 * (r ^ h) + (q ^ r / 4)];
-            __builtin_amdgcn_wave_barrier();
+            wave_exchange();
         };
         const auto take_s = [&](uint32_t (&so)[NT][kWords], uint32_t (&zo)[NT], int j) {
 #pragma unroll

@@ -129,7 +129,7 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p)
 #pragma unroll
     for (int j = 0; j < kPairs; ++j)
         if (lane + 64 * j < p.pairs) cs[lane + 64 * j] = turned_by(turns[j]);
-    __builtin_amdgcn_wave_barrier();
+    wave_exchange();
 
     // the lane's part of the angles, the other lane of its pairs, and its weights there
     const int half = p.pairs / V;
@@ -158,14 +158,14 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p)
         } else {
             D* const row = rows[wave] + g * p.dim;
             if (in) store_chunk<D, V>(row + at, v);
-            __builtin_amdgcn_wave_barrier();
+            wave_exchange();
             Chunk o;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int e = at + i;
                 o[i] = row[in && e < 2 * p.pairs ? (e < p.pairs ? e + p.pairs : e - p.pairs) : 0];
             }
-            __builtin_amdgcn_wave_barrier();
+            wave_exchange();
             return o;
         }
     };
