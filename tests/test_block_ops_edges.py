@@ -77,6 +77,30 @@ def test_layer_norm_far_from_zero(gpu, width, mean, std):
             assert ((got.cpu().double() - want.repeat(rows // 5, 1)).abs() <= off.repeat(rows // 5, 1)).all()
 
 
+# ---- the quantizer at the end of the range ----------------------------------------
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("asymmetric", [False, True])
+def test_quantizer_takes_the_largest_finite_weights(gpu, dtype, asymmetric):
+    """hi - lo may lie beyond binary32 where both are finite."""
+    big = torch.finfo(TYPES[dtype]).max
+    w = torch.zeros((2, 32), dtype=TYPES[dtype])
+    w[0, :4] = torch.tensor([big, -big, big / 2, 1.0])
+    w[1, :2] = torch.tensor([-big, big / 8])
+    codes, scales, zeros = (None if t is None else t.cpu() for t in B.convrot_quantize_weight_grouped(w.cuda(), 32, asymmetric))
+    v = w.double()
+    lo, hi = v.amin(-1, keepdim=True).clamp(max=0), v.amax(-1, keepdim=True).clamp(min=0)
+    s = ((hi - lo) / 15 if asymmetric else v.abs().amax(-1, keepdim=True) / 7)
+    # binary32 and the type's rounding: a step and a half of either
+    assert torch.isfinite(scales.double()).all() and ((scales.double() - s).abs() <= 1.5 * torch.finfo(TYPES[dtype]).eps * s).all()
+    c = torch.stack([codes & 15, codes >> 4], -1).flatten(1).double()
+    c = c - zeros.double() if asymmetric else torch.where(c >= 8, c - 16, c)
+    # half a scale for the code and for the zero point, and 15 scales' rounding
+    assert ((c * scales.double() - v).abs() <= scales.double() * (1.0 + 15 * 2.0 ** -8)).all()
+
+
 # ---- the binding's own checks, without a GPU --------------------------------------
 
 

@@ -38,7 +38,8 @@ __device__ __forceinline__ void quantize_row(const D* W, int bytes, uint8_t* cod
         const int other = __shfl_xor((int)bad, d, 64);
         bad = bad || other;
     }
-    const float s = bad ? NAN : (float)(D)(zeros ? (hi - lo) / 15.f : hi / 7.f);
+    const float span = hi - lo, step = span < INFINITY ? span / 15.f : hi / 15.f - lo / 15.f;   // of finite bf16: up to 2^129
+    const float s = bad ? NAN : (float)(D)(zeros ? step : hi / 7.f);
     const bool usable = s > 0.f && s < INFINITY;
     int z = 0, qa = 0, qb = 0;
     if (usable) {
