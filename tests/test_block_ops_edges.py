@@ -77,6 +77,81 @@ def test_layer_norm_far_from_zero(gpu, width, mean, std):
             assert ((got.cpu().double() - want.repeat(rows // 5, 1)).abs() <= off.repeat(rows // 5, 1)).all()
 
 
+# ---- outputs that are inputs, rows that end inside a chunk ------------------------
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("width", [65, 130, 1035, 2051, 4091, 8197, 16383])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rows", [5, 300])
+def test_norm_in_place_at_ragged_widths(gpu, dtype, width, rows):
+    """The last chunk of a row shares elements with the one before it, which may be
+    another wave's; the same bits as with outputs of their own."""
+    dt = TYPES[dtype]
+    x, y = rand((rows, width), 1, dt).cuda(), rand((rows, width), 2, dt).cuda()
+    mods = {k: rand((width,), s, dt, 0.4).cuda() for s, k in enumerate(("gate", "scale", "shift", "weight"), 3)}
+    for norm, post in (("layer", None), ("rms", "layer"), ("layer", "rms")):
+        kw = dict(mods, norm=norm, post_norm=post, post_weight=mods["weight"] if post else None)
+        r, h = B.convrot_residual_norm(x, y, **kw)
+        for first, second in (("x", "y"), ("y", "x"), ("x", None), (None, "x"), ("y", None), (None, "y")):
+            place = {"x": x.clone(), "y": y.clone()}
+            got = B.convrot_residual_norm(place["x"], place["y"], r=place.get(first), h=place.get(second), **kw)
+            assert torch.equal(got[0], r) and torch.equal(got[1], h), (norm, post, first, second)
+            for name, t in (("x", x), ("y", y)):
+                if name not in (first, second):
+                    assert torch.equal(place[name], t)
+
+
+# ---- the grouped linear: many blocks a wave, every count of tiles ------------------
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_grouped_scales_stay_with_their_blocks(gpu, dtype, group, zeros):
+    """Rows of so many blocks that a wave hands scales, zero points, codes and x on
+    from one round of four blocks to the next, with one to four output tiles a
+    workgroup and with four waves.  Integers times powers of two: every sum is a
+    whole number of eighths below 12544 * 2 * 15 * 8 < 2^24, so results are exact."""
+    dt = TYPES[dtype]
+    g = torch.Generator(device="cuda").manual_seed(group + zeros)
+    # rows of whole lines, and rows that end inside a block
+    for k in (4352, {32: 4128, 64: 4160, 128: 4224}[group], 12544, 8192 + group):
+        for n in (40, 5000, 9001, 16000):
+            codes = torch.randint(0, 256, (n, k // 2), generator=g, device="cuda", dtype=torch.uint8)
+            s = (2.0 ** torch.randint(-3, 1, (n, k // group), generator=g, device="cuda")).to(dt)
+            z = torch.randint(0, 16, (n, k // group), generator=g, device="cuda", dtype=torch.uint8) if zeros else None
+            b = torch.randint(-9, 10, (n,), generator=g, device="cuda").to(dt)
+            c = torch.stack([codes & 15, codes >> 4], -1).view(n, k // group, group).double()
+            c = torch.where(c >= 8, c - 16, c) if z is None else c - z.double().unsqueeze(-1)
+            w = (c * s.double().unsqueeze(-1)).view(n, k)
+            for m in (1, 4, 5, 8, 16, 32):
+                x = torch.randint(-2, 3, (m, k), generator=g, device="cuda").to(dt)
+                want = torch.mm(w, x.double().t().contiguous()).t() + b.double()
+                got = B.convrot_linear_grouped(x, codes, s, z, b, group)
+                assert torch.equal(got, want.to(dt)), (m, n, k)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("zeros", [False, True])
+def test_grouped_subnormal_halves(gpu, zeros):
+    """Subnormal values of x and of the scales count: whole numbers of 2^-24, exact sums."""
+    g = torch.Generator().manual_seed(7)
+    m, n, k, group = 5, 33, 512, 32
+    codes = torch.randint(0, 256, (n, k // 2), generator=g, dtype=torch.uint8)
+    z = torch.randint(0, 16, (n, k // group), generator=g, dtype=torch.uint8) if zeros else None
+    c = torch.stack([codes & 15, codes >> 4], -1).view(n, k // group, group).double()
+    c = torch.where(c >= 8, c - 16, c) if z is None else c - z.double().unsqueeze(-1)
+    whole = torch.randint(-9, 10, (m, k), generator=g).double()
+    steps = torch.randint(1, 9, (n, k // group), generator=g).double()
+    for x, s in ((whole * 2.0 ** -24, steps * 2.0 ** -3), (whole * 2.0 ** -3, steps * 2.0 ** -24)):
+        want = x @ (c * s.unsqueeze(-1)).view(n, k).t()
+        x, s = x.half(), s.half()
+        got = B.convrot_linear_grouped(x.cuda(), codes.cuda(), s.cuda(), None if z is None else z.cuda(), None, group)
+        assert torch.equal(got.cpu(), want.half())
+
+
 # ---- the quantizer at the end of the range ----------------------------------------
 
 
