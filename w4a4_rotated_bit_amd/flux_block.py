@@ -217,7 +217,7 @@ def run_conditioned(T: int = 1536, hidden: int = 3072, batch: int = 1, group_siz
     swapped = convert_linears(quant, group_size, rotation, include=lambda name: name != "modulation_linear")
     if sorted(swapped) != ["down", "proj", "qkv", "up"]:
         raise RuntimeError(f"unexpected linears swapped: {swapped}")
-    quant.modulation_linear = GroupedLinear.from_linear(quant.modulation_linear, 128 if hidden % 128 == 0 else 64)
+    quant.modulation_linear = GroupedLinear.from_linear(quant.modulation_linear, 128)   # of heads of 128
     x = tokens(batch * T, hidden).view(batch, T, hidden).cuda()
     vec = torch.from_numpy(synth.bf16_bits_to_f32(synth.random_bf16((batch, hidden), seed=8))).to(torch.bfloat16).cuda()
     inputs = (x, vec, picture(T, batch).cuda())
