@@ -584,9 +584,7 @@ def _check_tensor(t, name, device):
 
 def _check_tangents(*tensors):
     """No tensor of this call carries a tangent of forward differentiation, which
-    ``requires_grad`` does not tell."""
-    if getattr(_forward, "_current_level", 0) < 0:   # outside of any dual level
-        return
+    ``requires_grad`` does not tell; outside of any dual level there are none."""
     for t in tensors:
         if isinstance(t, _torch.Tensor) and _forward.unpack_dual(t).tangent is not None:
             raise RuntimeError("a tensor of this call has a tangent, and this operator has no derivative: "
@@ -672,7 +670,8 @@ def convrot_residual_norm(x, y=None, *, gate=None, scale=None, shift=None, weigh
     makes the inputs, and their memory is kept until it is done."""
     device = _on_gpu(x, "x")
     _check_tensor(x, "x", device)
-    _check_tangents(x, y, gate, scale, shift, weight, post_weight, r, h)
+    if getattr(_forward, "_current_level", 0) >= 0:
+        _check_tangents(x, y, gate, scale, shift, weight, post_weight, r, h)
     shape, dtype = x.shape, x.dtype
     width = shape[-1] if shape else 0
     code = _type_of(x, "x")
@@ -735,7 +734,8 @@ def convrot_residual_norm(x, y=None, *, gate=None, scale=None, shift=None, weigh
             x.data_ptr(), y_ptr, gate_ptr, scale_ptr, shift_ptr, w_ptr, post_ptr, r_ptr, h_ptr, rows, width, x_stride,
             y_stride, r_stride, h_stride, gate_step, scale_step, shift_step, per or 1, residual_scale, eps, code,
             vec_code or code, *norms), raw)
-        _written(r, h)
+        if r is not None or h is not None:
+            _written(r, h)
         return r_out, h_out
 
     return _launch(device, stream, call, (x, y, gate, scale, shift, weight, post_weight, r, h))
@@ -800,7 +800,8 @@ def convrot_rope(q, k, positions, freq, axis, *, layout: str = "interleaved", qk
     ``convrot_residual_norm``."""
     device = _on_gpu(q, "q")
     _check_tensor(q, "q", device)
-    _check_tangents(q, k, positions, q_weight, k_weight, q_out, k_out)
+    if getattr(_forward, "_current_level", 0) >= 0:
+        _check_tangents(q, k, positions, q_weight, k_weight, q_out, k_out)
     shape, dtype = q.shape, q.dtype
     if len(shape) != 4:
         raise ValueError(f"q must be [batch, tokens, heads, head_dim], got {tuple(shape)}")
@@ -847,7 +848,8 @@ def convrot_rope(q, k, positions, freq, axis, *, layout: str = "interleaved", qk
             pos_strides[0] if pos_shape[0] > 1 else 0, pos_strides[1], pos_code, pos_shape[2], freq.shape[0],
             _address(freq), _address(axis), order, CONVROT_NORM_RMS if qk_norm else CONVROT_NORM_NONE, code,
             eps), raw)
-        _written(q_out, k_out)
+        if q_out is not None or k_out is not None:
+            _written(q_out, k_out)
         return outs[0], outs[1]
 
     return _launch(device, stream, call, (q, k, positions, q_weight, k_weight, q_out, k_out))
@@ -889,7 +891,8 @@ def convrot_linear_grouped(X, codes, scales, zeros, bias, group: int, Y=None, st
     unsigned codes, None with two's complement ones; bias: [N] or None.
     ``stream``: as in ``convrot_residual_norm``."""
     device = _on_gpu(X, "X")
-    _check_tangents(X, codes, scales, zeros, bias, Y)
+    if getattr(_forward, "_current_level", 0) >= 0:
+        _check_tangents(X, codes, scales, zeros, bias, Y)
     dtype = X.dtype
     code = _type_of(X, "X")
     if code == CONVROT_F32:
@@ -920,7 +923,8 @@ def convrot_linear_grouped(X, codes, scales, zeros, bias, group: int, Y=None, st
         y_ptr = y.data_ptr() if Y is None else place(Y, "Y", dtype, M, N)
         _call("convrot_linear_grouped",
               GROUPED_ARGS.pack(x_ptr, codes_ptr, scales_ptr, zeros_ptr, bias_ptr, y_ptr, M, N, K, group, code), raw)
-        _written(Y)
+        if Y is not None:
+            _written(Y)
         return y
 
     return _launch(device, stream, call, (X, codes, scales, zeros, bias, Y))
