@@ -293,8 +293,9 @@ int convrot_gemm(const void* workspace_dev, size_t ws_bytes, int64_t M, int64_t 
  *   - outputs must not overlap inputs or one another, except where a field
  *     says so (CONVROT_EINVAL).
  * Sums, statistics and angles are held in 32 bits or more whatever the storage
- * type, and each output is rounded to it once (nearest even).  None of these
- * operators has a gradient. */
+ * type, and each output is rounded to it once (nearest even).  A row whose
+ * squares sum beyond 2^128 has an infinite norm.  None of these operators has a
+ * gradient. */
 
 /* Storage types. */
 #define CONVROT_BF16 1
@@ -384,8 +385,10 @@ int convrot_validate_rope(const convrot_rope_args* args_host);
  *   W[n][k] = scales[n][k / group] * (code[n][k] - zeros[n][k / group]).
  * codes is N x packed-K, uint8 [N][K/2], the low nibble the even channel:
  * unsigned codes with zeros (uint8 [N][K/group], 0 .. 15), two's complement
- * ones in [-8, 7] without (zeros NULL).  No rotation, no repacking.  A row of X
- * that holds an infinity gives NaN. */
+ * ones in [-8, 7] without (zeros NULL).  No rotation, no repacking.  The sums of
+ * code * X and zeros * X are taken apart, in binary32: a row of X that holds an
+ * infinity gives NaN, and so may values whose sum over a group, times 15, lies
+ * beyond 2^128. */
 typedef struct {
     const void* x_dev;           /* [M][K], 16-byte aligned                    */
     const void* codes_dev;       /* [N][K/2], 16-byte aligned                  */

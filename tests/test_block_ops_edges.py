@@ -315,6 +315,37 @@ def test_inputs_freed_while_another_stream_reads_them(gpu):
         assert torch.equal(a, b)
 
 
+@pytest.mark.gpu
+def test_a_captured_call_on_another_stream(gpu):
+    """A graph whose calls run on a stream of their own, their temporaries freed during the capture."""
+    side = torch.cuda.Stream()
+    x, w = rand((4, 512), 1, torch.bfloat16).cuda(), rand((1024, 512), 2, torch.bfloat16, 0.05).cuda()
+    codes, scales, zeros = B.convrot_quantize_weight_grouped(w, 64, asymmetric=True)
+
+    def run(stream):
+        scale, shift = B.convrot_linear_grouped(x * 0.5, codes, scales, zeros, None, 64, stream=stream).chunk(2, -1)
+        return B.convrot_residual_norm(x, scale=scale, shift=shift, stream=stream)
+
+    run(None)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        half = x * 0.5
+        side.wait_stream(torch.cuda.current_stream())
+        mods = B.convrot_linear_grouped(half, codes, scales, zeros, None, 64, stream=side)
+        del half
+        outs = B.convrot_residual_norm(x, scale=mods[:, :512], shift=mods[:, 512:], stream=side)
+        del mods
+        torch.cuda.current_stream().wait_stream(side)
+    for step in range(4):
+        x.copy_(rand(x.shape, step, torch.bfloat16))
+        want = [t.clone() for t in run(None)]
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(outs, want):
+            assert torch.equal(a, b), step
+
+
 # ---- sources ------------------------------------------------------------------------
 
 

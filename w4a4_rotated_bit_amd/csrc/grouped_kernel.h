@@ -20,9 +20,18 @@
 // 128 of them beside 8 or 16 matrix instructions: 32 x 16384 -> 16384 takes 44
 // us (143 MB, 3.2 TB/s), 34 with its codes in the cache and 26 for reading alone,
 // and 16 x 4128 -> 9001 with groups of 32 takes 13.3 us: 4.3 for launch, first
-// loads and the joining of the waves, then 1.6 to 1.8 for each block of a wave,
-// bound by the widening (10.8 with rows of 4096, which begin with a line of memory
-// and give a wave four blocks instead of five).
+// loads and the joining of the waves, then 1.6 to 1.8 for each block of a wave
+// (10.8 with rows of 4096, which begin with a line of memory and give a wave four
+// blocks instead of five).  Of those nine, the some 1200 vector instructions a
+// wave, two waves a SIMD at some 4.6 cycles each, are about half and its 66 matrix
+// instructions one; the rest is waiting for a block's way through shared memory,
+// which the fences around `multiply` leave in the open.
+//
+// Few outputs and long rows leave units idle: a workgroup for every 16 outputs
+// (8 for few rows of x), and only its own waves share K.  4096 -> 1024 takes 4.0,
+// 4.5, 5.1 and 7.2 us for 1, 8, 16 and 32 rows of x, 14336 -> 1024 7.3, 10.4, 12.6
+// and 18.8, and hardly less for 256 outputs; reading the codes alone would take 2
+// to 3 us.
 #pragma once
 #include "block_ops.h"
 
@@ -447,9 +456,9 @@ void launch_one(GroupedParams p, hipStream_t s)
 // M > 4: every workgroup reads all of x, so it takes as many outputs as one
 //   round (or several equal ones) over the units allows, up to 64 (16 x 4096 ->
 //   16384: 11.9 with 64 outputs, 14.0 with 32, 15.1 with 16), with eight waves:
-//   two a SIMD cover each other's waits (32 x 16384 -> 16384: 42.8, with four
-//   46.4; 32 x 4096 -> 16384 in groups of 32: 18.7, with four 22.9, although
-//   eight have to keep some 25 of their registers in memory).
+//   two a SIMD cover some of each other's waits (32 x 16384 -> 16384: 42.8, with four
+//   46.4; 32 x 4096 -> 16384 in groups of 32: 17.4 (with zero points 19.3), with
+//   four 22.9, although eight have to keep 10 (24 to 29) registers in memory).
 template <typename D, int GROUP, bool ZEROS>
 void launch_zeros(GroupedParams p, hipStream_t s)
 {

@@ -16,12 +16,13 @@
 //
 // Bound by memory: 32768 rows of 4096 bf16 with both norms, every vector and
 // both outputs move 1.07 GB in 194 us (5.5 TB/s; a copy of that size reaches
-// 5.0 TB/s, one of 256 MB 5.5), 1536 rows 50 MB in 10.2 us (4.9 TB/s).  Rows are
-// loaded and stored with the hint that they are used once, without it 215 and
-// 12.4 us; not where a chunk does not divide the width, whose chunks share lines
-// (999 rows of 1035 7.0 against 6.6 us).  Short inputs are
-// bound by latency: one row of 4096 takes 2.4 us where an empty kernel takes
-// 1.9, and 999 rows of 1035 f16, two norms, 6.8 us: four sums across the
+// 5.0 TB/s, one of 256 MB 5.5), 1536 rows 50 MB in 10.3 us (4.9 TB/s).  Rows are
+// loaded and stored with the hint that they are used once, without it 204 and
+// 12.5 us (16384 rows of 2048, whose 268 MB the last cache all but holds, 48.4
+// with it and 44.8 without); not where a chunk does not divide the width, whose
+// chunks share lines (999 rows of 1035: 6.8 us with and without).  Short inputs
+// are bound by latency: one row of 4096 takes 2.4 us where an empty kernel takes
+// 1.9, and 999 rows of 1035 f16, two norms, 6.8 us: four exchanges across the
 // workgroup one after the other, and chunks that cross lines of memory.
 //
 // One row a workgroup, and nothing else kept from row to row: workgroups that
@@ -220,8 +221,8 @@ void launch_one(const NormParams& p, hipStream_t s)
     // a grid dimension holds fewer than 2^32 threads
     const unsigned blocks = (p.rows + kRows - 1) / kRows, gx = blocks < (1u << 20) ? blocks : 1u << 20;
     // Registers for the vectors too only where that leaves as many rows
-    // resident: 16384 rows of 2048 49.6 us with, 52.5 without, 1536 of 4096 (two
-    // chunks a thread) 12.7 with, 10.2 without.
+    // resident: 16384 rows of 2048 48.4 us with, 49.4 without, 1536 of 4096 (two
+    // chunks a thread) 12.6 with, 10.3 without.
     hipLaunchKernelGGL((residual_norm_kernel<D, E, T, V, NV, TAIL, (NV == 1)>), dim3(gx, (blocks + gx - 1) / gx),
                        dim3(kThreads), 0, s, p);
 }
@@ -232,11 +233,11 @@ void launch_width(const NormParams& p, hipStream_t s)
     constexpr int V = 16 / sizeof(D);
     const int chunks = (p.width + V - 1) / V;
     // A row of up to 128 chunks is one wave's and needs no barrier; from there on
-    // a thread of a workgroup has one chunk (999 rows of 130 chunks: 6.6 us, one
-    // wave with three chunks a lane 7.3), or two, which holds more rows in
-    // flight (1536 rows of 512 chunks: 10.2 us, with one chunk a thread 12.6),
-    // unless there are fewer rows than units (one row of 512 chunks: 2.6 us with
-    // one chunk a thread, 2.8 with two).
+    // a thread of a workgroup has one chunk (999 rows of 130 chunks: 6.8 us, one
+    // wave with three chunks a lane 6.95), or two, which holds more rows in
+    // flight (1536 rows of 512 chunks: 10.3 us, with one chunk a thread 12.9),
+    // unless there are fewer rows than units (one row of 512 chunks: 2.4 us with
+    // one chunk a thread, 2.6 with two).
     if (chunks <= 64) launch_one<D, E, 64, V, 1, TAIL>(p, s);
     else if (chunks <= 128) launch_one<D, E, 64, V, 2, TAIL>(p, s);
     else if (chunks <= 256) launch_one<D, E, 256, V, 1, TAIL>(p, s);
