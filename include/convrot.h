@@ -414,6 +414,120 @@ int convrot_quantize_weight_grouped(const void* W_dev, int64_t N, int64_t K, int
 int convrot_validate_quantize_weight_grouped(const void* W_dev, int64_t N, int64_t K, int group, int dtype,
                                              const uint8_t* codes_dev, const void* scales_dev, const uint8_t* zeros_dev);
 
+/* ---- attention and the paged cache that it reads ------------------------- */
+/*
+ *   o[h] = sum_j p[h][j] v[j] / sum_j p[h][j],  p[h][j] = exp(scale q[h] . k[j])
+ * over the keys that a query sees.  Query heads share key heads in order: head
+ * h reads key head h / (q_heads / k_heads).  A query that sees no key has o = 0
+ * and lse = -infinity.  Scores, the softmax's running maximum and sum and the
+ * outputs are held in binary32; p is rounded to the type of the heads before it
+ * multiplies v.  lse (natural logarithm of sum_j p[h][j]) is optional.
+ * Kernels are launched on the caller's stream and keep no state; a workspace
+ * is written and read within one call, and holds nothing between calls.
+ */
+#define CONVROT_I64 5
+/* How a cache keeps its rows: as they are (BF16, F16), or in blocks of 32
+ * channels that share a scale 2^(s - 127), s a byte: e4m3 values (no
+ * infinities, largest 448), one a byte, or e2m1 values (0, 0.5, 1, 1.5, 2, 3, 4,
+ * 6), two a byte, the low nibble the even channel.  A block is written with
+ * 2^(s - 127) = 2^(floor(log2(its largest magnitude)) - 8 or - 2), at least
+ * 2^-127, and each value to the nearest one of the format (ties to even; beyond
+ * the largest, the largest).  A block that holds an infinity or a NaN gets s =
+ * 255 and reads back as NaN. */
+#define CONVROT_CACHE_E4M3 6
+#define CONVROT_CACHE_E2M1 7
+
+/* The rows of the keys or of the values; strides in bytes, multiples of 16, and
+ * rows_dev 16-byte aligned.  A row is head_dim values of the cache's kind. */
+typedef struct {
+    void* rows_dev;              /* [pages][heads][page_size] rows             */
+    uint8_t* scales_dev;         /* head_dim / 32 bytes a row; NULL for BF16, F16 */
+    int64_t page_stride, head_stride, token_stride;
+    int64_t scale_page_stride, scale_head_stride, scale_token_stride;
+} convrot_cache_rows;
+typedef struct {
+    convrot_cache_rows k, v;
+    int64_t pages;               /* 1 .. 2^31 - 1                              */
+    int page_size;               /* a power of two, 8 .. 65536                 */
+    int heads;                   /* 1 .. 65535                                 */
+    int head_dim;                /* 8 .. 256, a multiple of 8 (BF16, F16) or 32 */
+    int kind;                    /* CONVROT_BF16, _F16, _CACHE_E4M3 or _CACHE_E2M1 */
+} convrot_kv_cache;
+
+/* Rows of tokens into a cache, or out of one.  Token i's place is slots[i] = page
+ * * page_size + its place in the page.  A slot that lies outside the cache (-1 for
+ * the padding of a batch) is skipped by a write and read as zeros.  The slots of
+ * a write are distinct: what a place holds that two of them name is not
+ * specified (every other place is right).  dtype: BF16 or F16, that of the cache
+ * where it keeps rows as they are; rows of an e4m3 or e2m1 cache are read back
+ * rounded to dtype (exact in BF16 but for magnitudes beyond its range). */
+typedef struct {
+    convrot_kv_cache cache;
+    void *k_dev, *v_dev;         /* [tokens][heads][head_dim]: read by a write, written by a read */
+    const void* slots_dev;       /* [tokens]                                   */
+    int64_t tokens;              /* 0 .. 16777216                              */
+    int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;   /* elements */
+    int slots_dtype;             /* CONVROT_I32 or CONVROT_I64                 */
+    int dtype;
+} convrot_cache_args;
+int convrot_cache_write(const convrot_cache_args* args_host, void* stream);
+int convrot_cache_read(const convrot_cache_args* args_host, void* stream);
+int convrot_validate_cache_write(const convrot_cache_args* args_host);
+int convrot_validate_cache_read(const convrot_cache_args* args_host);
+
+/* One new token of each sequence against the cache: sequence b's keys are the
+ * first lengths[b] places of the pages page_table[b][0], [1], ... (its own new key
+ * among them, written before).  A length beyond the table's width counts as that
+ * width, a negative one as 0; places of a page outside the cache are not seen. */
+typedef struct {
+    convrot_kv_cache cache;
+    const void* q_dev;           /* [batch][q_heads][head_dim]                 */
+    void* o_dev;                 /* the same                                   */
+    float* lse_dev;              /* [batch][q_heads] or NULL                   */
+    const int* page_table_dev;   /* [batch][table_width], rows table_stride apart */
+    const int* lengths_dev;      /* [batch]                                    */
+    int64_t batch, table_width, table_stride;   /* 0 .. 65535; times page_size at most 2^30; elements */
+    int64_t q_batch_stride, q_head_stride, o_batch_stride, o_head_stride;   /* elements */
+    int q_heads;                 /* a multiple of the cache's heads, at most 65535 */
+    int dtype;                   /* of q and o: BF16 or F16, that of the cache where it keeps rows as they are */
+    float scale;
+    int reserved;                /* 0                                          */
+} convrot_attention_paged_args;
+/* Bytes of the workspace (16-byte aligned; 0: NULL will do). */
+int convrot_attention_paged_workspace_bytes(const convrot_attention_paged_args* args_host, size_t* bytes_host);
+int convrot_attention_paged(const convrot_attention_paged_args* args_host, void* workspace_dev, size_t ws_bytes,
+                            void* stream);
+int convrot_validate_attention_paged(const convrot_attention_paged_args* args_host, const void* workspace_dev,
+                                     size_t ws_bytes);
+
+/* Whole prompts.  With starts, sequences lie packed one behind the other:
+ * sequence b has the queries q_starts[b] .. q_starts[b + 1] - 1 of the q_tokens
+ * rows and the keys k_starts[b] .. k_starts[b + 1] - 1 (starts ascend and lie
+ * within the rows; what lies beyond is cut off).  Rows of o and lse of no
+ * sequence are left as they were.  Without (both NULL) batch entries of q_tokens
+ * queries and k_tokens keys lie batch strides apart.  causal: the last query sees
+ * every key, the one before it all but the last, and so on; a query left without
+ * a key has o = 0. */
+typedef struct {
+    const void *q_dev, *k_dev, *v_dev;   /* [batch][tokens][heads][head_dim], packed: [tokens][heads][head_dim] */
+    void* o_dev;
+    float* lse_dev;              /* [batch][q_tokens][q_heads], dense, or NULL */
+    const int *q_starts_dev, *k_starts_dev;   /* [batch + 1] or NULL           */
+    int64_t batch, q_tokens, k_tokens;        /* 0 .. 65535, 0 .. 16777216     */
+    int64_t q_batch_stride, q_token_stride, q_head_stride;   /* elements       */
+    int64_t k_batch_stride, k_token_stride, k_head_stride;
+    int64_t v_batch_stride, v_token_stride, v_head_stride;
+    int64_t o_batch_stride, o_token_stride, o_head_stride;   /* k's and v's token strides below 2^24 */
+    int q_heads, k_heads;        /* 1 .. 65535, q_heads a multiple of k_heads  */
+    int head_dim;                /* 8 .. 256, a multiple of 8                  */
+    int causal;                  /* 0 or 1                                     */
+    int dtype;                   /* BF16 or F16                                */
+    float scale;
+} convrot_attention_args;
+int convrot_attention_workspace_bytes(const convrot_attention_args* args_host, size_t* bytes_host);
+int convrot_attention(const convrot_attention_args* args_host, void* workspace_dev, size_t ws_bytes, void* stream);
+int convrot_validate_attention(const convrot_attention_args* args_host, const void* workspace_dev, size_t ws_bytes);
+
 /* ---- parity hooks (same kernels, exposed intermediate results) ---------- */
 
 /* Rotation + row absmax + quantization of `rows` bf16 rows, with plain

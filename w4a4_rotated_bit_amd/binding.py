@@ -13,6 +13,7 @@ import ctypes
 import os
 import struct
 import threading
+from typing import Any, NamedTuple
 
 import numpy as np
 
@@ -99,6 +100,16 @@ _SIGNATURES = {
     "convrot_validate_linear_grouped": ([_P], _I),
     "convrot_quantize_weight_grouped": ([_P, _I64, _I64, _I, _I, _P, _P, _P, _P], _I),
     "convrot_validate_quantize_weight_grouped": ([_P, _I64, _I64, _I, _I, _P, _P, _P], _I),
+    "convrot_cache_write": ([_P, _P], _I),
+    "convrot_cache_read": ([_P, _P], _I),
+    "convrot_validate_cache_write": ([_P], _I),
+    "convrot_validate_cache_read": ([_P], _I),
+    "convrot_attention_paged": ([_P, _P, _SZ, _P], _I),
+    "convrot_attention_paged_workspace_bytes": ([_P, ctypes.POINTER(_SZ)], _I),
+    "convrot_validate_attention_paged": ([_P, _P, _SZ], _I),
+    "convrot_attention": ([_P, _P, _SZ, _P], _I),
+    "convrot_attention_workspace_bytes": ([_P, ctypes.POINTER(_SZ)], _I),
+    "convrot_validate_attention": ([_P, _P, _SZ], _I),
     "convrot_host_pack_nk": ([_P, _I64, _I64, _P], _I),
     "convrot_host_unpack_nk": ([_P, _I64, _I64, _P], _I),
     "convrot_host_nk_to_kn": ([_P, _I64, _I64, _P], _I),
@@ -928,3 +939,358 @@ def convrot_linear_grouped(X, codes, scales, zeros, bias, group: int, Y=None, st
         return y
 
     return _launch(device, stream, call, (X, codes, scales, zeros, bias, Y))
+
+
+# --------------------------------------------------------------------------
+# attention and the paged cache that it reads
+# --------------------------------------------------------------------------
+
+CONVROT_I64 = 5
+CONVROT_CACHE_E4M3 = 6
+CONVROT_CACHE_E2M1 = 7
+
+# The argument structs of the C calls, in their order (native alignment).
+_CACHE_FIELDS = 2 * "2P6q" + "q4i"
+CACHE_ARGS = struct.Struct("@" + _CACHE_FIELDS + "3P5q2i")
+PAGED_ARGS = struct.Struct("@" + _CACHE_FIELDS + "5P7q2ifi")
+ATTENTION_ARGS = struct.Struct("@7P15q5if")
+
+
+class KVCache(NamedTuple):
+    """Keys and values in pages: k, v are [pages, heads, page_size, ...] device
+    tensors, dense in their last dimension, the other strides any multiples of 16
+    bytes (of a permuted view, of a slice of a tensor of all layers).
+
+    bfloat16 or float16 [..., head_dim] keeps rows as they are.  float8_e4m3fn [...,
+    head_dim] and uint8 [..., head_dim / 2] (two e2m1 values a byte, the low nibble
+    the even channel) keep blocks of 32 channels that share a scale, k_scales and
+    v_scales uint8 [pages, heads, page_size, head_dim / 32], which stand for
+    2^(s - 127).  page_size: a power of two, 8 to 65536; head_dim: up to 256, a multiple
+    of 8, or of 32 with scales.  ``new_kv_cache`` allocates one."""
+    k: Any
+    v: Any
+    k_scales: Any = None
+    v_scales: Any = None
+
+
+def new_kv_cache(pages: int, page_size: int, heads: int, head_dim: int, kind="e2m1", device="cuda") -> KVCache:
+    """A cache of zeros.  kind: "e2m1", "e4m3", torch.bfloat16 or torch.float16."""
+    torch = _torch or _use_torch()
+    shape = (pages, heads, page_size)
+    if kind in (torch.bfloat16, torch.float16):
+        return KVCache(*(torch.zeros((*shape, head_dim), dtype=kind, device=device) for _ in range(2)))
+    if kind not in ("e2m1", "e4m3"):
+        raise ValueError(f"unknown kind {kind!r}")
+    if head_dim % 32:
+        raise ValueError(f"a quantized cache takes whole blocks of 32 channels, got head_dim {head_dim}")
+    rows = [torch.zeros((*shape, head_dim if kind == "e4m3" else head_dim // 2), dtype=torch.uint8, device=device)
+            for _ in range(2)]
+    if kind == "e4m3":
+        rows = [r.view(torch.float8_e4m3fn) for r in rows]
+    scales = [torch.zeros((*shape, head_dim // 32), dtype=torch.uint8, device=device) for _ in range(2)]
+    return KVCache(*rows, *scales)
+
+
+def _cache_fields(cache, device):
+    """(fields of one convrot_kv_cache, heads, head_dim, type of rows kept as they are or None)."""
+    k, v, k_scales, v_scales = cache
+    for name, t in (("cache.k", k), ("cache.v", v)):
+        if not isinstance(t, _torch.Tensor) or t.get_device() != device or t.requires_grad:
+            _check_tensor(t, name, device)
+    shape, dtype = k.shape, k.dtype
+    if len(shape) != 4 or v.shape != shape or v.dtype != dtype:
+        raise ValueError("the cache's k and v must be [pages, heads, page_size, ...] of one shape and type, got "
+                         f"{tuple(shape)} {dtype} and {tuple(v.shape)} {v.dtype}")
+    pages, heads, page_size, last = shape
+    if dtype is _torch.float8_e4m3fn:
+        kind, size, dim, kept = CONVROT_CACHE_E4M3, 1, last, None
+    elif dtype is _torch.uint8:
+        kind, size, dim, kept = CONVROT_CACHE_E2M1, 1, 2 * last, None
+    elif dtype is _torch.bfloat16:
+        kind, size, dim, kept = CONVROT_BF16, 2, last, dtype
+    elif dtype is _torch.float16:
+        kind, size, dim, kept = CONVROT_F16, 2, last, dtype
+    else:
+        raise TypeError(f"a cache keeps bfloat16, float16, float8_e4m3fn or uint8 (e2m1) rows, not {dtype}")
+    fields = []
+    for name, rows, scales in (("k", k, k_scales), ("v", v, v_scales)):
+        page, head, token, one = rows.stride()
+        if one != 1 and last > 1:
+            raise ValueError(f"cache.{name} must be dense in its last dimension")
+        at = steps = None
+        if kept is None:
+            if not isinstance(scales, _torch.Tensor) or scales.get_device() != device:
+                _check_tensor(scales, f"cache.{name}_scales", device)
+            if scales.dtype is not _torch.uint8 or scales.shape != (pages, heads, page_size, dim // 32):
+                raise ValueError(f"cache.{name}_scales must be uint8 [pages, heads, page_size, head_dim / 32], got "
+                                 f"{scales.dtype} {tuple(scales.shape)}")
+            *steps, one = scales.stride()
+            if one != 1 and dim > 32:
+                raise ValueError(f"cache.{name}_scales must be dense in its last dimension")
+            at = scales.data_ptr()
+        elif scales is not None:
+            raise ValueError("a cache that keeps rows as they are has no scales")
+        fields += (rows.data_ptr(), at or 0, page * size, head * size, token * size, *(steps or (0, 0, 0)))
+    return (*fields, pages, page_size, heads, dim, kind), heads, dim, kept
+
+
+def _slots_code(slots, tokens, device):
+    if not isinstance(slots, _torch.Tensor) or slots.get_device() != device:
+        _check_tensor(slots, "slots", device)
+    if slots.dim() != 1 or slots.shape[0] != tokens or not slots.is_contiguous():
+        raise ValueError(f"slots must be one dense vector of {tokens} places, got shape {tuple(slots.shape)}")
+    if slots.dtype is _torch.int64:
+        return CONVROT_I64
+    if slots.dtype is _torch.int32:
+        return CONVROT_I32
+    raise TypeError(f"slots must be int32 or int64, got {slots.dtype}")
+
+
+def _token_rows(t, name, heads, dim, device):
+    """(token stride, head stride) of [tokens, heads, head_dim]."""
+    if not isinstance(t, _torch.Tensor) or t.get_device() != device or t.requires_grad:
+        _check_tensor(t, name, device)
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name} must be [tokens, {heads}, {dim}], got {tuple(shape)}")
+    token, head, one = t.stride()
+    if one != 1:
+        raise ValueError(f"{name} must be dense in its last dimension")
+    return token, head
+
+
+def _half_code(dtype, name):
+    code = _types.get(dtype)
+    if code not in (CONVROT_BF16, CONVROT_F16):
+        raise TypeError(f"{name} must be bfloat16 or float16, got {dtype}")
+    return code
+
+
+def convrot_cache_write(k, v, slots, cache: KVCache, stream=None) -> None:
+    """Rows of new tokens into a paged cache, quantized where it keeps blocks.
+
+    k, v: bf16 or f16 [tokens, heads, head_dim] of any strides but a dense last one
+    (slices of a packed projection).  slots: int32 or int64 [tokens], page *
+    page_size + place in the page; one outside the cache (-1) skips its token.
+    Slots are distinct: what a place holds that two of them name is not specified.
+    ``stream``: as in ``convrot_residual_norm``."""
+    device = _on_gpu(k, "k")
+    if getattr(_forward, "_current_level", 0) >= 0:
+        _check_tangents(k, v, *cache)
+    fields, heads, dim, kept = _cache_fields(cache, device)
+    k_strides, v_strides = _token_rows(k, "k", heads, dim, device), _token_rows(v, "v", heads, dim, device)
+    dtype, tokens = k.dtype, k.shape[0]
+    if v.dtype != dtype or v.shape[0] != tokens:
+        raise ValueError("k and v must have one shape and type")
+    code = _half_code(dtype, "k")
+    if kept is not None and kept != dtype:
+        raise TypeError(f"the cache keeps {kept} rows, k and v are {dtype}")
+    slots_code = _slots_code(slots, tokens, device)
+
+    def call(raw):
+        _call("convrot_cache_write", CACHE_ARGS.pack(*fields, k.data_ptr(), v.data_ptr(), slots.data_ptr(), tokens,
+                                                     *k_strides, *v_strides, slots_code, code), raw)
+        _written(*cache)
+
+    return _launch(device, stream, call, (k, v, slots, *cache))
+
+
+def convrot_cache_read(cache: KVCache, slots, dtype=None, k=None, v=None, stream=None):
+    """(k, v) [tokens, heads, head_dim]: the rows at ``slots``, zeros for a slot outside
+    the cache.  dtype: bfloat16 (also the default of a quantized cache) or float16; a
+    cache that keeps rows as they are reads back its own.  k, v given are
+    written.  ``stream``: as in ``convrot_residual_norm``."""
+    device = _on_gpu(cache[0], "cache.k")
+    if getattr(_forward, "_current_level", 0) >= 0:
+        _check_tangents(k, v, *cache)
+    fields, heads, dim, kept = _cache_fields(cache, device)
+    for t in (k, v):
+        if dtype is None and t is not None:
+            dtype = t.dtype
+    dtype = dtype or kept or _torch.bfloat16
+    code = _half_code(dtype, "dtype")
+    if kept is not None and kept != dtype:
+        raise TypeError(f"the cache keeps {kept} rows, not {dtype}")
+    if not isinstance(slots, _torch.Tensor):
+        raise TypeError("slots must be a torch tensor")
+    tokens = slots.numel()
+    slots_code = _slots_code(slots, tokens, device)
+
+    def call(raw):
+        outs, strides = [], []
+        for name, t in (("k", k), ("v", v)):
+            if t is None:
+                t = _torch.empty((tokens, heads, dim), dtype=dtype, device=slots.device)
+            strides += _token_rows(t, name, heads, dim, device)
+            if t.shape[0] != tokens or t.dtype != dtype:
+                raise ValueError(f"{name} must have {tokens} rows of {dtype}")
+            outs.append(t)
+        _call("convrot_cache_read", CACHE_ARGS.pack(*fields, outs[0].data_ptr(), outs[1].data_ptr(), slots.data_ptr(), tokens,
+                                                    *strides, slots_code, code), raw)
+        if k is not None or v is not None:
+            _written(k, v)
+        return outs[0], outs[1]
+
+    return _launch(device, stream, call, (slots, k, v, *cache))
+
+
+def _workspace(name, args, workspace, device):
+    """(address, bytes, what keeps it) of the call's workspace, allocated unless given."""
+    if workspace is None:
+        need = _SZ(0)
+        _call(name, args, ctypes.byref(need))
+        if need.value == 0:
+            return None, 0, None
+        workspace = _torch.empty(need.value, dtype=_torch.uint8, device=f"cuda:{device}")
+    else:
+        _check_tensor(workspace, "workspace", device)
+        if workspace.dtype is not _torch.uint8 or not workspace.is_contiguous():
+            raise ValueError("workspace must be a dense uint8 tensor")
+    return workspace.data_ptr(), workspace.numel(), workspace
+
+
+def _table(t, name, dims, device):
+    if not isinstance(t, _torch.Tensor) or t.get_device() != device:
+        _check_tensor(t, name, device)
+    if t.dtype is not _torch.int32:
+        raise TypeError(f"{name} must be int32, got {t.dtype}")
+    if t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must have {dims} dimensions and be dense in the last, got shape {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _output(out, q, want, name, shape, dtype, device):
+    """The output given (checked), a new one, or None."""
+    if out is None:
+        return _torch.empty(shape, dtype=dtype, device=q.device) if want else None
+    _check_tensor(out, name, device)
+    if out.shape != shape or out.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {out.dtype} {tuple(out.shape)}")
+    return out
+
+
+def convrot_attention_paged(q, cache: KVCache, page_table, lengths, *, scale=None, out=None, lse=None,
+                            want_lse: bool = False, workspace=None, stream=None):
+    """softmax(scale q K^T) V for one new token of each sequence over a paged cache.
+
+    q: bf16 or f16 [batch, q_heads, head_dim], any strides but a dense last one; q_heads a
+    multiple of the cache's heads, which they share in order.  page_table: int32
+    [batch, pages of a sequence]; lengths: int32 [batch], the keys of each sequence, its
+    new one (written before) among them.  A length of 0 gives zeros; places of a page
+    that is not in the cache are not seen.  scale: 1 / sqrt(head_dim) unless given.
+    Returns out [batch, q_heads, head_dim], with ``want_lse`` or a given lse (out, lse), lse
+    float32 [batch, q_heads] the natural logarithm of the sum of exponentials.
+    workspace: uint8, of ``convrot_attention_paged_workspace_bytes`` of the same
+    call; allocated where none is given.  Calls that may run at the same time,
+    captured ones among them, need one each.  ``stream``: as in
+    ``convrot_residual_norm``."""
+    device = _on_gpu(q, "q")
+    _check_tensor(q, "q", device)
+    if getattr(_forward, "_current_level", 0) >= 0:
+        _check_tangents(q, out, lse, *cache)
+    shape, dtype = q.shape, q.dtype
+    code = _half_code(dtype, "q")
+    fields, heads, dim, kept = _cache_fields(cache, device)
+    if len(shape) != 3 or shape[2] != dim or (dim > 1 and q.stride(2) != 1):
+        raise ValueError(f"q must be [batch, q_heads, {dim}] and dense in its last dimension, got {tuple(shape)}")
+    if shape[1] % heads:
+        raise ValueError(f"{shape[1]} query heads do not share {heads} key heads evenly")
+    if kept is not None and kept != dtype:
+        raise TypeError(f"the cache keeps {kept} rows, q is {dtype}")
+    table_ptr, lengths_ptr = _table(page_table, "page_table", 2, device), _table(lengths, "lengths", 1, device)
+    if page_table.shape[0] != shape[0] or lengths.shape[0] != shape[0]:
+        raise ValueError(f"page_table and lengths must have one row for each of the {shape[0]} sequences")
+    scale = dim ** -0.5 if scale is None else float(scale)
+
+    def call(raw):
+        o = _output(out, q, True, "out", shape, dtype, device)
+        if o.stride(2) != 1:
+            raise ValueError("out must be dense in its last dimension")
+        sums = _output(lse, q, want_lse, "lse", shape[:2], _torch.float32, device)
+        if sums is not None and not sums.is_contiguous():
+            raise ValueError("lse must be contiguous")
+        args = PAGED_ARGS.pack(*fields, q.data_ptr(), o.data_ptr(), 0 if sums is None else sums.data_ptr(), table_ptr,
+                               lengths_ptr, shape[0], page_table.shape[1], page_table.stride(0), q.stride(0), q.stride(1),
+                               o.stride(0), o.stride(1), shape[1], code, scale, 0)
+        ws_ptr, ws_bytes, _keep = _workspace("convrot_attention_paged_workspace_bytes", args, workspace, device)
+        _call("convrot_attention_paged", args, ws_ptr, ws_bytes, raw)
+        if out is not None or lse is not None:
+            _written(out, lse)
+        return o if sums is None else (o, sums)
+
+    return _launch(device, stream, call, (q, page_table, lengths, out, lse, workspace, *cache))
+
+
+def convrot_attention(q, k, v, *, q_starts=None, k_starts=None, causal: bool = False, scale=None, out=None, lse=None,
+                      want_lse: bool = False, workspace=None, stream=None):
+    """softmax(scale q K^T) V for whole prompts.
+
+    q: bf16 or f16 [batch, q_tokens, q_heads, head_dim], k, v: [batch, k_tokens, k_heads,
+    head_dim], any strides but a dense last one (slices of a packed projection); or, with
+    q_starts (and k_starts, the same unless given), sequences packed one behind the other,
+    [tokens, heads, head_dim]: int32 [sequences + 1] on the device, ascending.  q_heads is a
+    multiple of k_heads, which they share in order; head_dim a multiple of 8, at most 256.
+    causal: a sequence's last query sees all of its keys, the one before all but
+    the last, and so on.  A query that sees none gives zeros; rows behind the last
+    sequence are left as they are (of a new ``out``: unset).  scale: 1 / sqrt(head_dim)
+    unless given.  Returns out of q's shape, with ``want_lse`` or a given lse (out, lse),
+    lse float32 of q's shape without head_dim.  workspace: uint8, of
+    ``convrot_attention_workspace_bytes`` of the same call; allocated where none is given.
+    Calls that may run at the same time, captured ones among them, need one each.
+    ``stream``: as in ``convrot_residual_norm``."""
+    device = _on_gpu(q, "q")
+    _check_tensor(q, "q", device)
+    if getattr(_forward, "_current_level", 0) >= 0:
+        _check_tangents(q, k, v, out, lse)
+    shape, dtype = q.shape, q.dtype
+    code = _half_code(dtype, "q")
+    for name, t in (("k", k), ("v", v)):
+        _check_tensor(t, name, device)
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must have the type of q")
+    packed = q_starts is not None
+    rank = 3 if packed else 4
+    if len(shape) != rank or len(k.shape) != rank or v.shape != k.shape or k.shape[-1] != shape[-1]:
+        raise ValueError("q, k and v must be " + ("[tokens, heads, head_dim]" if packed else "[batch, tokens, heads, head_dim]") +
+                         f", k and v of one shape, got {tuple(shape)}, {tuple(k.shape)} and {tuple(v.shape)}")
+    q_starts_ptr = k_starts_ptr = 0
+    if packed:
+        q_starts_ptr = _table(q_starts, "q_starts", 1, device)
+        k_starts = q_starts if k_starts is None else k_starts
+        k_starts_ptr = _table(k_starts, "k_starts", 1, device)
+        batch = q_starts.shape[0] - 1
+        if batch < 0 or k_starts.shape != q_starts.shape:
+            raise ValueError("q_starts and k_starts must hold one value more than there are sequences")
+    elif k_starts is not None:
+        raise ValueError("k_starts need q_starts")
+    else:
+        batch = shape[0]
+        if k.shape[0] != batch:
+            raise ValueError(f"q has {batch} batch entries, k and v have {k.shape[0]}")
+    tokens, heads, dim = shape[-3:]
+    k_tokens, k_heads, _ = k.shape[-3:]
+    if k_heads == 0 or heads % k_heads:
+        raise ValueError(f"{heads} query heads do not share {k_heads} key heads evenly")
+    scale = dim ** -0.5 if scale is None else float(scale)
+
+    def steps(t, name):
+        s = t.stride()
+        if s[-1] != 1 and dim > 1:
+            raise ValueError(f"{name} must be dense in its last dimension")
+        return (0, s[0], s[1]) if packed else s[:3]
+
+    def call(raw):
+        o = _output(out, q, True, "out", shape, dtype, device)
+        sums = _output(lse, q, want_lse, "lse", shape[:-1], _torch.float32, device)
+        if sums is not None and not sums.is_contiguous():
+            raise ValueError("lse must be contiguous")
+        args = ATTENTION_ARGS.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), 0 if sums is None else sums.data_ptr(),
+                                   q_starts_ptr, k_starts_ptr, batch, tokens, k_tokens, *steps(q, "q"), *steps(k, "k"),
+                                   *steps(v, "v"), *steps(o, "out"), heads, k_heads, dim, 1 if causal else 0, code, scale)
+        ws_ptr, ws_bytes, _keep = _workspace("convrot_attention_workspace_bytes", args, workspace, device)
+        _call("convrot_attention", args, ws_ptr, ws_bytes, raw)
+        if out is not None or lse is not None:
+            _written(out, lse)
+        return o if sums is None else (o, sums)
+
+    return _launch(device, stream, call, (q, k, v, q_starts, k_starts, out, lse, workspace))

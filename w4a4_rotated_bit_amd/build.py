@@ -17,9 +17,10 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB_PATH = os.path.join(HERE, "libconvrot.so")
 ARCH = "gfx950"
 
-HIP_SOURCES = ["kernels.hip", "grouped_bf16.hip", "grouped_f16.hip", "norm.hip", "rope.hip", "grouped.hip", "api.hip",
-               "block_api.hip"]
-CXX_SOURCES = ["host.cpp", "block_host.cpp"]
+HIP_SOURCES = ["kernels.hip", "grouped_bf16.hip", "grouped_f16.hip", "prompt_bf16.hip", "prompt_f16.hip", "paged_bf16.hip",
+               "paged_f16.hip", "norm.hip", "rope.hip", "grouped.hip", "cache.hip", "api.hip", "block_api.hip",
+               "attention_api.hip"]
+CXX_SOURCES = ["host.cpp", "block_host.cpp", "attention_host.cpp"]
 
 COMMON = ["-O3", "-fPIC", "-std=c++17", "-Wall", "-I", CSRC, "-I", INCLUDE]
 HIP_FLAGS = ["-x", "hip", f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

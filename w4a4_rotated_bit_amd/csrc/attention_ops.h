@@ -1,0 +1,217 @@
+// attention_ops.h -- plans, launch interface and shared pieces of attention and
+// of the paged cache that it reads.
+#pragma once
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "../../include/convrot.h"
+#include "block_ops.h"
+
+namespace convrot {
+
+constexpr int kMaxHeadWidth = 256;          // channels of a head
+constexpr int kMaxPageSize = 65536;
+constexpr int64_t kMaxBatch = 65535;
+constexpr int64_t kMaxPlaces = (int64_t)1 << 30;   // of one sequence in a cache
+constexpr int64_t kMaxTokenStride = ((int64_t)1 << 24) - 1;   // 64 rows stay within 32-bit byte offsets
+constexpr int kBlock = 32;                  // channels that share a scale
+
+inline bool cache_quantized(int kind) { return kind == CONVROT_CACHE_E4M3 || kind == CONVROT_CACHE_E2M1; }
+// bytes of a row of `dim` values
+inline int64_t cache_row_bytes(int kind, int dim)
+{
+    return kind == CONVROT_CACHE_E4M3 ? dim : kind == CONVROT_CACHE_E2M1 ? dim / 2 : 2 * dim;
+}
+// channels that the kernels compute with
+inline int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
+
+// ---- one token over the pages ----
+constexpr int kPagedHeads = 16;    // query heads of a key head that one workgroup takes (columns of a matrix product)
+constexpr int kPagedTile = 32;     // keys of a wave's step
+constexpr int kPagedWaves = 4;
+constexpr int kPagedUnit = kPagedTile * kPagedWaves;   // keys of a workgroup's step: the unit that work is shared out by
+
+struct PagedPlan {
+    int columns;      // key heads times groups of query heads: each walks a sequence's keys by itself
+    int workgroups;   // that share all units out evenly; 0: one workgroup a sequence and column
+    int64_t slot;     // floats of one partial result
+    int64_t bytes() const { return 2 * (int64_t)workgroups * slot * 4; }
+};
+
+inline PagedPlan paged_plan(const convrot_attention_paged_args& a)
+{
+    PagedPlan p{};
+    const int group = a.q_heads / a.cache.heads;
+    p.columns = a.cache.heads * ((group + kPagedHeads - 1) / kPagedHeads);
+    p.slot = kPagedHeads * (padded_dim(a.cache.head_dim) + 2);
+    const int64_t capacity = a.table_width * a.cache.page_size;
+    if (capacity <= 2 * kPagedUnit) return p;
+    const int64_t units = a.batch * p.columns * ((capacity + kPagedUnit - 1) / kPagedUnit);
+    p.workgroups = (int)std::min<int64_t>(units, 512);
+    return p;
+}
+
+// ---- whole prompts ----
+constexpr int kPromptRows = 128;   // queries of a workgroup: four waves of 32
+constexpr int kPromptKeys = 64;    // keys of a step
+
+struct PromptPlan {
+    int64_t tiles;    // most tiles of kPromptRows queries that the sequences can have
+    int splits;       // workgroups that share the keys of a tile
+    int64_t rows;     // rows of partial results: splits * batch entries * q_tokens * q_heads
+    int64_t bytes(int head_dim) const { return splits > 1 ? rows * (head_dim + 2) * 4 : 0; }
+};
+
+inline PromptPlan prompt_plan(const convrot_attention_args& a)
+{
+    PromptPlan p{};
+    const bool packed = a.q_starts_dev != nullptr;
+    // packed: sum of ceil(len / 128) over the sequences, for any lengths
+    p.tiles = packed ? (a.q_tokens + (kPromptRows - 1) * std::min(a.batch, a.q_tokens)) / kPromptRows
+                     : a.batch * ((a.q_tokens + kPromptRows - 1) / kPromptRows);
+    p.splits = 1;
+    p.rows = p.splits * (packed ? 1 : a.batch) * a.q_tokens * a.q_heads;
+    return p;
+}
+
+}  // namespace convrot
+
+#if defined(__HIPCC__)
+#include <hip/hip_runtime.h>
+
+namespace convrot {
+
+void launch_cache(const convrot_cache_args& a, bool write, hipStream_t s);
+void launch_attention_paged(const convrot_attention_paged_args& a, const PagedPlan& plan, float* partial, hipStream_t s);
+void launch_attention(const convrot_attention_args& a, const PromptPlan& plan, float* partial, hipStream_t s);
+template <typename T>
+void launch_paged_typed(const convrot_attention_paged_args& a, const PagedPlan& plan, float* partial, hipStream_t s);
+template <typename T>
+void launch_prompt_typed(const convrot_attention_args& a, const PromptPlan& plan, float* partial, hipStream_t s);
+
+// ---- device helpers ---------------------------------------------------------
+
+typedef float F4 __attribute__((ext_vector_type(4)));
+typedef float F16v __attribute__((ext_vector_type(16)));
+typedef uint32_t U4 __attribute__((ext_vector_type(4)));
+typedef uint32_t U2 __attribute__((ext_vector_type(2)));
+
+constexpr float kInf = __builtin_inff();
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Two values to a register of two T, rounded to nearest.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    typedef T T2 __attribute__((ext_vector_type(2)));
+    typedef float F2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(F2{a, b}, T2));
+}
+
+// The scale 2^(s - 127) of a block as the conversions take it: they read the
+// exponent field alone, 0 as 2^-127 and 255 as NaN.
+__device__ __forceinline__ float block_scale(uint32_t s) { return __builtin_bit_cast(float, s << 23); }
+
+// Eight consecutive values of a quantized row to four registers of two T: exact
+// in bf16 (four significant bits at most), rounded to nearest in f16 where small.
+template <typename T>
+struct Unpack;
+template <>
+struct Unpack<__bf16> {
+    static __device__ __forceinline__ U4 e2m1(uint32_t c, float s)
+    {
+        return U4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0)),
+                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 1)),
+                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 2)),
+                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 3))};
+    }
+    static __device__ __forceinline__ U4 e4m3(uint32_t lo, uint32_t hi, float s)
+    {
+        return U4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, false)),
+                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, true)),
+                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, false)),
+                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, true))};
+    }
+};
+template <>
+struct Unpack<_Float16> {
+    static __device__ __forceinline__ U4 e2m1(uint32_t c, float s)
+    {
+        return U4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, 0)),
+                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, 1)),
+                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, 2)),
+                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, 3))};
+    }
+    static __device__ __forceinline__ U4 e4m3(uint32_t lo, uint32_t hi, float s)
+    {
+        return U4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, s, false)),
+                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, s, true)),
+                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, s, false)),
+                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, s, true))};
+    }
+};
+
+// v of the lane whose number differs by 32 (HALF) or by 16, beside this lane's
+// own: {v of lanes with that bit clear, v of lanes with it set}.
+struct Pair {
+    uint32_t low, high;
+};
+__device__ __forceinline__ Pair across32(uint32_t v)
+{
+    uint32_t copy = v;
+    asm volatile("" : "+v"(copy));   // a register of its own: swapped with itself it stays as it is
+    const auto r = __builtin_amdgcn_permlane32_swap(v, copy, false, false);
+    return Pair{(uint32_t)r[0], (uint32_t)r[1]};
+}
+__device__ __forceinline__ Pair across16(uint32_t v)
+{
+    uint32_t copy = v;
+    asm volatile("" : "+v"(copy));
+    const auto r = __builtin_amdgcn_permlane16_swap(v, copy, false, false);
+    return Pair{(uint32_t)r[0], (uint32_t)r[1]};
+}
+__device__ __forceinline__ float max32(float v)
+{
+    const Pair p = across32(__builtin_bit_cast(uint32_t, v));
+    return fmaxf(__builtin_bit_cast(float, p.low), __builtin_bit_cast(float, p.high));
+}
+__device__ __forceinline__ float sum32(float v)
+{
+    const Pair p = across32(__builtin_bit_cast(uint32_t, v));
+    return __builtin_bit_cast(float, p.low) + __builtin_bit_cast(float, p.high);
+}
+// over the four lanes that share lane % 16
+__device__ __forceinline__ float max4(float v)
+{
+    const Pair p = across16(__builtin_bit_cast(uint32_t, v));
+    return max32(fmaxf(__builtin_bit_cast(float, p.low), __builtin_bit_cast(float, p.high)));
+}
+__device__ __forceinline__ float sum4(float v)
+{
+    const Pair p = across16(__builtin_bit_cast(uint32_t, v));
+    return sum32(__builtin_bit_cast(float, p.low) + __builtin_bit_cast(float, p.high));
+}
+
+__device__ __forceinline__ int wave_sum(int v)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
+    return v;
+}
+// inclusive sum over the lanes up to this one
+__device__ __forceinline__ int wave_scan(int v)
+{
+    const int lane = __lane_id();
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int up = __shfl_up(v, d);
+        if (lane >= d) v += up;
+    }
+    return v;
+}
+
+}  // namespace convrot
+#endif
