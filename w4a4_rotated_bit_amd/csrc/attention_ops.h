@@ -70,7 +70,10 @@ inline PromptPlan prompt_plan(const convrot_attention_args& a)
     // packed: sum of ceil(len / 128) over the sequences, for any lengths
     p.tiles = packed ? (a.q_tokens + (kPromptRows - 1) * std::min(a.batch, a.q_tokens)) / kPromptRows
                      : a.batch * ((a.q_tokens + kPromptRows - 1) / kPromptRows);
-    p.splits = 1;
+    // Few queries against many keys: the keys of a tile go to several workgroups, as
+    // many as fill the chip (two on a unit), 256 keys each at least.
+    const int64_t groups = std::max<int64_t>(p.tiles * a.q_heads, 1);
+    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({512 / groups, a.k_tokens / 256, 64}));
     p.rows = p.splits * (packed ? 1 : a.batch) * a.q_tokens * a.q_heads;
     return p;
 }

@@ -385,6 +385,39 @@ __global__ __launch_bounds__(256, DIM > 128 ? 1 : 2) void prompt_kernel(PromptPa
         p.a.lse_dev[(kb * p.a.q_tokens + out_row) * p.a.q_heads + head] = sum == 0.f ? -kInf : (m + __log2f(sum)) * kLn2;
 }
 
+// The partial results of each row and head, joined: a wave a row of a head.
+template <typename T>
+__global__ __launch_bounds__(256) void prompt_join_kernel(PromptParams p)
+{
+    const int64_t r = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
+    if (r >= p.rows) return;
+    const int64_t row = r / p.a.q_heads;
+    const int head = (int)(r % p.a.q_heads), lane = threadIdx.x % 64, dim = p.a.head_dim;
+    int64_t b = 0, at = row;
+    if (p.a.q_starts_dev) {   // rows of no sequence stay as they are
+        if (row < starts_at(p.a.q_starts_dev, 0, p.a.q_tokens) || row >= starts_at(p.a.q_starts_dev, p.a.batch, p.a.q_tokens)) return;
+    } else {
+        b = row / p.a.q_tokens;
+        at = row % p.a.q_tokens;
+    }
+    const float* stats = p.partial + p.splits * p.rows * dim + 2 * r;
+    float most = -kInf, total = 0.f;
+    for (int i = 0; i < p.splits; ++i) most = fmaxf(most, stats[2 * i * p.rows]);
+    F4 out{0, 0, 0, 0};
+    const int c = 4 * lane;
+    for (int i = 0; i < p.splits; ++i) {
+        const float m = stats[2 * i * p.rows], f = m == -kInf ? 0.f : exp2_fast(m - most);
+        total += stats[2 * i * p.rows + 1] * f;
+        if (c < dim) out += *(const F4*)(p.partial + (i * p.rows + r) * dim + c) * f;
+    }
+    const float s = total == 0.f ? 0.f : 1.f / total;
+    typedef uint16_t H4 __attribute__((ext_vector_type(4)));
+    if (c < dim)
+        store_chunk<uint16_t, 4>((uint16_t*)p.a.o_dev + b * p.a.o_batch_stride + at * p.a.o_token_stride + head * p.a.o_head_stride + c,
+                                 __builtin_bit_cast(H4, U2{pack2<T>(out[0] * s, out[1] * s), pack2<T>(out[2] * s, out[3] * s)}));
+    if (lane == 0 && p.a.lse_dev) p.a.lse_dev[r] = total == 0.f ? -kInf : (most + __log2f(total)) * kLn2;
+}
+
 template <typename T>
 void launch_prompt_dim(const PromptParams& p, unsigned grid, hipStream_t s)
 {
@@ -412,6 +445,7 @@ void launch_prompt_typed(const convrot_attention_args& a, const PromptPlan& plan
     p.direct = bits % 16 == 0;
     p.scale = a.scale * kLog2e;
     launch_prompt_dim<T>(p, (unsigned)(plan.tiles * a.q_heads * plan.splits), s);
+    if (plan.splits > 1) prompt_join_kernel<T><<<(unsigned)((p.rows + 3) / 4), 256, 0, s>>>(p);
 }
 
 }  // namespace convrot
