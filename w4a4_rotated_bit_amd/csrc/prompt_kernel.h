@@ -18,6 +18,8 @@
 #pragma once
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "attention_ops.h"
 
 namespace convrot {
@@ -191,154 +193,191 @@ __global__ __launch_bounds__(256, DIM > 128 ? 1 : 2) void prompt_kernel(PromptPa
     const int open = least / KEYS;                      // steps without a mask
     const int limit = p.a.causal ? min(row + shift, nk - 1) : nk - 1;    // this lane's last key
 
+    // The scale's sign goes to the queries (exactly), and a scale of 0 makes them
+    // zeros: scores grow with the products.
+    const float scale = p.scale == 0.f ? 1.f : fabsf(p.scale);
+    const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
     U4 q[STEPS];
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
         const int c = i * 16 + half * 8;
-        q[i] = c < dim ? __builtin_bit_cast(U4, load_chunk<uint16_t, 8>((const uint16_t*)q_row + c)) : U4{0, 0, 0, 0};
+        q[i] = c < dim && p.scale != 0.f ? __builtin_bit_cast(U4, load_chunk<uint16_t, 8>((const uint16_t*)q_row + c)) ^ flip : U4{0, 0, 0, 0};
     }
 
     // copies: piece s of a stage holds piece (s % PIECES) ^ (row's permutation) of row s / PIECES
     const auto permuted = [](int r) { return DIM == 64 ? (r >> 1) & 7 : r & 15; };       // keys
     const auto permuted_v = [](int r) { return DIM == 64 ? ((r >> 1) & 1) << 2 : (r & 3) << 2; };
     const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)&shared[0][0][0];
-    const auto issue = [&](int j, int stage) {
-        const int key0 = j * KEYS, rows = nk - key0;
-        const U4 kd = descriptor(k_base + 2 * (int64_t)key0 * p.a.k_token_stride), vd = descriptor(v_base + 2 * (int64_t)key0 * p.a.v_token_stride);
+    uint32_t from_k[COPIES], from_v[COPIES];
 #pragma unroll
-        for (int i = 0; i < COPIES; ++i) {
-            const int s = (wave * COPIES + i) * 64 + lane, r = s / PIECES, pc = s % PIECES;
-            const int ck = pc ^ permuted(r), cv = pc ^ permuted_v(r);
-            const uint32_t ok = r < rows && 8 * ck < dim ? (uint32_t)(2 * r * (int)p.a.k_token_stride + 16 * ck) : kBeyond;
-            const uint32_t ov = r < rows && 8 * cv < dim ? (uint32_t)(2 * r * (int)p.a.v_token_stride + 16 * cv) : kBeyond;
-            const int at = (wave * COPIES + i) * 1024;
-            if (p.direct) {
-                copy16(kd, ok, base + stage * 2 * STAGE + at);
-                copy16(vd, ov, base + stage * 2 * STAGE + STAGE + at);
-            } else {     // rows that do not begin with a multiple of 16 bytes
+    for (int i = 0; i < COPIES; ++i) {
+        const int s = (wave * COPIES + i) * 64 + lane, r = s / PIECES, pc = s % PIECES;
+        const int ck = pc ^ permuted(r), cv = pc ^ permuted_v(r);
+        from_k[i] = 8 * ck < dim ? (uint32_t)(2 * r * (int)p.a.k_token_stride + 16 * ck) : kBeyond;
+        from_v[i] = 8 * cv < dim ? (uint32_t)(2 * r * (int)p.a.v_token_stride + 16 * cv) : kBeyond;
+    }
+    const auto issue = [&](int j, int stage) {
+        const int rows = nk - j * KEYS;
+        const char *k_from = k_base + 2 * (int64_t)(j * KEYS) * p.a.k_token_stride, *v_from = v_base + 2 * (int64_t)(j * KEYS) * p.a.v_token_stride;
+        const uint32_t to = base + stage * 2 * STAGE + wave * COPIES * 1024;
+        if (p.direct) {
+            const U4 kd = descriptor(k_from), vd = descriptor(v_from);
+            if (rows >= KEYS) {
+#pragma unroll
+                for (int i = 0; i < COPIES; ++i) copy16(kd, from_k[i], to + i * 1024);
+#pragma unroll
+                for (int i = 0; i < COPIES; ++i) copy16(vd, from_v[i], to + STAGE + i * 1024);
+            } else {
+#pragma unroll
+                for (int i = 0; i < COPIES; ++i) {
+                    const bool in = ((wave * COPIES + i) * 64 + lane) / PIECES < rows;
+                    copy16(kd, in ? from_k[i] : kBeyond, to + i * 1024);
+                    copy16(vd, in ? from_v[i] : kBeyond, to + STAGE + i * 1024);
+                }
+            }
+        } else {     // rows that do not begin with a multiple of 16 bytes
+#pragma unroll
+            for (int i = 0; i < COPIES; ++i) {
+                const int at = (wave * COPIES + i) * 1024 + 16 * lane;
+                const bool in = ((wave * COPIES + i) * 64 + lane) / PIECES < rows;
                 U4 a{0, 0, 0, 0}, c{0, 0, 0, 0};
-                if (ok != kBeyond) a = __builtin_bit_cast(U4, load_chunk<uint16_t, 8>((const uint16_t*)(k_base + 2 * (int64_t)key0 * p.a.k_token_stride + ok)));
-                if (ov != kBeyond) c = __builtin_bit_cast(U4, load_chunk<uint16_t, 8>((const uint16_t*)(v_base + 2 * (int64_t)key0 * p.a.v_token_stride + ov)));
-                *(U4*)&shared[stage][0][at + 16 * lane] = a;
-                *(U4*)&shared[stage][1][at + 16 * lane] = c;
+                if (in && from_k[i] != kBeyond) a = __builtin_bit_cast(U4, load_chunk<uint16_t, 8>((const uint16_t*)(k_from + from_k[i])));
+                if (in && from_v[i] != kBeyond) c = __builtin_bit_cast(U4, load_chunk<uint16_t, 8>((const uint16_t*)(v_from + from_v[i])));
+                *(U4*)&shared[stage][0][at] = a;
+                *(U4*)&shared[stage][1][at] = c;
             }
         }
+    };
+    // four keys (16 n + 4 half ..) of channel 32 c + lane % 32, and the four 8 behind them
+    const auto values = [&](const char* vs, int n, int c) {
+        typedef short S4 __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) S4 Shared4;
+        U4 v;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = 16 * n + 8 * h + 4 * half + lane / 4 % 4;
+            const int piece = (c * 4 + lane / 16 % 2 * 2 + lane % 4 / 2) ^ permuted_v(r);
+            const U2 u = __builtin_bit_cast(U2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Shared4*)(vs + r * ROW + piece * 16 + lane % 2 * 8)));
+            v[2 * h] = u[0];
+            v[2 * h + 1] = u[1];
+        }
+        return v;
     };
 
     float m = -kInf, sum = 0.f;
     F16v o[TILES];
-    bool careful = false;
-    for (;;) {
+    const auto step = [&](int j, int stage, auto masked, auto careful) {
+        const char *ks = shared[stage][0], *vs = shared[stage][1];
+        // scores: this lane's query against keys 32 kt + 8 (i / 4) + 4 half + i % 4
+        F16v s[2] = {F16v{}, F16v{}};
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt) {
+                const int r = kt * 32 + col;
+                s[kt] = Mfma32<T>::run(*(const U4*)(ks + r * ROW + ((2 * i + half) ^ permuted(r)) * 16), q[i], s[kt]);
+            }
+        const int mine = limit - j * KEYS - 4 * half;    // this lane's last key, from the step's first of its half
+        if constexpr (masked.value) {
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (kt * 32 + 8 * (i / 4) + i % 4 > mine) s[kt][i] = -kInf;
+        }
+        float top = fmaxf(s[0][0], s[1][0]);
+#pragma unroll
+        for (int i = 1; i < 16; ++i) top = fmaxf(fmaxf(top, s[0][i]), s[1][i]);
+        top *= scale;
+        if (__ballot(top > m + 8.f)) {
+            const float next = fmaxf(m, max32(top));
+            const float f = next == -kInf ? 0.f : exp2_fast(m - next);
+            sum *= f;
+#pragma unroll
+            for (int i = 0; i < TILES; ++i) o[i] *= f;
+            m = next;
+        }
+        const float from = m == -kInf ? 0.f : m;
+        U4 w[4];
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                s[kt][i] = exp2_fast(__builtin_fmaf(s[kt][i], scale, -from));
+                sum += s[kt][i];
+            }
+        // weights rounded to T: at most half a step of each, as the outputs are
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i / 4][i % 4] = pack2<T>(s[i / 8][2 * (i % 8)], s[i / 8][2 * (i % 8) + 1]);
+        if constexpr (!careful.value) {
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int c = 0; c < TILES; ++c) o[c] = Mfma32<T>::run(values(vs, n, c), w[n], o[c]);
+        } else {
+            // Values that are no numbers left out of the products, and counted for the
+            // queries that see them: 1 for an infinity, 128 for a negative one, 16384 for a
+            // NaN, each at most 64 times.
+            const uint16_t one = __builtin_bit_cast(uint16_t, (T)1.f), many = __builtin_bit_cast(uint16_t, (T)128.f),
+                           most16 = __builtin_bit_cast(uint16_t, (T)16384.f), top16 = sizeof(T) == 2 && (T)65537.f == (T)65536.f ? 0x7f80 : 0x7c00;
+#pragma unroll
+            for (int c = 0; c < TILES; ++c) {
+                F16v count{};
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    typedef uint16_t H8 __attribute__((ext_vector_type(8)));
+                    H8 v = __builtin_bit_cast(H8, values(vs, n, c)), bad, seen;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint16_t bits = v[e] & 0x7fff;
+                        bad[e] = bits < top16 ? 0 : bits > top16 ? most16 : v[e] >> 15 ? many : one;
+                        if (bits >= top16) v[e] = 0;
+                        seen[e] = 16 * n + 8 * (e / 4) + e % 4 <= mine ? one : 0;
+                    }
+                    o[c] = Mfma32<T>::run(__builtin_bit_cast(U4, v), w[n], o[c]);
+                    count = Mfma32<T>::run(__builtin_bit_cast(U4, bad), __builtin_bit_cast(U4, seen), count);
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int k = (int)count[e];
+                    if (k % 128) o[c][e] += kInf;
+                    if (k / 128 % 128) o[c][e] -= kInf;
+                    if (k / 16384) o[c][e] = __builtin_nanf("");
+                }
+            }
+        }
+    };
+    const auto walk = [&](int from, int to, auto masked, auto careful) {
+        for (int j = from; j < to; ++j) {
+            const int stage = (j - begin) & 1;
+            copies_done();
+            if (j + 1 < end) issue(j + 1, stage ^ 1);
+            step(j, stage, masked, careful);
+        }
+    };
+    const auto reset = [&]() {
         m = -kInf;
         sum = 0.f;
 #pragma unroll
         for (int i = 0; i < TILES; ++i) o[i] = F16v{};
         if (begin < end) issue(begin, 0);
-        for (int j = begin; j < end; ++j) {
-            const int stage = (j - begin) & 1;
-            copies_done();
-            if (j + 1 < end) issue(j + 1, stage ^ 1);
-            const char *ks = shared[stage][0], *vs = shared[stage][1];
-            // scores: this lane's query against keys 32 kt + 8 (i / 4) + 4 half + i % 4
-            F16v s[2] = {F16v{}, F16v{}};
-#pragma unroll
-            for (int i = 0; i < STEPS; ++i)
-#pragma unroll
-                for (int kt = 0; kt < 2; ++kt) {
-                    const int r = kt * 32 + col;
-                    const U4 k = *(const U4*)(ks + r * ROW + ((2 * i + half) ^ permuted(r)) * 16);
-                    s[kt] = Mfma32<T>::run(k, q[i], s[kt]);
-                }
-#pragma unroll
-            for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) s[kt][i] *= p.scale;   // of either sign: before the mask
-            const bool masked = j >= open;
-            if (masked) {
-                const int mine = limit - j * KEYS - 4 * half;
-#pragma unroll
-                for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (kt * 32 + 8 * (i / 4) + i % 4 > mine) s[kt][i] = -kInf;
-            }
-            float top = -kInf;
-#pragma unroll
-            for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) top = fmaxf(top, s[kt][i]);
-            if (__ballot(top > m + 8.f)) {
-                const float next = fmaxf(m, max32(top));
-                const float f = next == -kInf ? 0.f : exp2_fast(m - next);
-                sum *= f;
-#pragma unroll
-                for (int i = 0; i < TILES; ++i) o[i] *= f;
-                m = next;
-            }
-            const float from = m == -kInf ? 0.f : m;
-            U4 w[4];
-#pragma unroll
-            for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    s[kt][i] = exp2_fast(s[kt][i] - from);
-                    sum += s[kt][i];
-                }
-            // weights rounded to T: at most half a step of each, as the outputs are
-#pragma unroll
-            for (int i = 0; i < 16; ++i) w[i / 4][i % 4] = pack2<T>(s[i / 8][2 * (i % 8)], s[i / 8][2 * (i % 8) + 1]);
-            if (!(careful && masked)) {
-#pragma unroll
-                for (int n = 0; n < 4; ++n)
-#pragma unroll
-                    for (int c = 0; c < TILES; ++c) {
-                        typedef short S4 __attribute__((ext_vector_type(4)));
-                        typedef __attribute__((address_space(3))) S4 Shared4;
-                        const int rr = lane / 4 % 4;
-                        U4 v;
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int r = 16 * n + 8 * h + 4 * half + rr;
-                            const int piece = (c * 4 + lane / 16 % 2 * 2 + lane % 4 / 2) ^ permuted_v(r);
-                            const S4 part = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Shared4*)(vs + r * ROW + piece * 16 + lane % 2 * 8));
-                            const U2 u = __builtin_bit_cast(U2, part);
-                            v[2 * h] = u[0];
-                            v[2 * h + 1] = u[1];
-                        }
-                        o[c] = Mfma32<T>::run(v, w[n], o[c]);
-                    }
-            } else {
-                // Key by key, and a query's masked ones left out: a value that is no
-                // number does not reach queries that do not see it.
-                for (int key = 0; key < KEYS; ++key) {
-                    const int kt = key / 32, i = key % 32 / 8 * 4 + key % 4, from_half = key / 4 % 2;
-                    float weight = 0.f;
-#pragma unroll
-                    for (int a = 0; a < 32; ++a)
-                        if (a == kt * 16 + i) weight = (float)(T)s[a / 16][a % 16];
-                    weight = __shfl(weight, from_half * 32 + col);
-                    const bool seen = key <= limit - j * KEYS;
-#pragma unroll
-                    for (int c = 0; c < TILES; ++c)
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const int ch = c * 32 + 8 * (e / 4) + 4 * half + e % 4;
-                            const T v = *(const T*)(vs + key * ROW + ((ch / 8) ^ permuted_v(key)) * 16 + ch % 8 * 2);
-                            if (seen) o[c][e] += weight * (float)v;
-                        }
-                }
-            }
-        }
-        // Weights of 0 times a masked value that is no number leave none behind:
-        // then the rows are computed once more, carefully where keys are masked.
-        if (!p.a.causal || careful || begin >= end) break;
+    };
+    reset();
+    walk(begin, min(end, open), std::false_type{}, std::false_type{});
+    walk(max(begin, open), end, std::true_type{}, std::false_type{});
+    // Weights of 0 times a masked value that is no number leave no number behind:
+    // then the rows are computed once more, carefully where keys are masked.
+    if (p.a.causal && open < end) {
         float check = 0.f;
 #pragma unroll
         for (int c = 0; c < TILES; ++c)
 #pragma unroll
             for (int e = 0; e < 16; ++e) check += o[c][e] * 0.f;
-        if (!__syncthreads_or(!(check == 0.f))) break;
-        careful = true;
+        if (__syncthreads_or(!(check == 0.f))) {
+            reset();
+            walk(begin, min(end, open), std::false_type{}, std::false_type{});
+            walk(max(begin, open), end, std::true_type{}, std::true_type{});
+        }
     }
 
     sum = sum32(sum);
