@@ -207,7 +207,6 @@ __global__ __launch_bounds__(256, DIM > 128 ? 1 : 2) void prompt_kernel(PromptPa
     // copies: piece s of a stage holds piece (s % PIECES) ^ (row's permutation) of row s / PIECES
     const auto permuted = [](int r) { return DIM == 64 ? (r >> 1) & 7 : r & 15; };       // keys
     const auto permuted_v = [](int r) { return DIM == 64 ? ((r >> 1) & 1) << 2 : (r & 3) << 2; };
-    const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)&shared[0][0][0];
     uint32_t from_k[COPIES], from_v[COPIES];
 #pragma unroll
     for (int i = 0; i < COPIES; ++i) {
@@ -216,38 +215,33 @@ __global__ __launch_bounds__(256, DIM > 128 ? 1 : 2) void prompt_kernel(PromptPa
         from_k[i] = 8 * ck < dim ? (uint32_t)(2 * r * (int)p.a.k_token_stride + 16 * ck) : kBeyond;
         from_v[i] = 8 * cv < dim ? (uint32_t)(2 * r * (int)p.a.v_token_stride + 16 * cv) : kBeyond;
     }
-    const auto issue = [&](int j, int stage) {
+    // the 64 rows of step j to shared memory; rows behind the last key as zeros
+    const auto issue = [&](const char* rows_at, int64_t stride, const uint32_t (&from)[COPIES], int j, char* to) {
         const int rows = nk - j * KEYS;
-        const char *k_from = k_base + 2 * (int64_t)(j * KEYS) * p.a.k_token_stride, *v_from = v_base + 2 * (int64_t)(j * KEYS) * p.a.v_token_stride;
-        const uint32_t to = base + stage * 2 * STAGE + wave * COPIES * 1024;
+        const char* at = rows_at + 2 * (int64_t)(j * KEYS) * stride;
         if (p.direct) {
-            const U4 kd = descriptor(k_from), vd = descriptor(v_from);
+            const U4 d = descriptor(at);
+            const uint32_t dest = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)to + wave * COPIES * 1024;
             if (rows >= KEYS) {
 #pragma unroll
-                for (int i = 0; i < COPIES; ++i) copy16(kd, from_k[i], to + i * 1024);
-#pragma unroll
-                for (int i = 0; i < COPIES; ++i) copy16(vd, from_v[i], to + STAGE + i * 1024);
+                for (int i = 0; i < COPIES; ++i) copy16(d, from[i], dest + i * 1024);
             } else {
 #pragma unroll
-                for (int i = 0; i < COPIES; ++i) {
-                    const bool in = ((wave * COPIES + i) * 64 + lane) / PIECES < rows;
-                    copy16(kd, in ? from_k[i] : kBeyond, to + i * 1024);
-                    copy16(vd, in ? from_v[i] : kBeyond, to + STAGE + i * 1024);
-                }
+                for (int i = 0; i < COPIES; ++i)
+                    copy16(d, ((wave * COPIES + i) * 64 + lane) / PIECES < rows ? from[i] : kBeyond, dest + i * 1024);
             }
         } else {     // rows that do not begin with a multiple of 16 bytes
 #pragma unroll
             for (int i = 0; i < COPIES; ++i) {
-                const int at = (wave * COPIES + i) * 1024 + 16 * lane;
                 const bool in = ((wave * COPIES + i) * 64 + lane) / PIECES < rows;
-                U4 a{0, 0, 0, 0}, c{0, 0, 0, 0};
-                if (in && from_k[i] != kBeyond) a = __builtin_bit_cast(U4, load_chunk<uint16_t, 8>((const uint16_t*)(k_from + from_k[i])));
-                if (in && from_v[i] != kBeyond) c = __builtin_bit_cast(U4, load_chunk<uint16_t, 8>((const uint16_t*)(v_from + from_v[i])));
-                *(U4*)&shared[stage][0][at] = a;
-                *(U4*)&shared[stage][1][at] = c;
+                U4 a{0, 0, 0, 0};
+                if (in && from[i] != kBeyond) a = __builtin_bit_cast(U4, load_chunk<uint16_t, 8>((const uint16_t*)(at + from[i])));
+                *(U4*)(to + (wave * COPIES + i) * 1024 + 16 * lane) = a;
             }
         }
     };
+    const auto issue_keys = [&](int j, int stage) { issue(k_base, p.a.k_token_stride, from_k, j, shared[stage][0]); };
+    const auto issue_values = [&](int j, int stage) { issue(v_base, p.a.v_token_stride, from_v, j, shared[stage][1]); };
     // four keys (16 n + 4 half ..) of channel 32 c + lane % 32, and the four 8 behind them
     const auto values = [&](const char* vs, int n, int c) {
         typedef short S4 __attribute__((ext_vector_type(4)));
@@ -266,29 +260,24 @@ __global__ __launch_bounds__(256, DIM > 128 ? 1 : 2) void prompt_kernel(PromptPa
 
     float m = -kInf, sum = 0.f;
     F16v o[TILES];
-    const auto step = [&](int j, int stage, auto masked, auto careful) {
-        const char *ks = shared[stage][0], *vs = shared[stage][1];
-        // scores: this lane's query against keys 32 kt + 8 (i / 4) + 4 half + i % 4
-        F16v s[2] = {F16v{}, F16v{}};
-#pragma unroll
-        for (int i = 0; i < STEPS; ++i)
-#pragma unroll
-            for (int kt = 0; kt < 2; ++kt) {
-                const int r = kt * 32 + col;
-                s[kt] = Mfma32<T>::run(*(const U4*)(ks + r * ROW + ((2 * i + half) ^ permuted(r)) * 16), q[i], s[kt]);
-            }
+    // Scores of step j: this lane's query against keys 32 kt + 8 (i / 4) + 4 half + i % 4.
+    struct Scores {
+        F16v s[2];
+    };
+    const auto product = [&](Scores& x, const char* ks, int i, int kt) {
+        const int r = kt * 32 + col;
+        x.s[kt] = Mfma32<T>::run(*(const U4*)(ks + r * ROW + ((2 * i + half) ^ permuted(r)) * 16), q[i], x.s[kt]);
+    };
+    const auto hide = [&](Scores& x, int j) {
         const int mine = limit - j * KEYS - 4 * half;    // this lane's last key, from the step's first of its half
-        if constexpr (masked.value) {
 #pragma unroll
-            for (int kt = 0; kt < 2; ++kt)
+        for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (kt * 32 + 8 * (i / 4) + i % 4 > mine) s[kt][i] = -kInf;
-        }
-        float top = fmaxf(s[0][0], s[1][0]);
-#pragma unroll
-        for (int i = 1; i < 16; ++i) top = fmaxf(fmaxf(top, s[0][i]), s[1][i]);
-        top *= scale;
+            for (int i = 0; i < 16; ++i)
+                if (kt * 32 + 8 * (i / 4) + i % 4 > mine) x.s[kt][i] = -kInf;
+    };
+    // The running maximum moves when one of these scores exceeds it by 2^8.
+    const auto raise = [&](float top) {
         if (__ballot(top > m + 8.f)) {
             const float next = fmaxf(m, max32(top));
             const float f = next == -kInf ? 0.f : exp2_fast(m - next);
@@ -297,86 +286,137 @@ __global__ __launch_bounds__(256, DIM > 128 ? 1 : 2) void prompt_kernel(PromptPa
             for (int i = 0; i < TILES; ++i) o[i] *= f;
             m = next;
         }
+    };
+    const auto highest = [&](const Scores& x) {
+        float top = fmaxf(x.s[0][0], x.s[1][0]);
+#pragma unroll
+        for (int i = 1; i < 16; ++i) top = fmaxf(fmaxf(top, x.s[0][i]), x.s[1][i]);
+        return top * scale;
+    };
+    const auto weigh = [&](Scores& x, int e, float from) {
+        x.s[e / 16][e % 16] = exp2_fast(__builtin_fmaf(x.s[e / 16][e % 16], scale, -from));
+        sum += x.s[e / 16][e % 16];
+    };
+    // weights rounded to T: at most half a step of each, as the outputs are
+    const auto weights = [&](const Scores& x, int n) {
+        const F16v& s = x.s[n / 2];
+        const int e = n % 2 * 8;
+        return U4{pack2<T>(s[e], s[e + 1]), pack2<T>(s[e + 2], s[e + 3]), pack2<T>(s[e + 4], s[e + 5]), pack2<T>(s[e + 6], s[e + 7])};
+    };
+    constexpr int kLast = 0, kOpen = 1, kMasked = 2;
+
+    // Step j's weights and outputs, between them the scores of step j + 1 (next:
+    // whether there is one, and whether its keys are masked).
+    Scores cur;
+    float top;
+    const auto step = [&](int j, auto next) {
+        const int stage = (j - begin) & 1;
+        copies_done();       // keys of step j + 1, values of step j; nobody reads the other stages any more
+        if (j + 2 < end) issue_keys(j + 2, stage);
+        if (j + 1 < end) issue_values(j + 1, stage ^ 1);
+        raise(top);
         const float from = m == -kInf ? 0.f : m;
+        const char *ks = shared[stage ^ 1][0], *vs = shared[stage][1];
+        Scores y{};
+        constexpr int EACH = 32 / (2 * STEPS) ? 32 / (2 * STEPS) : 1;
+#pragma unroll
+        for (int i = 0; i < 2 * STEPS; ++i) {
+            if constexpr (next.value != kLast) product(y, ks, i / 2, i % 2);
+#pragma unroll
+            for (int e = i * EACH; e < (i + 1) * EACH && e < 32; ++e) weigh(cur, e, from);
+        }
         U4 w[4];
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt)
+        for (int n = 0; n < 4; ++n) w[n] = weights(cur, n);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                s[kt][i] = exp2_fast(__builtin_fmaf(s[kt][i], scale, -from));
-                sum += s[kt][i];
-            }
-        // weights rounded to T: at most half a step of each, as the outputs are
+        for (int n = 0; n < 4; ++n)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) w[i / 4][i % 4] = pack2<T>(s[i / 8][2 * (i % 8)], s[i / 8][2 * (i % 8) + 1]);
-        if constexpr (!careful.value) {
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-#pragma unroll
-                for (int c = 0; c < TILES; ++c) o[c] = Mfma32<T>::run(values(vs, n, c), w[n], o[c]);
-        } else {
-            // Values that are no numbers left out of the products, and counted for the
-            // queries that see them: 1 for an infinity, 128 for a negative one, 16384 for a
-            // NaN, each at most 64 times.
-            const uint16_t one = __builtin_bit_cast(uint16_t, (T)1.f), many = __builtin_bit_cast(uint16_t, (T)128.f),
-                           most16 = __builtin_bit_cast(uint16_t, (T)16384.f), top16 = sizeof(T) == 2 && (T)65537.f == (T)65536.f ? 0x7f80 : 0x7c00;
-#pragma unroll
-            for (int c = 0; c < TILES; ++c) {
-                F16v count{};
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    typedef uint16_t H8 __attribute__((ext_vector_type(8)));
-                    H8 v = __builtin_bit_cast(H8, values(vs, n, c)), bad, seen;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const uint16_t bits = v[e] & 0x7fff;
-                        bad[e] = bits < top16 ? 0 : bits > top16 ? most16 : v[e] >> 15 ? many : one;
-                        if (bits >= top16) v[e] = 0;
-                        seen[e] = 16 * n + 8 * (e / 4) + e % 4 <= mine ? one : 0;
-                    }
-                    o[c] = Mfma32<T>::run(__builtin_bit_cast(U4, v), w[n], o[c]);
-                    count = Mfma32<T>::run(__builtin_bit_cast(U4, bad), __builtin_bit_cast(U4, seen), count);
-                }
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int k = (int)count[e];
-                    if (k % 128) o[c][e] += kInf;
-                    if (k / 128 % 128) o[c][e] -= kInf;
-                    if (k / 16384) o[c][e] = __builtin_nanf("");
-                }
-            }
+            for (int c = 0; c < TILES; ++c) o[c] = Mfma32<T>::run(values(vs, n, c), w[n], o[c]);
+        if constexpr (next.value == kMasked) hide(y, j + 1);
+        if constexpr (next.value != kLast) {
+            cur = y;
+            top = highest(cur);
         }
     };
-    const auto walk = [&](int from, int to, auto masked, auto careful) {
-        for (int j = from; j < to; ++j) {
-            const int stage = (j - begin) & 1;
-            copies_done();
-            if (j + 1 < end) issue(j + 1, stage ^ 1);
-            step(j, stage, masked, careful);
-        }
-    };
-    const auto reset = [&]() {
-        m = -kInf;
-        sum = 0.f;
+    if (begin < end) {
 #pragma unroll
         for (int i = 0; i < TILES; ++i) o[i] = F16v{};
-        if (begin < end) issue(begin, 0);
-    };
-    reset();
-    walk(begin, min(end, open), std::false_type{}, std::false_type{});
-    walk(max(begin, open), end, std::true_type{}, std::false_type{});
+        issue_keys(begin, 0);
+        issue_values(begin, 0);
+        if (begin + 1 < end) issue_keys(begin + 1, 1);
+        copies_done();
+        cur = Scores{};
+#pragma unroll
+        for (int i = 0; i < 2 * STEPS; ++i) product(cur, shared[0][0], i / 2, i % 2);
+        if (begin >= open) hide(cur, begin);
+        top = highest(cur);
+        int j = begin;
+        for (; j + 1 < min(end, open); ++j) step(j, std::integral_constant<int, kOpen>{});
+        for (; j + 1 < end; ++j) step(j, std::integral_constant<int, kMasked>{});
+        step(j, std::integral_constant<int, kLast>{});
+    } else {
+#pragma unroll
+        for (int i = 0; i < TILES; ++i) o[i] = F16v{};
+    }
+
     // Weights of 0 times a masked value that is no number leave no number behind:
-    // then the rows are computed once more, carefully where keys are masked.
-    if (p.a.causal && open < end) {
+    // then the rows are computed once more, step by step, with values that are no
+    // numbers left out of the products, and counted for the queries that see them:
+    // 1 for an infinity, 128 for a negative one, 16384 for a NaN, each at most 64 times.
+    if (p.a.causal && open < end && begin < end) {
         float check = 0.f;
 #pragma unroll
         for (int c = 0; c < TILES; ++c)
 #pragma unroll
             for (int e = 0; e < 16; ++e) check += o[c][e] * 0.f;
         if (__syncthreads_or(!(check == 0.f))) {
-            reset();
-            walk(begin, min(end, open), std::false_type{}, std::false_type{});
-            walk(max(begin, open), end, std::true_type{}, std::true_type{});
+            constexpr uint16_t one = __builtin_bit_cast(uint16_t, (T)1.f), many = __builtin_bit_cast(uint16_t, (T)128.f),
+                               most16 = __builtin_bit_cast(uint16_t, (T)16384.f), top16 = __builtin_bit_cast(uint16_t, (T)kInf);
+            m = -kInf;
+            sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < TILES; ++i) o[i] = F16v{};
+            for (int j = begin; j < end; ++j) {
+                issue_keys(j, 0);
+                issue_values(j, 0);
+                copies_done();
+                cur = Scores{};
+#pragma unroll
+                for (int i = 0; i < 2 * STEPS; ++i) product(cur, shared[0][0], i / 2, i % 2);
+                hide(cur, j);
+                raise(highest(cur));
+                const float from = m == -kInf ? 0.f : m;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) weigh(cur, e, from);
+                const int mine = limit - j * KEYS - 4 * half;
+                const char* vs = shared[0][1];
+#pragma unroll
+                for (int c = 0; c < TILES; ++c) {
+                    F16v count{};
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        typedef uint16_t H8 __attribute__((ext_vector_type(8)));
+                        H8 v = __builtin_bit_cast(H8, values(vs, n, c)), bad, seen;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const uint16_t bits = v[e] & 0x7fff;
+                            bad[e] = bits < top16 ? 0 : bits > top16 ? most16 : v[e] >> 15 ? many : one;
+                            if (bits >= top16) v[e] = 0;
+                            seen[e] = 16 * n + 8 * (e / 4) + e % 4 <= mine ? one : 0;
+                        }
+                        o[c] = Mfma32<T>::run(__builtin_bit_cast(U4, v), weights(cur, n), o[c]);
+                        count = Mfma32<T>::run(__builtin_bit_cast(U4, bad), __builtin_bit_cast(U4, seen), count);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int k = (int)count[e];
+                        if (k % 128) o[c][e] += kInf;
+                        if (k / 128 % 128) o[c][e] -= kInf;
+                        if (k / 16384) o[c][e] = __builtin_nanf("");
+                    }
+                }
+                __syncthreads();     // the next step's rows come to the same place
+            }
         }
     }
 
