@@ -53,11 +53,12 @@ inline PagedPlan paged_plan(const convrot_attention_paged_args& a)
 }
 
 // ---- whole prompts ----
-constexpr int kPromptRows = 128;   // queries of a workgroup: four waves of 32
+constexpr int kPromptRows = 32;    // queries of a wave
 constexpr int kPromptKeys = 64;    // keys of a step
 
 struct PromptPlan {
-    int64_t tiles;    // most tiles of kPromptRows queries that the sequences can have
+    int waves;        // of a workgroup: its tile has 32 queries for each
+    int64_t tiles;    // most tiles that the sequences can have
     int splits;       // workgroups that share the keys of a tile
     int64_t rows;     // rows of partial results: splits * batch entries * q_tokens * q_heads
     int64_t bytes(int head_dim) const { return splits > 1 ? rows * (head_dim + 2) * 4 : 0; }
@@ -67,9 +68,14 @@ inline PromptPlan prompt_plan(const convrot_attention_args& a)
 {
     PromptPlan p{};
     const bool packed = a.q_starts_dev != nullptr;
-    // packed: sum of ceil(len / 128) over the sequences, for any lengths
-    p.tiles = packed ? (a.q_tokens + (kPromptRows - 1) * std::min(a.batch, a.q_tokens)) / kPromptRows
-                     : a.batch * ((a.q_tokens + kPromptRows - 1) / kPromptRows);
+    const auto tiles = [&](int64_t rows) {   // packed: sum of ceil(len / rows) over the sequences, for any lengths
+        return packed ? (a.q_tokens + (rows - 1) * std::min(a.batch, a.q_tokens)) / rows : a.batch * ((a.q_tokens + rows - 1) / rows);
+    };
+    // Eight waves share a copy of the keys among 256 queries, where there are enough of
+    // them in each sequence (16384 causal queries of 32 heads: 2010 against 2050 us) and not
+    // where tiles end in the middle (seven ragged sequences of up to 3001: 226 against 206).
+    p.waves = padded_dim(a.head_dim) == 128 && a.q_tokens >= 4096 * (packed ? a.batch : 1) && tiles(8 * kPromptRows) * a.q_heads >= 512 ? 8 : 4;
+    p.tiles = tiles(p.waves * kPromptRows);
     // Few queries against many keys: the keys of a tile go to several workgroups, as
     // many as fill the chip (two on a unit), 256 keys each at least.
     const int64_t groups = std::max<int64_t>(p.tiles * a.q_heads, 1);
@@ -198,11 +204,21 @@ __device__ __forceinline__ float sum4(float v)
     return sum32(__builtin_bit_cast(float, p.low) + __builtin_bit_cast(float, p.high));
 }
 
+template <int CTRL>
+__device__ __forceinline__ int lane_perm(int v)
+{
+    return __builtin_amdgcn_mov_dpp(v, CTRL, 0xF, 0xF, true);
+}
+// sum over the wave, in all lanes
 __device__ __forceinline__ int wave_sum(int v)
 {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
-    return v;
+    v += lane_perm<0xB1>(v);     // neighbour, other pair of four, other four of eight, other eight of sixteen
+    v += lane_perm<0x4E>(v);
+    v += lane_perm<0x141>(v);
+    v += lane_perm<0x140>(v);
+    const Pair a = across16((uint32_t)v);
+    const Pair b = across32(a.low + a.high);
+    return (int)(b.low + b.high);
 }
 // inclusive sum over the lanes up to this one
 __device__ __forceinline__ int wave_scan(int v)

@@ -48,7 +48,7 @@ struct PromptParams {
     convrot_attention_args a;
     float* partial;      // outputs [splits][rows][head_dim], then maximum and sum [splits][rows][2]
     int64_t tiles, rows;
-    int splits, group, direct;   // heads a key head; whether rows can be copied 16 bytes at a time
+    int splits, waves, group, direct;   // waves a workgroup; heads a key head; whether rows can be copied 16 bytes at a time
     float scale;         // times log2(e)
 };
 
@@ -63,27 +63,20 @@ __device__ __forceinline__ int starts_at(const int* starts, int64_t b, int64_t r
 {
     return min(max(starts[b], 0), (int)rows);
 }
-__device__ __forceinline__ int tiles_of(const PromptParams& p, int64_t b)
+__device__ __forceinline__ int tiles_of(const PromptParams& p, int64_t b, int rows)
 {
     if (b >= p.a.batch) return 0;
     const int n = starts_at(p.a.q_starts_dev, b + 1, p.a.q_tokens) - starts_at(p.a.q_starts_dev, b, p.a.q_tokens);
-    return (max(n, 0) + kPromptRows - 1) / kPromptRows;
-}
-// Tiles whose number within their sequence is `level` or more.
-__device__ __forceinline__ int tiles_from(const PromptParams& p, int level)
-{
-    const int lane = __lane_id();
-    int sum = 0;
-    for (int64_t b = 0; b < p.a.batch; b += 64) sum += wave_sum(max(tiles_of(p, b + lane) - level, 0));
-    return sum;
+    return (max(n, 0) + rows - 1) / rows;
 }
 
-// Tile t of all sequences', those with the highest numbers first: under a
-// causal mask they have the most keys, and what starts last should be short.
-__device__ __forceinline__ bool find_prompt(const PromptParams& p, int64_t t, Prompt& x)
+// Tile t of all sequences'.  Up to 64 sequences, the tiles with the highest numbers
+// come first: under a causal mask they have the most keys, and what starts last
+// should be short.  More sequences follow one another.
+__device__ __forceinline__ bool find_prompt(const PromptParams& p, int64_t t, int rows, Prompt& x)
 {
     if (!p.a.q_starts_dev) {
-        const int per = (int)((p.a.q_tokens + kPromptRows - 1) / kPromptRows);
+        const int per = (int)((p.a.q_tokens + rows - 1) / rows);
         x.b = (int)(t % p.a.batch);
         x.tile = per - 1 - (int)(t / p.a.batch);
         x.q0 = x.k0 = 0;
@@ -92,29 +85,36 @@ __device__ __forceinline__ bool find_prompt(const PromptParams& p, int64_t t, Pr
         return true;
     }
     const int lane = __lane_id();
-    if (t >= tiles_from(p, 0)) return false;
-    int low = 0, high = (int)((p.a.q_tokens + kPromptRows - 1) / kPromptRows);   // tiles_from(low) > t >= tiles_from(high)
-    int above = 0;
-    while (high - low > 1) {
-        const int mid = (low + high) / 2, n = tiles_from(p, mid);
-        if (n > t) low = mid;
-        else high = mid, above = n;
-    }
-    // the (t - above)-th of the sequences that have tile `low`
-    int rank = (int)(t - above);
-    for (int64_t b = 0;; b += 64) {
-        const bool has = tiles_of(p, b + lane) > low;
-        const uint64_t mask = __ballot(has);
-        const int n = __popcll(mask);
-        if (rank < n) {
-            const int before = __popcll(mask & (((uint64_t)1 << lane) - 1));
-            const uint64_t here = __ballot(has && before == rank);
-            x.b = (int)b + __builtin_ctzll(here);
-            break;
+    if (p.a.batch <= 64) {
+        const int n = tiles_of(p, lane, rows);
+        const auto from = [&](int level) { return wave_sum(max(n - level, 0)); };   // tiles numbered `level` or more
+        if (t >= from(0)) return false;
+        int low = 0, high = (int)((p.a.q_tokens + rows - 1) / rows), above = 0;     // from(low) > t >= from(high) = above
+        while (high - low > 1) {
+            const int mid = (low + high) / 2, count = from(mid);
+            if (count > t) low = mid;
+            else high = mid, above = count;
         }
-        rank -= n;
+        // the (t - above)-th of the sequences that have a tile `low`
+        const bool has = n > low;
+        const int before = __popcll(__ballot(has) & (((uint64_t)1 << lane) - 1));
+        x.b = __builtin_ctzll(__ballot(has && before == (int)t - above));
+        x.tile = low;
+    } else {
+        int64_t b = 0;
+        int rank = (int)t;
+        for (;; b += 64) {
+            if (b >= p.a.batch) return false;
+            const int n = tiles_of(p, b + lane, rows), sum = wave_scan(n), all = __builtin_amdgcn_readlane(sum, 63);
+            if (rank < all) {
+                const int l = __builtin_ctzll(__ballot(sum > rank));
+                x.b = (int)b + l;
+                x.tile = __builtin_amdgcn_readlane(sum, l) - 1 - rank;
+                break;
+            }
+            rank -= all;
+        }
     }
-    x.tile = low;
     x.q0 = starts_at(p.a.q_starts_dev, x.b, p.a.q_tokens);
     x.nq = max(starts_at(p.a.q_starts_dev, x.b + 1, p.a.q_tokens) - (int)x.q0, 0);
     x.k0 = starts_at(p.a.k_starts_dev, x.b, p.a.k_tokens);
@@ -133,7 +133,7 @@ __device__ __forceinline__ void copy16(U4 rows, uint32_t offset, uint32_t to)
                  : "v"(offset), "s"(rows), "s"(to)
                  : "memory", "m0");
 }
-// Every copy of this wave has landed, every read of shared memory returned; then all waves meet.
+// Every copy of this wave has landed, every access to shared memory is done; then all waves meet.
 __device__ __forceinline__ void copies_done()
 {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -149,12 +149,14 @@ __device__ __forceinline__ U4 descriptor(const char* base)
     return d;
 }
 
-template <typename T, int DIM>
-__global__ __launch_bounds__(256, DIM > 128 ? 1 : 2) void prompt_kernel(PromptParams p)
+// WAVES: of 32 queries each.
+template <typename T, int DIM, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, DIM > 128 ? 1 : 2) void prompt_kernel(PromptParams p)
 {
     constexpr int KEYS = kPromptKeys, ROW = 2 * DIM, PIECES = DIM / 8;   // bytes and 16-byte pieces of a row
-    constexpr int STAGE = KEYS * ROW, COPIES = KEYS * PIECES / 256, STEPS = DIM / 16, TILES = DIM / 32;
-    __shared__ __attribute__((aligned(16))) char shared[2][2][STAGE];    // stage; keys, values
+    constexpr int STAGE = KEYS * ROW, COPIES = KEYS * PIECES / (64 * WAVES), STEPS = DIM / 16, TILES = DIM / 32;
+    constexpr int ROWS = 32 * WAVES;
+    __shared__ __attribute__((aligned(16))) char shared[2][2][STAGE];    // keys, values; stages
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int col = lane % 32, half = lane / 32;
     const int dim = p.a.head_dim;
@@ -174,9 +176,9 @@ __global__ __launch_bounds__(256, DIM > 128 ? 1 : 2) void prompt_kernel(PromptPa
         t = id / p.a.q_heads;
     }
     Prompt x;
-    if (!find_prompt(p, t, x)) return;
+    if (!find_prompt(p, t, ROWS, x)) return;
     const int b = __builtin_amdgcn_readfirstlane(x.b), nq = __builtin_amdgcn_readfirstlane(x.nq), nk = __builtin_amdgcn_readfirstlane(x.nk);
-    const int first_row = __builtin_amdgcn_readfirstlane(x.tile) * kPromptRows;
+    const int first_row = __builtin_amdgcn_readfirstlane(x.tile) * ROWS;
     const int row = first_row + wave * 32 + col;        // this lane's query
     const int64_t kb = p.a.q_starts_dev ? 0 : b;        // batch entries lie apart unless packed
     const T* q_row = (const T*)p.a.q_dev + kb * p.a.q_batch_stride + (x.q0 + min(row, nq - 1)) * p.a.q_token_stride + head * p.a.q_head_stride;
@@ -185,7 +187,7 @@ __global__ __launch_bounds__(256, DIM > 128 ? 1 : 2) void prompt_kernel(PromptPa
 
     // keys that the rows see: row i those up to i + nk - nq under a causal mask
     const int shift = nk - nq;
-    const int last_row = min(first_row + kPromptRows, nq) - 1;
+    const int last_row = min(first_row + ROWS, nq) - 1;
     const int most = p.a.causal ? min(max(last_row + shift + 1, 0), nk) : nk;            // that any row sees
     const int least = p.a.causal ? min(max(first_row + shift + 1, 0), nk) : nk;          // that every row sees
     const int steps = (most + KEYS - 1) / KEYS;
@@ -240,23 +242,27 @@ __global__ __launch_bounds__(256, DIM > 128 ? 1 : 2) void prompt_kernel(PromptPa
             }
         }
     };
-    const auto issue_keys = [&](int j, int stage) { issue(k_base, p.a.k_token_stride, from_k, j, shared[stage][0]); };
-    const auto issue_values = [&](int j, int stage) { issue(v_base, p.a.v_token_stride, from_v, j, shared[stage][1]); };
-    // four keys (16 n + 4 half ..) of channel 32 c + lane % 32, and the four 8 behind them
-    const auto values = [&](const char* vs, int n, int c) {
-        typedef short S4 __attribute__((ext_vector_type(4)));
-        typedef __attribute__((address_space(3))) S4 Shared4;
-        U4 v;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = 16 * n + 8 * h + 4 * half + lane / 4 % 4;
-            const int piece = (c * 4 + lane / 16 % 2 * 2 + lane % 4 / 2) ^ permuted_v(r);
-            const U2 u = __builtin_bit_cast(U2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Shared4*)(vs + r * ROW + piece * 16 + lane % 2 * 8)));
-            v[2 * h] = u[0];
-            v[2 * h + 1] = u[1];
-        }
-        return v;
+    const auto issue_keys = [&](int j, int stage) { issue(k_base, p.a.k_token_stride, from_k, j, shared[0][stage]); };
+    const auto issue_values = [&](int j, int stage) { issue(v_base, p.a.v_token_stride, from_v, j, shared[1][stage]); };
+    // Shared memory by address: the pieces' permutation is an exclusive or of bits that
+    // the rest of an address leaves clear, so a step's address is one of the lane's own.
+    typedef __attribute__((address_space(3))) const U4 Piece;
+    typedef short S4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) S4 Quarter;
+    const uint32_t key_at = col * ROW + ((half ^ permuted(col)) << 4);
+    const int v_row = 4 * half + lane / 4 % 4;
+    const uint32_t value_at = v_row * ROW + (((lane / 16 % 2 * 2 + lane % 4 / 2) ^ permuted_v(v_row)) << 4) + lane % 2 * 8;
+    // channels 16 i + 8 half .. of key 32 kt + lane % 32
+    const auto key = [&](uint32_t keys, int i, int kt) { return *(Piece*)((keys ^ (i * 32)) + kt * 32 * ROW); };
+    // channel 32 c + lane % 32 of keys 16 n + 4 half .. and of the four 8 behind them
+    const auto value = [&](uint32_t vals, int n, int c) {
+        const uint32_t at = (vals ^ (c * 64)) + n * 16 * ROW;
+        const U2 x = __builtin_bit_cast(U2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Quarter*)at));
+        const U2 y = __builtin_bit_cast(U2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Quarter*)(at + 8 * ROW)));
+        return U4{x[0], x[1], y[0], y[1]};
     };
+    const auto keys_of = [&](int stage) { return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)shared[0][stage] + key_at; };
+    const auto values_of = [&](int stage) { return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)shared[1][stage] + value_at; };
 
     float m = -kInf, sum = 0.f;
     F16v o[TILES];
@@ -264,9 +270,9 @@ __global__ __launch_bounds__(256, DIM > 128 ? 1 : 2) void prompt_kernel(PromptPa
     struct Scores {
         F16v s[2];
     };
-    const auto product = [&](Scores& x, const char* ks, int i, int kt) {
-        const int r = kt * 32 + col;
-        x.s[kt] = Mfma32<T>::run(*(const U4*)(ks + r * ROW + ((2 * i + half) ^ permuted(r)) * 16), q[i], x.s[kt]);
+    const auto product = [&](Scores& x, uint32_t keys) {
+#pragma unroll
+        for (int i = 0; i < 2 * STEPS; ++i) x.s[i % 2] = Mfma32<T>::run(key(keys, i / 2, i % 2), q[i / 2], x.s[i % 2]);
     };
     const auto hide = [&](Scores& x, int j) {
         const int mine = limit - j * KEYS - 4 * half;    // this lane's last key, from the step's first of its half
@@ -306,57 +312,95 @@ __global__ __launch_bounds__(256, DIM > 128 ? 1 : 2) void prompt_kernel(PromptPa
     constexpr int kLast = 0, kOpen = 1, kMasked = 2;
 
     // Step j's weights and outputs, between them the scores of step j + 1 (next:
-    // whether there is one, and whether its keys are masked).
-    Scores cur;
+    // whether there is one, and whether its keys are masked).  The order is written
+    // out, a matrix product a slot: behind it come the vector instructions that fill its
+    // time, and the shared memory read of the product four slots on.
     float top;
-    const auto step = [&](int j, auto next) {
+    const auto step = [&](int j, auto next, Scores& cur, Scores& out) {
         const int stage = (j - begin) & 1;
-        copies_done();       // keys of step j + 1, values of step j; nobody reads the other stages any more
+        // keys of step j + 1 and values of step j are there, and nobody reads the stages of the ones before
+        copies_done();
         if (j + 2 < end) issue_keys(j + 2, stage);
         if (j + 1 < end) issue_values(j + 1, stage ^ 1);
         raise(top);
         const float from = m == -kInf ? 0.f : m;
-        const char *ks = shared[stage ^ 1][0], *vs = shared[stage][1];
-        Scores y{};
-        constexpr int EACH = 32 / (2 * STEPS) ? 32 / (2 * STEPS) : 1;
+        const uint32_t keys = keys_of(stage ^ 1), vals = values_of(stage);
+        constexpr int RING = 4, SCORES = 2 * STEPS, OUTS = 4 * TILES;
+        // weights worked out by the end of slot i: those of the first outputs' keys among the
+        // scores, the others just ahead of theirs
+        constexpr int EARLY = 20;
+        U4 ring[RING], w[4];
+        const auto read = [&](int i) {     // what slot i multiplies
+            if (i < SCORES) return key(keys, i / 2, i % 2);
+            return value(vals, (i - SCORES) / TILES, (i - SCORES) % TILES);
+        };
+        constexpr int FIRST = next.value == kLast ? SCORES : 0;
+        if constexpr (next.value != kLast) out = Scores{};
 #pragma unroll
-        for (int i = 0; i < 2 * STEPS; ++i) {
-            if constexpr (next.value != kLast) product(y, ks, i / 2, i % 2);
+        for (int i = 0; i < RING; ++i) ring[i] = read(FIRST + i);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (next.value == kLast) {
 #pragma unroll
-            for (int e = i * EACH; e < (i + 1) * EACH && e < 32; ++e) weigh(cur, e, from);
+            for (int e = 0; e < EARLY; ++e) weigh(cur, e, from);
+            w[0] = weights(cur, 0);
+            w[1] = weights(cur, 1);
+        } else {
+#pragma unroll
+            for (int i = 0; i < SCORES; ++i) {
+                out.s[i % 2] = Mfma32<T>::run(ring[i % RING], q[i / 2], out.s[i % 2]);
+                ring[i % RING] = read(i + RING);
+#pragma unroll
+                for (int e = i * EARLY / SCORES; e < (i + 1) * EARLY / SCORES; ++e) weigh(cur, e, from);
+                if (i == SCORES - 2) w[0] = weights(cur, 0);
+                if (i == SCORES - 1) w[1] = weights(cur, 1);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if constexpr (next.value == kMasked) hide(out, j + 1);
         }
-        U4 w[4];
+        float high[2] = {-kInf, -kInf};
 #pragma unroll
-        for (int n = 0; n < 4; ++n) w[n] = weights(cur, n);
+        for (int i = 0; i < OUTS; ++i) {
+            const int n = i / TILES, c = i % TILES;
+            o[c] = Mfma32<T>::run(ring[i % RING], w[n], o[c]);
+            if (i + RING < OUTS) ring[i % RING] = read(SCORES + i + RING);
+            // the rest of the weights in the first half, the next scores' maximum in the second
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+            for (int e = EARLY + i * (32 - EARLY) * 2 / OUTS; e < EARLY + (i + 1) * (32 - EARLY) * 2 / OUTS && e < 32; ++e) weigh(cur, e, from);
+            if (i == OUTS / 2 - TILES / 2 - 1) w[2] = weights(cur, 2);
+            if (i == OUTS / 2 - 1) w[3] = weights(cur, 3);
+            if (next.value != kLast && i >= OUTS / 2) {
 #pragma unroll
-            for (int c = 0; c < TILES; ++c) o[c] = Mfma32<T>::run(values(vs, n, c), w[n], o[c]);
-        if constexpr (next.value == kMasked) hide(y, j + 1);
-        if constexpr (next.value != kLast) {
-            cur = y;
-            top = highest(cur);
+                for (int e = (i - OUTS / 2) * 32 / OUTS; e < (i + 1 - OUTS / 2) * 32 / OUTS; ++e) high[e % 2] = fmaxf(fmaxf(high[e % 2], out.s[0][e]), out.s[1][e]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
+        if constexpr (next.value != kLast) top = fmaxf(high[0], high[1]) * scale;
     };
-    if (begin < end) {
 #pragma unroll
-        for (int i = 0; i < TILES; ++i) o[i] = F16v{};
+    for (int i = 0; i < TILES; ++i) o[i] = F16v{};
+    if (begin < end) {
+        Scores cur{}, out;
         issue_keys(begin, 0);
         issue_values(begin, 0);
         if (begin + 1 < end) issue_keys(begin + 1, 1);
         copies_done();
-        cur = Scores{};
-#pragma unroll
-        for (int i = 0; i < 2 * STEPS; ++i) product(cur, shared[0][0], i / 2, i % 2);
+        product(cur, keys_of(0));
         if (begin >= open) hide(cur, begin);
         top = highest(cur);
         int j = begin;
-        for (; j + 1 < min(end, open); ++j) step(j, std::integral_constant<int, kOpen>{});
-        for (; j + 1 < end; ++j) step(j, std::integral_constant<int, kMasked>{});
-        step(j, std::integral_constant<int, kLast>{});
-    } else {
-#pragma unroll
-        for (int i = 0; i < TILES; ++i) o[i] = F16v{};
+        for (; j + 2 < min(end, open); j += 2) {
+            step(j, std::integral_constant<int, kOpen>{}, cur, out);
+            step(j + 1, std::integral_constant<int, kOpen>{}, out, cur);
+        }
+        for (; j + 1 < min(end, open); ++j) {
+            step(j, std::integral_constant<int, kOpen>{}, cur, out);
+            cur = out;
+        }
+        for (; j + 1 < end; ++j) {
+            step(j, std::integral_constant<int, kMasked>{}, cur, out);
+            cur = out;
+        }
+        step(j, std::integral_constant<int, kLast>{}, cur, out);
     }
 
     // Weights of 0 times a masked value that is no number leave no number behind:
@@ -380,23 +424,21 @@ __global__ __launch_bounds__(256, DIM > 128 ? 1 : 2) void prompt_kernel(PromptPa
                 issue_keys(j, 0);
                 issue_values(j, 0);
                 copies_done();
-                cur = Scores{};
-#pragma unroll
-                for (int i = 0; i < 2 * STEPS; ++i) product(cur, shared[0][0], i / 2, i % 2);
+                Scores cur{};
+                product(cur, keys_of(0));
                 hide(cur, j);
                 raise(highest(cur));
                 const float from = m == -kInf ? 0.f : m;
 #pragma unroll
                 for (int e = 0; e < 32; ++e) weigh(cur, e, from);
                 const int mine = limit - j * KEYS - 4 * half;
-                const char* vs = shared[0][1];
 #pragma unroll
                 for (int c = 0; c < TILES; ++c) {
                     F16v count{};
 #pragma unroll
                     for (int n = 0; n < 4; ++n) {
                         typedef uint16_t H8 __attribute__((ext_vector_type(8)));
-                        H8 v = __builtin_bit_cast(H8, values(vs, n, c)), bad, seen;
+                        H8 v = __builtin_bit_cast(H8, value(values_of(0), n, c)), bad, seen;
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             const uint16_t bits = v[e] & 0x7fff;
@@ -501,9 +543,13 @@ template <typename T>
 void launch_prompt_dim(const PromptParams& p, unsigned grid, hipStream_t s)
 {
     switch (padded_dim(p.a.head_dim)) {
-    case 64: prompt_kernel<T, 64><<<grid, 256, 0, s>>>(p); break;
-    case 128: prompt_kernel<T, 128><<<grid, 256, 0, s>>>(p); break;
-    default: prompt_kernel<T, 256><<<grid, 256, 0, s>>>(p); break;
+    case 64:
+        prompt_kernel<T, 64, 4><<<grid, 256, 0, s>>>(p);
+        break;
+    case 128:
+        p.waves == 8 ? prompt_kernel<T, 128, 8><<<grid, 512, 0, s>>>(p) : prompt_kernel<T, 128, 4><<<grid, 256, 0, s>>>(p);
+        break;
+    default: prompt_kernel<T, 256, 4><<<grid, 256, 0, s>>>(p); break;
     }
 }
 
@@ -517,6 +563,7 @@ void launch_prompt_typed(const convrot_attention_args& a, const PromptPlan& plan
     p.partial = partial;
     p.tiles = plan.tiles;
     p.splits = plan.splits;
+    p.waves = plan.waves;
     p.rows = plan.rows / plan.splits;
     p.group = a.q_heads / a.k_heads;
     const uint64_t bits = (uint64_t)a.k_dev | (uint64_t)a.v_dev | 2 * (uint64_t)(a.k_batch_stride | a.k_token_stride | a.k_head_stride |
