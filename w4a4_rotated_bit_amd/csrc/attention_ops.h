@@ -64,6 +64,16 @@ struct PromptPlan {
     int64_t bytes(int head_dim) const { return splits > 1 ? rows * (head_dim + 2) * 4 : 0; }
 };
 
+// Whether rows of keys and values can be copied in pieces of 16 bytes, with the end of
+// the last one as the only bound.
+inline bool prompt_direct(const convrot_attention_args& a)
+{
+    const uint64_t bits = (uint64_t)a.k_dev | (uint64_t)a.v_dev |
+                          2 * (uint64_t)(a.k_batch_stride | a.k_token_stride | a.k_head_stride | a.v_batch_stride |
+                                         a.v_token_stride | a.v_head_stride);
+    return bits % 16 == 0 && a.k_token_stride >= a.head_dim && a.v_token_stride >= a.head_dim;
+}
+
 inline PromptPlan prompt_plan(const convrot_attention_args& a)
 {
     PromptPlan p{};
@@ -74,7 +84,7 @@ inline PromptPlan prompt_plan(const convrot_attention_args& a)
     // Eight waves share a copy of the keys among 256 queries, where there are enough of
     // them in each sequence (16384 causal queries of 32 heads: 2010 against 2050 us) and not
     // where tiles end in the middle (seven ragged sequences of up to 3001: 226 against 206).
-    p.waves = padded_dim(a.head_dim) == 128 && a.q_tokens >= 4096 * (packed ? a.batch : 1) && tiles(8 * kPromptRows) * a.q_heads >= 512 ? 8 : 4;
+    p.waves = prompt_direct(a) && padded_dim(a.head_dim) == 128 && a.q_tokens >= 4096 * (packed ? a.batch : 1) && tiles(8 * kPromptRows) * a.q_heads >= 512 ? 8 : 4;
     p.tiles = tiles(p.waves * kPromptRows);
     // Few queries against many keys: the keys of a tile go to several workgroups, as
     // many as fill the chip (two on a unit), 256 keys each at least.

@@ -138,19 +138,22 @@ __device__ __forceinline__ void copies_done()
 {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
-__device__ __forceinline__ U4 descriptor(const char* base)
+// Of `bytes` bytes from base; what lies behind them reads as zeros.
+__device__ __forceinline__ U4 descriptor(const char* base, uint32_t bytes)
 {
     const uint64_t at = (uint64_t)base;
     U4 d;
     d[0] = __builtin_amdgcn_readfirstlane((uint32_t)at);
     d[1] = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32) & 0xffffu);
-    d[2] = kBeyond;
+    d[2] = __builtin_amdgcn_readfirstlane(bytes);
     d[3] = 0x20000;
     return d;
 }
 
-// WAVES: of 32 queries each.
-template <typename T, int DIM, int WAVES>
+// WAVES: of 32 queries each.  DIRECT: keys and values are copied straight to shared
+// memory; otherwise (rows that do not begin with a multiple of 16 bytes, or overlap) by
+// way of registers.
+template <typename T, int DIM, int WAVES, bool DIRECT>
 __global__ __launch_bounds__(64 * WAVES, DIM > 128 ? 1 : 2) void prompt_kernel(PromptParams p)
 {
     constexpr int KEYS = kPromptKeys, ROW = 2 * DIM, PIECES = DIM / 8;   // bytes and 16-byte pieces of a row
@@ -217,33 +220,48 @@ __global__ __launch_bounds__(64 * WAVES, DIM > 128 ? 1 : 2) void prompt_kernel(P
         from_k[i] = 8 * ck < dim ? (uint32_t)(2 * r * (int)p.a.k_token_stride + 16 * ck) : kBeyond;
         from_v[i] = 8 * cv < dim ? (uint32_t)(2 * r * (int)p.a.v_token_stride + 16 * cv) : kBeyond;
     }
-    // the 64 rows of step j to shared memory; rows behind the last key as zeros
-    const auto issue = [&](const char* rows_at, int64_t stride, const uint32_t (&from)[COPIES], int j, char* to) {
+    // The 64 rows of a step to a stage of shared memory, rows behind the last key as
+    // zeros, in COPIES pieces a wave.
+    struct Source {
+        U4 rows;
+        uint32_t to;
+    };
+    const auto source = [&](const char* rows_at, int64_t stride, int j, const char* to) {
+        const int rows = min(max(nk - j * KEYS, 0), KEYS);
+        return Source{descriptor(rows_at + 2 * (int64_t)(j * KEYS) * stride, (uint32_t)(2 * rows * (int)stride)),
+                      (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)to + wave * COPIES * 1024};
+    };
+    const auto by_registers = [&](const char* rows_at, int64_t stride, const uint32_t (&from)[COPIES], int j, char* to) {
         const int rows = nk - j * KEYS;
         const char* at = rows_at + 2 * (int64_t)(j * KEYS) * stride;
-        if (p.direct) {
-            const U4 d = descriptor(at);
-            const uint32_t dest = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)to + wave * COPIES * 1024;
-            if (rows >= KEYS) {
 #pragma unroll
-                for (int i = 0; i < COPIES; ++i) copy16(d, from[i], dest + i * 1024);
-            } else {
-#pragma unroll
-                for (int i = 0; i < COPIES; ++i)
-                    copy16(d, ((wave * COPIES + i) * 64 + lane) / PIECES < rows ? from[i] : kBeyond, dest + i * 1024);
-            }
-        } else {     // rows that do not begin with a multiple of 16 bytes
-#pragma unroll
-            for (int i = 0; i < COPIES; ++i) {
-                const bool in = ((wave * COPIES + i) * 64 + lane) / PIECES < rows;
-                U4 a{0, 0, 0, 0};
-                if (in && from[i] != kBeyond) a = __builtin_bit_cast(U4, load_chunk<uint16_t, 8>((const uint16_t*)(at + from[i])));
-                *(U4*)(to + (wave * COPIES + i) * 1024 + 16 * lane) = a;
-            }
+        for (int i = 0; i < COPIES; ++i) {
+            const bool in = ((wave * COPIES + i) * 64 + lane) / PIECES < rows;
+            U4 a{0, 0, 0, 0};
+            if (in && from[i] != kBeyond) a = __builtin_bit_cast(U4, load_chunk<uint16_t, 8>((const uint16_t*)(at + from[i])));
+            *(U4*)(to + (wave * COPIES + i) * 1024 + 16 * lane) = a;
         }
     };
-    const auto issue_keys = [&](int j, int stage) { issue(k_base, p.a.k_token_stride, from_k, j, shared[0][stage]); };
-    const auto issue_values = [&](int j, int stage) { issue(v_base, p.a.v_token_stride, from_v, j, shared[1][stage]); };
+    const auto keys_from = [&](int j, int stage) { return source(k_base, p.a.k_token_stride, j, shared[0][stage]); };
+    const auto values_from = [&](int j, int stage) { return source(v_base, p.a.v_token_stride, j, shared[1][stage]); };
+    const auto issue_keys = [&](int j, int stage) {
+        if constexpr (DIRECT) {
+            const Source s = keys_from(j, stage);
+#pragma unroll
+            for (int i = 0; i < COPIES; ++i) copy16(s.rows, from_k[i], s.to + i * 1024);
+        } else {
+            by_registers(k_base, p.a.k_token_stride, from_k, j, shared[0][stage]);
+        }
+    };
+    const auto issue_values = [&](int j, int stage) {
+        if constexpr (DIRECT) {
+            const Source s = values_from(j, stage);
+#pragma unroll
+            for (int i = 0; i < COPIES; ++i) copy16(s.rows, from_v[i], s.to + i * 1024);
+        } else {
+            by_registers(v_base, p.a.v_token_stride, from_v, j, shared[1][stage]);
+        }
+    };
     // Shared memory by address: the pieces' permutation is an exclusive or of bits that
     // the rest of an address leaves clear, so a step's address is one of the lane's own.
     typedef __attribute__((address_space(3))) const U4 Piece;
@@ -312,16 +330,21 @@ __global__ __launch_bounds__(64 * WAVES, DIM > 128 ? 1 : 2) void prompt_kernel(P
     constexpr int kLast = 0, kOpen = 1, kMasked = 2;
 
     // Step j's weights and outputs, between them the scores of step j + 1 (next:
-    // whether there is one, and whether its keys are masked).  The order is written
-    // out, a matrix product a slot: behind it come the vector instructions that fill its
-    // time, and the shared memory read of the product four slots on.
+    // whether there is one, and whether its keys are masked) and the copies of the steps
+    // behind it (beyond the last one: zeros).  The order is written out, a matrix product a
+    // slot: behind it come the vector instructions that fill its time, the shared memory
+    // read of the product four slots on, and now and then a copy: issued one after the
+    // other they would hold the wave up.
     float top;
     const auto step = [&](int j, auto next, Scores& cur, Scores& out) {
         const int stage = (j - begin) & 1;
         // keys of step j + 1 and values of step j are there, and nobody reads the stages of the ones before
         copies_done();
-        if (j + 2 < end) issue_keys(j + 2, stage);
-        if (j + 1 < end) issue_values(j + 1, stage ^ 1);
+        if constexpr (!DIRECT && next.value != kLast) {
+            issue_keys(j + 2, stage);
+            issue_values(j + 1, stage ^ 1);
+        }
+        const Source next_keys = keys_from(j + 2, stage), next_values = values_from(j + 1, stage ^ 1);
         raise(top);
         const float from = m == -kInf ? 0.f : m;
         const uint32_t keys = keys_of(stage ^ 1), vals = values_of(stage);
@@ -330,6 +353,19 @@ __global__ __launch_bounds__(64 * WAVES, DIM > 128 ? 1 : 2) void prompt_kernel(P
         // scores, the others just ahead of theirs
         constexpr int EARLY = 20;
         U4 ring[RING], w[4];
+        float sums[2] = {0.f, 0.f};
+        // An element's three instructions, slots apart so that none waits for the one before
+        // it; its exponential belongs to the slot `at`.
+        const auto weigh_in = [&](int slot) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+                const int at = e < EARLY ? 1 + e * (SCORES - 2) / EARLY : SCORES + (e - EARLY) * OUTS / 2 / (32 - EARLY);
+                const float s = cur.s[e / 16][e % 16];
+                if (at - 1 == slot) cur.s[e / 16][e % 16] = __builtin_fmaf(s, scale, -from);
+                if (at == slot) cur.s[e / 16][e % 16] = exp2_fast(s);
+                if (at + 1 == slot) sums[e % 2] += s;
+            }
+        };
         const auto read = [&](int i) {     // what slot i multiplies
             if (i < SCORES) return key(keys, i / 2, i % 2);
             return value(vals, (i - SCORES) / TILES, (i - SCORES) % TILES);
@@ -341,16 +377,23 @@ __global__ __launch_bounds__(64 * WAVES, DIM > 128 ? 1 : 2) void prompt_kernel(P
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (next.value == kLast) {
 #pragma unroll
-            for (int e = 0; e < EARLY; ++e) weigh(cur, e, from);
-            w[0] = weights(cur, 0);
-            w[1] = weights(cur, 1);
+            for (int i = 0; i < SCORES; ++i) {
+                weigh_in(i);
+                if (i == SCORES - 1) w[0] = weights(cur, 0), w[1] = weights(cur, 1);
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < SCORES; ++i) {
                 out.s[i % 2] = Mfma32<T>::run(ring[i % RING], q[i / 2], out.s[i % 2]);
                 ring[i % RING] = read(i + RING);
+                if constexpr (DIRECT) {
 #pragma unroll
-                for (int e = i * EARLY / SCORES; e < (i + 1) * EARLY / SCORES; ++e) weigh(cur, e, from);
+                    for (int k = i * 2 * COPIES / SCORES; k < (i + 1) * 2 * COPIES / SCORES; ++k) {
+                        if (k < COPIES) copy16(next_keys.rows, from_k[k % COPIES], next_keys.to + k % COPIES * 1024);
+                        else copy16(next_values.rows, from_v[k % COPIES], next_values.to + k % COPIES * 1024);
+                    }
+                }
+                weigh_in(i);
                 if (i == SCORES - 2) w[0] = weights(cur, 0);
                 if (i == SCORES - 1) w[1] = weights(cur, 1);
                 __builtin_amdgcn_sched_barrier(0);
@@ -364,8 +407,7 @@ __global__ __launch_bounds__(64 * WAVES, DIM > 128 ? 1 : 2) void prompt_kernel(P
             o[c] = Mfma32<T>::run(ring[i % RING], w[n], o[c]);
             if (i + RING < OUTS) ring[i % RING] = read(SCORES + i + RING);
             // the rest of the weights in the first half, the next scores' maximum in the second
-#pragma unroll
-            for (int e = EARLY + i * (32 - EARLY) * 2 / OUTS; e < EARLY + (i + 1) * (32 - EARLY) * 2 / OUTS && e < 32; ++e) weigh(cur, e, from);
+            weigh_in(SCORES + i);
             if (i == OUTS / 2 - TILES / 2 - 1) w[2] = weights(cur, 2);
             if (i == OUTS / 2 - 1) w[3] = weights(cur, 3);
             if (next.value != kLast && i >= OUTS / 2) {
@@ -374,6 +416,7 @@ __global__ __launch_bounds__(64 * WAVES, DIM > 128 ? 1 : 2) void prompt_kernel(P
             }
             __builtin_amdgcn_sched_barrier(0);
         }
+        sum += sums[0] + sums[1];
         if constexpr (next.value != kLast) top = fmaxf(high[0], high[1]) * scale;
     };
 #pragma unroll
@@ -382,7 +425,7 @@ __global__ __launch_bounds__(64 * WAVES, DIM > 128 ? 1 : 2) void prompt_kernel(P
         Scores cur{}, out;
         issue_keys(begin, 0);
         issue_values(begin, 0);
-        if (begin + 1 < end) issue_keys(begin + 1, 1);
+        issue_keys(begin + 1, 1);
         copies_done();
         product(cur, keys_of(0));
         if (begin >= open) hide(cur, begin);
@@ -544,12 +587,15 @@ void launch_prompt_dim(const PromptParams& p, unsigned grid, hipStream_t s)
 {
     switch (padded_dim(p.a.head_dim)) {
     case 64:
-        prompt_kernel<T, 64, 4><<<grid, 256, 0, s>>>(p);
+        p.direct ? prompt_kernel<T, 64, 4, true><<<grid, 256, 0, s>>>(p) : prompt_kernel<T, 64, 4, false><<<grid, 256, 0, s>>>(p);
         break;
     case 128:
-        p.waves == 8 ? prompt_kernel<T, 128, 8><<<grid, 512, 0, s>>>(p) : prompt_kernel<T, 128, 4><<<grid, 256, 0, s>>>(p);
+        if (p.waves == 8) prompt_kernel<T, 128, 8, true><<<grid, 512, 0, s>>>(p);
+        else p.direct ? prompt_kernel<T, 128, 4, true><<<grid, 256, 0, s>>>(p) : prompt_kernel<T, 128, 4, false><<<grid, 256, 0, s>>>(p);
         break;
-    default: prompt_kernel<T, 256, 4><<<grid, 256, 0, s>>>(p); break;
+    default:
+        p.direct ? prompt_kernel<T, 256, 4, true><<<grid, 256, 0, s>>>(p) : prompt_kernel<T, 256, 4, false><<<grid, 256, 0, s>>>(p);
+        break;
     }
 }
 
@@ -566,9 +612,7 @@ void launch_prompt_typed(const convrot_attention_args& a, const PromptPlan& plan
     p.waves = plan.waves;
     p.rows = plan.rows / plan.splits;
     p.group = a.q_heads / a.k_heads;
-    const uint64_t bits = (uint64_t)a.k_dev | (uint64_t)a.v_dev | 2 * (uint64_t)(a.k_batch_stride | a.k_token_stride | a.k_head_stride |
-                                                                                  a.v_batch_stride | a.v_token_stride | a.v_head_stride);
-    p.direct = bits % 16 == 0;
+    p.direct = prompt_direct(a);
     p.scale = a.scale * kLog2e;
     launch_prompt_dim<T>(p, (unsigned)(plan.tiles * a.q_heads * plan.splits), s);
     if (plan.splits > 1) prompt_join_kernel<T><<<(unsigned)((p.rows + 3) / 4), 256, 0, s>>>(p);
