@@ -31,6 +31,7 @@ constexpr int kPagedHeads = 16;    // query heads of a key head that one workgro
 constexpr int kPagedTile = 32;     // keys of a wave's step
 constexpr int kPagedWaves = 4;
 constexpr int kPagedUnit = kPagedTile * kPagedWaves;   // keys of a workgroup's step: the unit that work is shared out by
+constexpr int kPagedShares = 512;  // most workgroups that share the units: two on each compute unit
 
 struct PagedPlan {
     int columns;      // key heads times groups of query heads: each walks a sequence's keys by itself
@@ -48,13 +49,14 @@ inline PagedPlan paged_plan(const convrot_attention_paged_args& a)
     const int64_t capacity = a.table_width * a.cache.page_size;
     if (capacity <= 2 * kPagedUnit) return p;
     const int64_t units = a.batch * p.columns * ((capacity + kPagedUnit - 1) / kPagedUnit);
-    p.workgroups = (int)std::min<int64_t>(units, 512);
+    p.workgroups = (int)std::min<int64_t>(units, kPagedShares);
     return p;
 }
 
 // ---- whole prompts ----
 constexpr int kPromptRows = 32;    // queries of a wave
 constexpr int kPromptKeys = 64;    // keys of a step
+constexpr int kPromptSplits = 64;  // most workgroups that share a tile's keys: a lane each when they are joined
 
 struct PromptPlan {
     int waves;        // of a workgroup: its tile has 32 queries for each
@@ -84,12 +86,12 @@ inline PromptPlan prompt_plan(const convrot_attention_args& a)
     // Eight waves share a copy of the keys among 256 queries, where there are enough of
     // them in each sequence (16384 causal queries of 32 heads: 2010 against 2050 us) and not
     // where tiles end in the middle (seven ragged sequences of up to 3001: 226 against 206).
-    p.waves = prompt_direct(a) && padded_dim(a.head_dim) == 128 && a.q_tokens >= 4096 * (packed ? a.batch : 1) && tiles(8 * kPromptRows) * a.q_heads >= 512 ? 8 : 4;
+    p.waves = prompt_direct(a) && a.head_dim > 96 && a.head_dim <= 128 && a.q_tokens >= 4096 * (packed ? a.batch : 1) && tiles(8 * kPromptRows) * a.q_heads >= 512 ? 8 : 4;
     p.tiles = tiles(p.waves * kPromptRows);
     // Few queries against many keys: the keys of a tile go to several workgroups, as
-    // many as fill the chip (two on a unit), 256 keys each at least.
+    // many as fill the chip (two on each compute unit), 256 keys each at least.
     const int64_t groups = std::max<int64_t>(p.tiles * a.q_heads, 1);
-    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({512 / groups, a.k_tokens / 256, 64}));
+    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({512 / groups, a.k_tokens / 256, kPromptSplits}));
     p.rows = p.splits * (packed ? 1 : a.batch) * a.q_tokens * a.q_heads;
     return p;
 }

@@ -453,15 +453,15 @@ __global__ __launch_bounds__(64 * kPagedWaves, 2) void paged_kernel(PagedParams 
 template <typename T>
 __global__ __launch_bounds__(256) void paged_join_kernel(PagedParams p, int pitch)
 {
+    __shared__ float factors[kPagedHeads][kPagedShares + 1], scales[kPagedHeads];
+    __shared__ F4 sums[256];
     const int b = blockIdx.x / p.columns, column = blockIdx.x % p.columns;
     const int head = column / p.groups, part = column % p.groups;
     const int heads = min(p.group - part * kPagedHeads, kPagedHeads), q_head = head * p.group + part * kPagedHeads;
-    const int dim = p.a.cache.head_dim, lane = __lane_id();
-    const int length = length_of(p, b);
-    const int mine = units_of(length);
-    int w0 = 0, w1 = -1;
+    const int dim = p.a.cache.head_dim, lane = __lane_id(), wave = threadIdx.x / 64;
+    const int mine = units_of(length_of(p, b));
+    int w0 = 0, count = 0, shares = 0;
     int64_t units = 0, u0 = 0;
-    int shares = 0;
     if (mine > 0) {
         int64_t before = 0;
         for (int c = 0; c < p.a.batch; c += 64) {
@@ -473,29 +473,60 @@ __global__ __launch_bounds__(256) void paged_join_kernel(PagedParams p, int pitc
         shares = sharing(p, units);
         u0 = before * p.columns + (int64_t)column * mine;
         w0 = share_of(units, shares, u0);
-        w1 = share_of(units, shares, u0 + mine - 1);
-        if (w0 == w1) return;   // one workgroup had all of it, and wrote the outputs
+        count = share_of(units, shares, u0 + mine - 1) - w0 + 1;
+        if (count == 1) return;   // one workgroup had all of it, and wrote the outputs
     }
     // the first part is its workgroup's first one if that workgroup begins here
-    const float* slot0 = p.partial + (2 * (int64_t)w0 + (mine > 0 && share_begin(units, shares, w0) == u0 ? 0 : 1)) * p.slot;
-    for (int i = threadIdx.x; i < heads * (dim / 4); i += 256) {
-        const int h = i / (dim / 4), c = i % (dim / 4) * 4;
+    const bool begins = count > 0 && share_begin(units, shares, w0) == u0;
+    const auto slot = [&](int i) { return p.partial + (2 * (int64_t)(w0 + i) + (i == 0 && !begins ? 1 : 0)) * p.slot; };
+    // a wave a head: what each part counts for
+    for (int h = wave; h < heads; h += 4) {
         float most = -kInf, total = 0.f;
-        F4 out{0, 0, 0, 0};
-        for (int w = w0; w <= w1; ++w) most = fmaxf(most, (w == w0 ? slot0 : p.partial + 2 * (int64_t)w * p.slot)[2 * h]);
-        for (int w = w0; w <= w1; ++w) {
-            const float* s = w == w0 ? slot0 : p.partial + 2 * (int64_t)w * p.slot;
-            const float f = s[2 * h] == -kInf ? 0.f : exp2_fast(s[2 * h] - most);
-            total += s[2 * h + 1] * f;
-            out += *(const F4*)(s + 2 * kPagedHeads + h * pitch + c) * f;
+        for (int i = lane; i < count; i += 64) most = fmaxf(most, slot(i)[2 * h]);
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) most = fmaxf(most, __shfl_xor(most, d));
+        for (int i = lane; i < count; i += 64) {
+            const float m = slot(i)[2 * h], f = m == -kInf ? 0.f : exp2_fast(m - most);
+            factors[h][i] = f;
+            total += slot(i)[2 * h + 1] * f;
         }
-        const float r = total == 0.f ? 0.f : 1.f / total;
-        U2 packed{pack2<T>(out[0] * r, out[1] * r), pack2<T>(out[2] * r, out[3] * r)};
-        typedef uint16_t H4 __attribute__((ext_vector_type(4)));
-        store_chunk<uint16_t, 4>((uint16_t*)p.a.o_dev + b * p.a.o_batch_stride + (q_head + h) * p.a.o_head_stride + c,
-                                 __builtin_bit_cast(H4, packed));
-        if (c == 0 && p.a.lse_dev)
-            p.a.lse_dev[(int64_t)b * p.a.q_heads + q_head + h] = total == 0.f ? -kInf : (most + __log2f(total)) * kLn2;
+        total = lane_sum<64>(total);
+        if (lane == 0) {
+            scales[h] = total == 0.f ? 0.f : 1.f / total;
+            if (p.a.lse_dev) p.a.lse_dev[(int64_t)b * p.a.q_heads + q_head + h] = total == 0.f ? -kInf : (most + __log2f(total)) * kLn2;
+        }
+    }
+    __syncthreads();
+    // four channels a thread; threads left over share the parts
+    const int items = heads * (dim / 4), groups = max(256 / items, 1);
+    for (int i0 = 0; i0 < items; i0 += 256) {
+        const int item = i0 + (int)threadIdx.x % min(items, 256), g = groups > 1 ? threadIdx.x / items : 0;
+        const int h = item / (dim / 4), c = item % (dim / 4) * 4;
+        const bool on = item < items && g < groups;
+        F4 out{0, 0, 0, 0};
+        if (on) {
+            int i = g;
+            for (; i + 3 * groups < count; i += 4 * groups) {     // loads of four parts in flight
+                F4 v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = *(const F4*)(slot(i + k * groups) + 2 * kPagedHeads + h * pitch + c);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) out += v[k] * factors[h][i + k * groups];
+            }
+            for (; i < count; i += groups) out += *(const F4*)(slot(i) + 2 * kPagedHeads + h * pitch + c) * factors[h][i];
+        }
+        if (groups > 1) {
+            sums[threadIdx.x] = out;
+            __syncthreads();
+            if (on && g == 0)
+                for (int k = 1; k < groups; ++k) out += sums[k * items + item];
+        }
+        if (on && g == 0) {
+            const float r = scales[h];
+            typedef uint16_t H4 __attribute__((ext_vector_type(4)));
+            store_chunk<uint16_t, 4>((uint16_t*)p.a.o_dev + b * p.a.o_batch_stride + (q_head + h) * p.a.o_head_stride + c,
+                                     __builtin_bit_cast(H4, U2{pack2<T>(out[0] * r, out[1] * r), pack2<T>(out[2] * r, out[3] * r)}));
+        }
     }
 }
 

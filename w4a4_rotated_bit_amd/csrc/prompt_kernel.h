@@ -150,14 +150,16 @@ __device__ __forceinline__ U4 descriptor(const char* base, uint32_t bytes)
     return d;
 }
 
-// WAVES: of 32 queries each.  DIRECT: keys and values are copied straight to shared
+// WIDTH: channels computed with, those of a head and zeros behind them.  WAVES: of 32
+// queries each.  DIRECT: keys and values are copied straight to shared
 // memory; otherwise (rows that do not begin with a multiple of 16 bytes, or overlap) by
 // way of registers.
-template <typename T, int DIM, int WAVES, bool DIRECT>
-__global__ __launch_bounds__(64 * WAVES, DIM > 128 ? 1 : 2) void prompt_kernel(PromptParams p)
+template <typename T, int WIDTH, int WAVES, bool DIRECT>
+__global__ __launch_bounds__(64 * WAVES, WIDTH > 128 ? 1 : 2) void prompt_kernel(PromptParams p)
 {
+    constexpr int DIM = WIDTH <= 64 ? 64 : WIDTH <= 128 ? 128 : 256;     // of a row in shared memory: the permutations need a power of two
     constexpr int KEYS = kPromptKeys, ROW = 2 * DIM, PIECES = DIM / 8;   // bytes and 16-byte pieces of a row
-    constexpr int STAGE = KEYS * ROW, COPIES = KEYS * PIECES / (64 * WAVES), STEPS = DIM / 16, TILES = DIM / 32;
+    constexpr int STAGE = KEYS * ROW, COPIES = KEYS * PIECES / (64 * WAVES), STEPS = WIDTH / 16, TILES = WIDTH / 32;
     constexpr int ROWS = 32 * WAVES;
     __shared__ __attribute__((aligned(16))) char shared[2][2][STAGE];    // keys, values; stages
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -564,39 +566,58 @@ __global__ __launch_bounds__(256) void prompt_join_kernel(PromptParams p)
         b = row / p.a.q_tokens;
         at = row % p.a.q_tokens;
     }
-    const float* stats = p.partial + p.splits * p.rows * dim + 2 * r;
-    float most = -kInf, total = 0.f;
-    for (int i = 0; i < p.splits; ++i) most = fmaxf(most, stats[2 * i * p.rows]);
-    F4 out{0, 0, 0, 0};
-    const int c = 4 * lane;
-    for (int i = 0; i < p.splits; ++i) {
-        const float m = stats[2 * i * p.rows], f = m == -kInf ? 0.f : exp2_fast(m - most);
-        total += stats[2 * i * p.rows + 1] * f;
-        if (c < dim) out += *(const F4*)(p.partial + (i * p.rows + r) * dim + c) * f;
-    }
+    // a lane a part: its maximum, sum, and what it counts for
+    const float* stats = p.partial + p.splits * p.rows * dim + 2 * (lane * p.rows + r);
+    const float m = lane < p.splits ? stats[0] : -kInf, l = lane < p.splits ? stats[1] : 0.f;
+    float most = m;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) most = fmaxf(most, __shfl_xor(most, d));
+    const float f = m == -kInf ? 0.f : exp2_fast(m - most);
+    const float total = lane_sum<64>(l * f);
     const float s = total == 0.f ? 0.f : 1.f / total;
+    // four channels a lane; lanes left over share the parts, in up to four groups
+    const int per = dim / 4, groups = min(64 / per, 4), g = lane / per, c = lane % per * 4;
+    F4 out{0, 0, 0, 0};
+    const float* from = p.partial + r * dim + c;
+    for (int i = 0; i < p.splits; i += 4 * groups) {     // loads of four parts in flight
+        F4 v[4];
+        float w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int part = i + k * groups + g;
+            const bool on = g < groups && part < p.splits;
+            w[k] = __shfl(f, min(part, 63));
+            v[k] = on ? *(const F4*)(from + part * p.rows * dim) : F4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) out += v[k] * w[k];
+    }
+    F4 sum = out;
+    for (int k = 1; k < groups; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[j] += __shfl(out[j], lane + k * per);
     typedef uint16_t H4 __attribute__((ext_vector_type(4)));
-    if (c < dim)
+    if (lane < per)
         store_chunk<uint16_t, 4>((uint16_t*)p.a.o_dev + b * p.a.o_batch_stride + at * p.a.o_token_stride + head * p.a.o_head_stride + c,
-                                 __builtin_bit_cast(H4, U2{pack2<T>(out[0] * s, out[1] * s), pack2<T>(out[2] * s, out[3] * s)}));
+                                 __builtin_bit_cast(H4, U2{pack2<T>(sum[0] * s, sum[1] * s), pack2<T>(sum[2] * s, sum[3] * s)}));
     if (lane == 0 && p.a.lse_dev) p.a.lse_dev[r] = total == 0.f ? -kInf : (most + __log2f(total)) * kLn2;
 }
 
+template <typename T, int WIDTH>
+void launch_prompt_width(const PromptParams& p, unsigned grid, hipStream_t s)
+{
+    p.direct ? prompt_kernel<T, WIDTH, 4, true><<<grid, 256, 0, s>>>(p) : prompt_kernel<T, WIDTH, 4, false><<<grid, 256, 0, s>>>(p);
+}
 template <typename T>
 void launch_prompt_dim(const PromptParams& p, unsigned grid, hipStream_t s)
 {
-    switch (padded_dim(p.a.head_dim)) {
-    case 64:
-        p.direct ? prompt_kernel<T, 64, 4, true><<<grid, 256, 0, s>>>(p) : prompt_kernel<T, 64, 4, false><<<grid, 256, 0, s>>>(p);
-        break;
-    case 128:
-        if (p.waves == 8) prompt_kernel<T, 128, 8, true><<<grid, 512, 0, s>>>(p);
-        else p.direct ? prompt_kernel<T, 128, 4, true><<<grid, 256, 0, s>>>(p) : prompt_kernel<T, 128, 4, false><<<grid, 256, 0, s>>>(p);
-        break;
-    default:
-        p.direct ? prompt_kernel<T, 256, 4, true><<<grid, 256, 0, s>>>(p) : prompt_kernel<T, 256, 4, false><<<grid, 256, 0, s>>>(p);
-        break;
-    }
+    const int width = (p.a.head_dim + 31) / 32;
+    if (width <= 2) launch_prompt_width<T, 64>(p, grid, s);
+    else if (width == 3) launch_prompt_width<T, 96>(p, grid, s);
+    else if (width == 4 && p.waves == 8) prompt_kernel<T, 128, 8, true><<<grid, 512, 0, s>>>(p);
+    else if (width == 4) launch_prompt_width<T, 128>(p, grid, s);
+    else if (width <= 6) launch_prompt_width<T, 192>(p, grid, s);
+    else launch_prompt_width<T, 256>(p, grid, s);
 }
 
 }  // namespace
