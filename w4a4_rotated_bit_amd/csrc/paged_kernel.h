@@ -13,6 +13,10 @@
 // (a factor that binary32 sums and 16-bit weights of the softmax bear), so most
 // steps rescale nothing.
 //
+// Bound by the bytes of the keys and values: one to three steps' rows are under way
+// while one is computed, and a row costs no address arithmetic but that of its
+// page, which is scalar (a lane's place among a step's rows never changes).
+//
 // Work is shared out in units of 128 keys, over all sequences and key heads in
 // one line that the workgroups cut into equal parts: the lengths are known on
 // the GPU alone.  A workgroup's part may end inside a sequence; such ends go to
@@ -100,20 +104,22 @@ __device__ __forceinline__ int share_of(int64_t units, int workgroups, int64_t u
     return (int)(((u + 1) * workgroups - 1) / units);
 }
 
-// The raw bytes of 32 keys or values, as a lane holds them.
+// The raw bytes of 32 keys and values, as a lane holds them.
 // DIM: padded width, 64, 128 or 256.
 template <int KIND, int DIM>
 struct Shape {
     static constexpr int STEPS = DIM / 32;                  // matrix products over the channels of 16 keys
     static constexpr int LANE = DIM / 4;                    // channels of a key that a quantized lane holds
     static constexpr bool QUANT = KIND >= CONVROT_CACHE_E4M3;
-    static constexpr int K_BYTES = KIND == CONVROT_CACHE_E4M3 ? LANE : KIND == CONVROT_CACHE_E2M1 ? LANE / 2 : 2 * LANE;
-    static constexpr int K_WORDS = K_BYTES / 4;
+    static constexpr int BITS = KIND == CONVROT_CACHE_E4M3 ? 8 : KIND == CONVROT_CACHE_E2M1 ? 4 : 16;
+    static constexpr int K_WORDS = LANE * BITS / 32;
     static constexpr int K_SCALES = QUANT ? (LANE + kBlock - 1) / kBlock : 1;
     static constexpr int WIDE = DIM == 64 ? 4 : 8;          // channels of a value that a lane loads at once
     static constexpr int SETS = DIM / (16 * WIDE);          // such loads a row
-    static constexpr int V_BYTES = KIND == CONVROT_CACHE_E4M3 ? WIDE : KIND == CONVROT_CACHE_E2M1 ? WIDE / 2 : 2 * WIDE;
+    static constexpr int V_BYTES = WIDE * BITS / 8;
     static constexpr int V_WORDS = (V_BYTES + 3) / 4;
+    static constexpr int REGISTERS = 2 * K_WORDS + 8 * SETS * V_WORDS + (QUANT ? 2 * K_SCALES + 8 * SETS : 0);
+    static constexpr int HELD = REGISTERS <= 32 ? 4 : REGISTERS <= 48 ? 3 : 2;   // steps in registers, the current one among them
 };
 
 template <int KIND, int DIM>
@@ -121,132 +127,7 @@ struct Tile {
     using S = Shape<KIND, DIM>;
     uint32_t k[2][S::K_WORDS];
     uint32_t v[8][S::SETS][S::V_WORDS];
-    uint8_t ks[2][S::K_SCALES], vs[8][S::SETS];
-};
-
-struct Lookup {
-    int k[2], v[2];   // pages of this lane's keys (two of 16) and of its two quads of values
-};
-
-template <typename T, int KIND, int DIM>
-struct Walker {
-    using S = Shape<KIND, DIM>;
-    const PagedParams& p;
-    const int* table;         // of the sequence
-    int length, head, lane, col, quad;
-    // offsets inside a row of this lane's bytes
-    int dim;
-
-    __device__ __forceinline__ Lookup lookup(int t) const
-    {
-        Lookup l;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            l.k[h] = table[min(t * kPagedTile + 16 * h + col, length - 1) >> p.shift];
-            l.v[h] = table[min(t * kPagedTile + 16 * h + 4 * quad, length - 1) >> p.shift];
-        }
-        return l;
-    }
-    __device__ __forceinline__ bool good(int page) const { return (uint32_t)page < (uint32_t)p.a.cache.pages; }
-
-    __device__ __forceinline__ void load(Tile<KIND, DIM>& x, int t, const Lookup& l) const
-    {
-        const convrot_cache_rows &kr = p.a.cache.k, &vr = p.a.cache.v;
-        const int mask = (1 << p.shift) - 1;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t page = good(l.k[h]) ? l.k[h] : 0;
-            const int place = min(t * kPagedTile + 16 * h + col, length - 1) & mask;
-            const char* row = (const char*)kr.rows_dev + page * kr.page_stride + head * kr.head_stride + place * kr.token_stride;
-            if constexpr (!S::QUANT) {
-#pragma unroll
-                for (int i = 0; i < S::STEPS; ++i) {
-                    const int c = i * 32 + quad * 8;
-                    const U4 r = *(const U4*)(row + (c < dim ? 2 * c : 0));   // beyond the head: its first channels, times 0
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) x.k[h][4 * i + j] = r[j];
-                }
-            } else {
-                const uint8_t* scales = kr.scales_dev + page * kr.scale_page_stride + head * kr.scale_head_stride + place * kr.scale_token_stride;
-                // whole blocks: a lane's bytes lie inside the head or beyond it, 16 (8) bytes at a time
-                constexpr int PART = S::K_BYTES < 16 ? S::K_BYTES : 16;
-                constexpr int VALUES = KIND == CONVROT_CACHE_E4M3 ? PART : 2 * PART;
-#pragma unroll
-                for (int i = 0; i < S::K_BYTES / PART; ++i) {
-                    const int c = quad * S::LANE + i * VALUES;
-                    const char* at = row + (c < dim ? (KIND == CONVROT_CACHE_E4M3 ? c : c / 2) : 0);
-                    if constexpr (PART == 16) {
-                        const U4 r = *(const U4*)at;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) x.k[h][4 * i + j] = r[j];
-                    } else {
-                        const U2 r = *(const U2*)at;
-                        x.k[h][0] = r[0];
-                        x.k[h][1] = r[1];
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < S::K_SCALES; ++i) {
-                    const int c = quad * S::LANE + i * kBlock;
-                    x.ks[h][i] = scales[c < dim ? c / kBlock : 0];
-                }
-            }
-            const int64_t vpage = good(l.v[h]) ? l.v[h] : 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int vplace = min(t * kPagedTile + 16 * h + 4 * quad + j, length - 1) & mask;
-                const char* vrow = (const char*)vr.rows_dev + vpage * vr.page_stride + head * vr.head_stride + vplace * vr.token_stride;
-#pragma unroll
-                for (int set = 0; set < S::SETS; ++set) {
-                    const int c0 = (set * 16 + col) * S::WIDE;
-                    const int c = c0 < dim ? c0 : 0;   // beyond the head: outputs that nobody reads
-                    uint32_t(&d)[S::V_WORDS] = x.v[4 * h + j][set];
-                    if constexpr (S::V_BYTES == 16) {
-                        const U4 r = *(const U4*)(vrow + 2 * c);
-                        d[0] = r[0], d[1] = r[1], d[2] = r[2], d[3] = r[3];
-                    } else if constexpr (S::V_BYTES == 8) {
-                        const U2 r = *(const U2*)(vrow + c * S::V_BYTES / S::WIDE);
-                        d[0] = r[0], d[1] = r[1];
-                    } else if constexpr (S::V_BYTES == 4) {
-                        d[0] = *(const uint32_t*)(vrow + c * S::V_BYTES / S::WIDE);
-                    } else {
-                        d[0] = *(const uint16_t*)(vrow + c / 2);
-                    }
-                    if constexpr (S::QUANT)
-                        x.vs[4 * h + j][set] = vr.scales_dev[vpage * vr.scale_page_stride + head * vr.scale_head_stride +
-                                                             vplace * vr.scale_token_stride + c / kBlock];
-                }
-            }
-        }
-    }
-
-    // eight channels of a key as the operand of step i
-    __device__ __forceinline__ U4 key(const Tile<KIND, DIM>& x, int h, int i) const
-    {
-        if constexpr (!S::QUANT) {
-            return U4{x.k[h][4 * i], x.k[h][4 * i + 1], x.k[h][4 * i + 2], x.k[h][4 * i + 3]};
-        } else {
-            const float s = block_scale(x.ks[h][i * 8 / kBlock]);
-            if constexpr (KIND == CONVROT_CACHE_E4M3) return Unpack<T>::e4m3(x.k[h][2 * i], x.k[h][2 * i + 1], s);
-            else return Unpack<T>::e2m1(x.k[h][i], s);
-        }
-    }
-    // the channels of step i that this lane's queries have to match
-    __device__ __forceinline__ int channel(int i) const { return S::QUANT ? quad * S::LANE + i * 8 : i * 32 + quad * 8; }
-
-    // one value's channels as registers of two
-    __device__ __forceinline__ U4 value(const Tile<KIND, DIM>& x, int j, int set) const
-    {
-        const uint32_t(&d)[S::V_WORDS] = x.v[j][set];
-        if constexpr (!S::QUANT) {
-            if constexpr (S::WIDE == 8) return U4{d[0], d[1], d[2], d[3]};
-            else return U4{d[0], d[1], 0, 0};
-        } else {
-            const float s = block_scale(x.vs[j][set]);
-            if constexpr (KIND == CONVROT_CACHE_E4M3) return Unpack<T>::e4m3(d[0], S::WIDE == 8 ? d[S::V_WORDS - 1] : 0u, s);
-            else return Unpack<T>::e2m1(d[0], s);
-        }
-    }
+    uint32_t ks[2][S::K_SCALES], vs[8][S::SETS];
 };
 
 template <typename T, int KIND, int DIM>
@@ -282,50 +163,172 @@ __global__ __launch_bounds__(64 * kPagedWaves, 2) void paged_kernel(PagedParams 
     }
     const int64_t start = u;
 
+    // Offsets of this lane's bytes from the first of 16 rows: row `col` of the keys, rows
+    // 4 quad .. of the values.  What lies beyond the head is not read: its first bytes
+    // stand for it, times a query's zeros, or for outputs that nobody reads.
+    const convrot_cache_rows &kr = p.a.cache.k, &vr = p.a.cache.v;
+    constexpr int K_PART = S::K_WORDS * 4 < 16 ? S::K_WORDS * 4 : 16;   // bytes of a load, all inside the head or beyond it
+    constexpr int K_LOADS = S::K_WORDS * 4 / K_PART;
+    uint32_t k_off[K_LOADS], v_off[S::SETS], ks_off[S::K_SCALES], vs_off[S::SETS];
+    const auto key_channel = [&](int i) {    // first channel of load i of a key
+        return S::QUANT ? quad * S::LANE + i * K_PART * 8 / S::BITS : i * 32 + quad * 8;
+    };
+#pragma unroll
+    for (int i = 0; i < K_LOADS; ++i)
+        k_off[i] = col * (uint32_t)kr.token_stride + (key_channel(i) < dim ? key_channel(i) * S::BITS / 8 : 0);
+#pragma unroll
+    for (int set = 0; set < S::SETS; ++set) {
+        const int c = (set * 16 + col) * S::WIDE;
+        v_off[set] = 4 * quad * (uint32_t)vr.token_stride + (c < dim ? c * S::BITS / 8 : 0);
+        vs_off[set] = 4 * quad * (uint32_t)vr.scale_token_stride + (c < dim ? c / kBlock : 0);
+    }
+#pragma unroll
+    for (int i = 0; i < S::K_SCALES; ++i) {
+        const int c = quad * S::LANE + i * kBlock;
+        ks_off[i] = col * (uint32_t)kr.scale_token_stride + (c < dim ? c / kBlock : 0);
+    }
+
     for (;;) {
-        const int take = (int)min((int64_t)(at.units - first), last - u);
-        const int length = length_of(p, at.b);
+        const int b = __builtin_amdgcn_readfirstlane(at.b), units = __builtin_amdgcn_readfirstlane(at.units);
+        first = __builtin_amdgcn_readfirstlane(first);
+        column = __builtin_amdgcn_readfirstlane(column);
+        const int take = (int)min((int64_t)(units - first), last - u);
+        const int length = __builtin_amdgcn_readfirstlane(length_of(p, b));
         const int head = column / p.groups, part = column % p.groups;
         const int heads = min(p.group - part * kPagedHeads, kPagedHeads);       // columns in use
         const int q_head = head * p.group + part * kPagedHeads;                 // the first of them
-        const Walker<T, KIND, DIM> walk{p, p.a.page_table_dev + at.b * p.a.table_stride, length, head, lane, col, quad, dim};
+        typedef __attribute__((address_space(4))) const int Constant;           // scalar loads
+        Constant* table = (Constant*)(p.a.page_table_dev + b * p.a.table_stride);
+        const char* keys = (const char*)kr.rows_dev + head * kr.head_stride;
+        const char* vals = (const char*)vr.rows_dev + head * vr.head_stride;
+        const uint8_t* key_scales = kr.scales_dev + head * kr.scale_head_stride;
+        const uint8_t* val_scales = vr.scales_dev + head * vr.scale_head_stride;
+        // this wave's steps: t0, t0 + NW, ... below end; those of the whole share when it has none
+        const int end = __builtin_amdgcn_readfirstlane(min((first + take) * NW, (length + kPagedTile - 1) / kPagedTile));
+        const int t0 = first * NW + wave;
+
+        // The pages of a step's four groups of eight keys (a page has eight places at least);
+        // behind the last key its page.
+        struct Pages {
+            int page[4];
+        };
+        const auto pages_of = [&](int t) {
+            Pages x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x.page[i] = table[min(min(t, end - 1) * kPagedTile + 8 * i, length - 1) >> p.shift];
+            return x;
+        };
+        const auto good = [&](int page) { return (uint32_t)page < (uint32_t)p.a.cache.pages; };
 
         U4 q[S::STEPS];
         {
-            const T* row = (const T*)p.a.q_dev + at.b * p.a.q_batch_stride + (q_head + min(col, heads - 1)) * p.a.q_head_stride;
+            const T* row = (const T*)p.a.q_dev + b * p.a.q_batch_stride + (q_head + min(col, heads - 1)) * p.a.q_head_stride;
 #pragma unroll
             for (int i = 0; i < S::STEPS; ++i) {
-                const int c = walk.channel(i);
+                const int c = S::QUANT ? quad * S::LANE + i * 8 : i * 32 + quad * 8;
                 q[i] = col < heads && c < dim ? __builtin_bit_cast(U4, load_chunk<uint16_t, 8>((const uint16_t*)row + c)) : U4{0, 0, 0, 0};
             }
         }
+
+        const auto load = [&](Tile<KIND, DIM>& x, int t, const Pages& pages) {
+            t = min(t, end - 1);    // behind the last step: it again, so that the loads under way are always as many
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                // 16 keys, or twice 8 on pages of 8: their first rows
+                const auto first_of = [&](int g, const char* base, int64_t page_stride, int64_t token_stride) {
+                    const int page = pages.page[2 * h + g];
+                    return base + (good(page) ? page : 0) * page_stride + ((t * kPagedTile + 16 * h + 8 * g) & ((1 << p.shift) - 1)) * token_stride;
+                };
+                const auto rows = [&](const char* base, int64_t page_stride, int64_t token_stride, int second) {
+                    const char* low = first_of(0, base, page_stride, token_stride);
+                    if (p.shift > 3) return low;
+                    // offsets count from the first of the 16 rows
+                    return second ? first_of(1, base, page_stride, token_stride) - 8 * token_stride : low;
+                };
+                const char* k_rows = rows(keys, kr.page_stride, kr.token_stride, col / 8);
+                const char* v_rows = rows(vals, vr.page_stride, vr.token_stride, quad / 2);
+#pragma unroll
+                for (int i = 0; i < K_LOADS; ++i) {
+                    if constexpr (K_PART == 16) {
+                        const U4 r = *(const U4*)(k_rows + k_off[i]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) x.k[h][4 * i + j] = r[j];
+                    } else {
+                        const U2 r = *(const U2*)(k_rows + k_off[i]);
+                        x.k[h][0] = r[0];
+                        x.k[h][1] = r[1];
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int set = 0; set < S::SETS; ++set) {
+                        const char* at_v = v_rows + j * vr.token_stride + v_off[set];
+                        uint32_t(&d)[S::V_WORDS] = x.v[4 * h + j][set];
+                        if constexpr (S::V_BYTES == 16) {
+                            const U4 r = *(const U4*)at_v;
+                            d[0] = r[0], d[1] = r[1], d[2] = r[2], d[3] = r[3];
+                        } else if constexpr (S::V_BYTES == 8) {
+                            const U2 r = *(const U2*)at_v;
+                            d[0] = r[0], d[1] = r[1];
+                        } else if constexpr (S::V_BYTES == 4) {
+                            d[0] = *(const uint32_t*)at_v;
+                        } else {
+                            d[0] = *(const uint16_t*)at_v;
+                        }
+                    }
+                if constexpr (S::QUANT) {
+                    const char* ks_rows = rows((const char*)key_scales, kr.scale_page_stride, kr.scale_token_stride, col / 8);
+                    const char* vs_rows = rows((const char*)val_scales, vr.scale_page_stride, vr.scale_token_stride, quad / 2);
+#pragma unroll
+                    for (int i = 0; i < S::K_SCALES; ++i) x.ks[h][i] = *(const uint8_t*)(ks_rows + ks_off[i]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int set = 0; set < S::SETS; ++set)
+                            x.vs[4 * h + j][set] = *(const uint8_t*)(vs_rows + j * vr.scale_token_stride + vs_off[set]);
+                }
+            }
+        };
+
         float m = -kInf, sum = 0.f;
         F4 o[TILES];
 #pragma unroll
         for (int i = 0; i < TILES; ++i) o[i] = F4{0, 0, 0, 0};
 
-        const auto step = [&](const Tile<KIND, DIM>& x, int t, const Lookup& l) {
+        const auto step = [&](Tile<KIND, DIM>& x, int t, const Pages& pages) {
             float s[8];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 F4 acc{0, 0, 0, 0};
 #pragma unroll
-                for (int i = 0; i < S::STEPS; ++i) acc = Mfma16<T>::run(walk.key(x, h, i), q[i], acc);
+                for (int i = 0; i < S::STEPS; ++i) {
+                    U4 a;
+                    if constexpr (!S::QUANT) a = U4{x.k[h][4 * i], x.k[h][4 * i + 1], x.k[h][4 * i + 2], x.k[h][4 * i + 3]};
+                    else if constexpr (KIND == CONVROT_CACHE_E4M3) a = Unpack<T>::e4m3(x.k[h][2 * i], x.k[h][2 * i + 1], block_scale(x.ks[h][i * 8 / kBlock]));
+                    else a = Unpack<T>::e2m1(x.k[h][i], block_scale(x.ks[h][i * 8 / kBlock]));
+                    acc = Mfma16<T>::run(a, q[i], acc);
+                }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) s[4 * h + j] = acc[j] * p.scale;
             }
-            // keys behind the last one, or on a page that is none: not seen, and their values not multiplied
-            bool seen[8];
-            bool all = true;
+            bool whole = (t + 1) * kPagedTile <= length;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                seen[j] = t * kPagedTile + (j & 4) * 4 + quad * 4 + (j & 3) < length && walk.good(l.v[j / 4]);
-                all &= seen[j];
-            }
-            const bool partial = __ballot(!all) != 0;
-            if (partial) {
+            for (int i = 0; i < 4; ++i) whole &= good(pages.page[i]);
+            if (!whole) {
+                // keys behind the last one, or on a page that is none: not seen, and their values zeros
 #pragma unroll
-                for (int j = 0; j < 8; ++j) s[j] = seen[j] ? s[j] : -kInf;
+                for (int j = 0; j < 8; ++j) {
+                    const int page = quad < 2 ? pages.page[j / 4 * 2] : pages.page[j / 4 * 2 + 1];
+                    if (good(page) && t * kPagedTile + (j & 4) * 4 + quad * 4 + (j & 3) < length) continue;
+                    s[j] = -kInf;
+#pragma unroll
+                    for (int set = 0; set < S::SETS; ++set) {
+                        x.vs[j][set] = 0;
+#pragma unroll
+                        for (int k = 0; k < S::V_WORDS; ++k) x.v[j][set][k] = 0;
+                    }
+                }
             }
             float most = s[0];
 #pragma unroll
@@ -348,11 +351,17 @@ __global__ __launch_bounds__(64 * kPagedWaves, 2) void paged_kernel(PagedParams 
             const U4 w{pack2<T>(s[0], s[1]), pack2<T>(s[2], s[3]), pack2<T>(s[4], s[5]), pack2<T>(s[6], s[7])};
 #pragma unroll
             for (int set = 0; set < S::SETS; ++set) {
-                U4 v[8];
+                U4 v[8];     // a value's channels as registers of two
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    v[j] = walk.value(x, j, set);
-                    if (partial && !seen[j]) v[j] = U4{0, 0, 0, 0};
+                    const uint32_t(&d)[S::V_WORDS] = x.v[j][set];
+                    if constexpr (!S::QUANT) {
+                        v[j] = U4{d[0], d[1], S::WIDE == 8 ? d[S::V_WORDS - 2] : 0u, S::WIDE == 8 ? d[S::V_WORDS - 1] : 0u};
+                    } else {
+                        const float scale = block_scale(x.vs[j][set]);
+                        if constexpr (KIND == CONVROT_CACHE_E4M3) v[j] = Unpack<T>::e4m3(d[0], S::WIDE == 8 ? d[S::V_WORDS - 1] : 0u, scale);
+                        else v[j] = Unpack<T>::e2m1(d[0], scale);
+                    }
                 }
 #pragma unroll
                 for (int c = 0; c < S::WIDE; ++c) {
@@ -365,26 +374,25 @@ __global__ __launch_bounds__(64 * kPagedWaves, 2) void paged_kernel(PagedParams 
             }
         };
 
-        // A step's rows are asked for one step ahead, the pages they lie on two.
-        int t = first * NW + wave;
-        const int end = min((first + take) * NW, (length + kPagedTile - 1) / kPagedTile);
-        if (t < end) {
-            Tile<KIND, DIM> x, y;
-            Lookup lx = walk.lookup(t), ly = walk.lookup(t + NW);
-            walk.load(x, t, lx);
-            for (;;) {
-                Lookup next = walk.lookup(t + 2 * NW);
-                if (t + NW < end) walk.load(y, t + NW, ly);
-                step(x, t, lx);
-                t += NW;
-                if (t >= end) break;
-                lx = next;
-                next = walk.lookup(t + 2 * NW);
-                if (t + NW < end) walk.load(x, t + NW, lx);
-                step(y, t, ly);
-                t += NW;
-                if (t >= end) break;
-                ly = next;
+        // Steps in registers in turn; a step's pages are asked for before its rows.
+        if (t0 < end) {
+            constexpr int HELD = S::HELD;
+            Tile<KIND, DIM> x[HELD];
+            Pages pages[HELD];
+#pragma unroll
+            for (int i = 0; i < HELD; ++i) pages[i] = pages_of(t0 + i * NW);
+#pragma unroll
+            for (int i = 0; i + 1 < HELD; ++i) load(x[i], t0 + i * NW, pages[i]);
+            for (int t = t0; t < end;) {
+#pragma unroll
+                for (int i = 0; i < HELD; ++i) {
+                    constexpr int LAST = HELD - 1;
+                    load(x[(i + LAST) % HELD], t + LAST * NW, pages[(i + LAST) % HELD]);
+                    step(x[i], t, pages[i]);
+                    pages[i] = pages_of(t + HELD * NW);
+                    t += NW;
+                    if (t >= end) break;
+                }
             }
         }
 
@@ -404,7 +412,7 @@ __global__ __launch_bounds__(64 * kPagedWaves, 2) void paged_kernel(PagedParams 
                     *(F4*)&outs[wave][col][(set * 16 + quad * 4 + j) * S::WIDE + c] = F4{o[i][j], o[i + 1][j], o[i + 2][j], o[i + 3][j]};
                 }
         __syncthreads();
-        const bool whole = take == at.units;
+        const bool whole = take == units;
         float* slot = p.partial + (2 * (int64_t)blockIdx.x + (u == start ? 0 : 1)) * p.slot;
         for (int i = threadIdx.x; i < heads * (dim / 4); i += 64 * NW) {
             const int h = i / (dim / 4), c = i % (dim / 4) * 4;
@@ -424,10 +432,10 @@ __global__ __launch_bounds__(64 * kPagedWaves, 2) void paged_kernel(PagedParams 
                 const float r = total == 0.f ? 0.f : 1.f / total;
                 U2 packed{pack2<T>(out[0] * r, out[1] * r), pack2<T>(out[2] * r, out[3] * r)};
                 typedef uint16_t H4 __attribute__((ext_vector_type(4)));
-                store_chunk<uint16_t, 4>((uint16_t*)p.a.o_dev + at.b * p.a.o_batch_stride + (q_head + h) * p.a.o_head_stride + c,
+                store_chunk<uint16_t, 4>((uint16_t*)p.a.o_dev + b * p.a.o_batch_stride + (q_head + h) * p.a.o_head_stride + c,
                                          __builtin_bit_cast(H4, packed));
                 if (c == 0 && p.a.lse_dev)
-                    p.a.lse_dev[(int64_t)at.b * p.a.q_heads + q_head + h] = total == 0.f ? -kInf : (most + __log2f(total)) * kLn2;
+                    p.a.lse_dev[(int64_t)b * p.a.q_heads + q_head + h] = total == 0.f ? -kInf : (most + __log2f(total)) * kLn2;
             } else {
                 *(F4*)(slot + 2 * kPagedHeads + h * DIM + c) = out;
                 if (c == 0) {
