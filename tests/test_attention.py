@@ -606,8 +606,8 @@ def test_attention_outputs_and_workspaces_given(gpu):
     version = wide._version
     got = B.convrot_attention(q, k, v, out=wide.transpose(1, 2), lse=lse)
     assert got[0].data_ptr() == wide.data_ptr() and torch.equal(got[0], out) and got[1] is lse and wide._version > version
-    cache = new_cache(40, 16, 4, 64, "same", "bf16", seed=5)
-    table = torch.arange(40, dtype=torch.int32, device="cuda").view(1, 40)
+    cache = new_cache(130, 16, 4, 64, "same", "bf16", seed=5)
+    table = torch.arange(130, dtype=torch.int32, device="cuda").view(1, 130)     # wide enough for shares of the keys
     n = torch.tensor([640], dtype=torch.int32, device="cuda")
     want = B.convrot_attention_paged(q[0, :1], cache, table, n)
     ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")

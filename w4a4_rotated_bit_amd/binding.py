@@ -13,7 +13,6 @@ import ctypes
 import os
 import struct
 import threading
-from typing import Any, NamedTuple
 
 import numpy as np
 
@@ -949,14 +948,17 @@ CONVROT_I64 = 5
 CONVROT_CACHE_E4M3 = 6
 CONVROT_CACHE_E2M1 = 7
 
-# The argument structs of the C calls, in their order (native alignment).
-_CACHE_FIELDS = 2 * "2P6q" + "q4i"
-CACHE_ARGS = struct.Struct("@" + _CACHE_FIELDS + "3P5q2i")
-PAGED_ARGS = struct.Struct("@" + _CACHE_FIELDS + "5P7q2ifi")
+# The argument structs of the C calls, in their order (native alignment): the cache's
+# part, and what follows it.
+CACHE_FIELDS = struct.Struct("@" + 2 * "2P6q" + "q4i")
+_ROWS_FIELDS = struct.Struct("@3P5q2i")
+_PAGED_FIELDS = struct.Struct("@5P7q2ifi")
+CACHE_ARGS = struct.Struct(CACHE_FIELDS.format + _ROWS_FIELDS.format[1:])
+PAGED_ARGS = struct.Struct(CACHE_FIELDS.format + _PAGED_FIELDS.format[1:])
 ATTENTION_ARGS = struct.Struct("@7P15q5if")
 
 
-class KVCache(NamedTuple):
+class KVCache:
     """Keys and values in pages: k, v are [pages, heads, page_size, ...] device
     tensors, dense in their last dimension, the other strides any multiples of 16
     bytes (of a permuted view, of a slice of a tensor of all layers).
@@ -966,11 +968,65 @@ class KVCache(NamedTuple):
     the even channel) keep blocks of 32 channels that share a scale, k_scales and
     v_scales uint8 [pages, heads, page_size, head_dim / 32], which stand for
     2^(s - 127).  page_size: a power of two, 8 to 65536; head_dim: up to 256, a multiple
-    of 8, or of 32 with scales.  ``new_kv_cache`` allocates one."""
-    k: Any
-    v: Any
-    k_scales: Any = None
-    v_scales: Any = None
+    of 8, or of 32 with scales.  ``new_kv_cache`` allocates one.
+
+    The tensors' places are taken when it is made, and their memory is kept as long as
+    it lives: a tensor that is set to other storage later needs a new KVCache."""
+
+    __slots__ = ("k", "v", "k_scales", "v_scales", "heads", "head_dim", "kept", "device", "_fields", "_memory")
+
+    def __init__(self, k, v, k_scales=None, v_scales=None):
+        device = _on_gpu(k, "cache.k")
+        for name, t in (("cache.k", k), ("cache.v", v)):
+            _check_tensor(t, name, device)
+        shape, dtype = k.shape, k.dtype
+        if len(shape) != 4 or v.shape != shape or v.dtype != dtype:
+            raise ValueError("the cache's k and v must be [pages, heads, page_size, ...] of one shape and type, got "
+                             f"{tuple(shape)} {dtype} and {tuple(v.shape)} {v.dtype}")
+        pages, heads, page_size, last = shape
+        if dtype is _torch.float8_e4m3fn:
+            kind, size, dim, kept = CONVROT_CACHE_E4M3, 1, last, None
+        elif dtype is _torch.uint8:
+            kind, size, dim, kept = CONVROT_CACHE_E2M1, 1, 2 * last, None
+        elif dtype is _torch.bfloat16:
+            kind, size, dim, kept = CONVROT_BF16, 2, last, dtype
+        elif dtype is _torch.float16:
+            kind, size, dim, kept = CONVROT_F16, 2, last, dtype
+        else:
+            raise TypeError(f"a cache keeps bfloat16, float16, float8_e4m3fn or uint8 (e2m1) rows, not {dtype}")
+        fields = []
+        for name, rows, scales in (("k", k, k_scales), ("v", v, v_scales)):
+            page, head, token, one = rows.stride()
+            if one != 1 and last > 1:
+                raise ValueError(f"cache.{name} must be dense in its last dimension")
+            at, steps = 0, (0, 0, 0)
+            if kept is None:
+                _check_tensor(scales, f"cache.{name}_scales", device)
+                if scales.dtype is not _torch.uint8 or scales.shape != (pages, heads, page_size, dim // 32):
+                    raise ValueError(f"cache.{name}_scales must be uint8 [pages, heads, page_size, head_dim / 32], got "
+                                     f"{scales.dtype} {tuple(scales.shape)}")
+                *steps, one = scales.stride()
+                if one != 1 and dim > 32:
+                    raise ValueError(f"cache.{name}_scales must be dense in its last dimension")
+                at = scales.data_ptr()
+            elif scales is not None:
+                raise ValueError("a cache that keeps rows as they are has no scales")
+            fields += (rows.data_ptr(), at, page * size, head * size, token * size, *steps)
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        self.heads, self.head_dim, self.kept, self.device = heads, dim, kept, device
+        self._fields = CACHE_FIELDS.pack(*fields, pages, page_size, heads, dim, kind)
+        self._memory = [t.untyped_storage() for t in (k, v, k_scales, v_scales) if t is not None]
+
+    def __iter__(self):
+        return iter((self.k, self.v, self.k_scales, self.v_scales))
+
+    def _replace(self, **kw):
+        """Another cache with some of its tensors given."""
+        return KVCache(**{"k": self.k, "v": self.v, "k_scales": self.k_scales, "v_scales": self.v_scales, **kw})
+
+    def _written(self):
+        kept = (self.k, self.v) if self.k_scales is None else (self.k, self.v, self.k_scales, self.v_scales)
+        _torch.autograd.graph.increment_version(kept)
 
 
 def new_kv_cache(pages: int, page_size: int, heads: int, head_dim: int, kind="e2m1", device="cuda") -> KVCache:
@@ -991,47 +1047,19 @@ def new_kv_cache(pages: int, page_size: int, heads: int, head_dim: int, kind="e2
     return KVCache(*rows, *scales)
 
 
-def _cache_fields(cache, device):
-    """(fields of one convrot_kv_cache, heads, head_dim, type of rows kept as they are or None)."""
-    k, v, k_scales, v_scales = cache
-    for name, t in (("cache.k", k), ("cache.v", v)):
-        if not isinstance(t, _torch.Tensor) or t.get_device() != device or t.requires_grad:
-            _check_tensor(t, name, device)
-    shape, dtype = k.shape, k.dtype
-    if len(shape) != 4 or v.shape != shape or v.dtype != dtype:
-        raise ValueError("the cache's k and v must be [pages, heads, page_size, ...] of one shape and type, got "
-                         f"{tuple(shape)} {dtype} and {tuple(v.shape)} {v.dtype}")
-    pages, heads, page_size, last = shape
-    if dtype is _torch.float8_e4m3fn:
-        kind, size, dim, kept = CONVROT_CACHE_E4M3, 1, last, None
-    elif dtype is _torch.uint8:
-        kind, size, dim, kept = CONVROT_CACHE_E2M1, 1, 2 * last, None
-    elif dtype is _torch.bfloat16:
-        kind, size, dim, kept = CONVROT_BF16, 2, last, dtype
-    elif dtype is _torch.float16:
-        kind, size, dim, kept = CONVROT_F16, 2, last, dtype
-    else:
-        raise TypeError(f"a cache keeps bfloat16, float16, float8_e4m3fn or uint8 (e2m1) rows, not {dtype}")
-    fields = []
-    for name, rows, scales in (("k", k, k_scales), ("v", v, v_scales)):
-        page, head, token, one = rows.stride()
-        if one != 1 and last > 1:
-            raise ValueError(f"cache.{name} must be dense in its last dimension")
-        at = steps = None
-        if kept is None:
-            if not isinstance(scales, _torch.Tensor) or scales.get_device() != device:
-                _check_tensor(scales, f"cache.{name}_scales", device)
-            if scales.dtype is not _torch.uint8 or scales.shape != (pages, heads, page_size, dim // 32):
-                raise ValueError(f"cache.{name}_scales must be uint8 [pages, heads, page_size, head_dim / 32], got "
-                                 f"{scales.dtype} {tuple(scales.shape)}")
-            *steps, one = scales.stride()
-            if one != 1 and dim > 32:
-                raise ValueError(f"cache.{name}_scales must be dense in its last dimension")
-            at = scales.data_ptr()
-        elif scales is not None:
-            raise ValueError("a cache that keeps rows as they are has no scales")
-        fields += (rows.data_ptr(), at or 0, page * size, head * size, token * size, *(steps or (0, 0, 0)))
-    return (*fields, pages, page_size, heads, dim, kind), heads, dim, kept
+def _check_cache(cache, device, dtype, what):
+    """A cache of this call: on its device, of rows that ``what`` of this type may meet."""
+    if cache.__class__ is not KVCache:
+        raise TypeError("cache must be a KVCache")
+    if cache.device != device:
+        raise ValueError(f"the cache is on cuda:{cache.device}, {what} on cuda:{device}")
+    kept = cache.kept
+    if kept is not None:
+        if kept is not dtype:
+            raise TypeError(f"the cache keeps {kept} rows, {what} is {dtype}")
+        if cache.k.requires_grad or cache.v.requires_grad:
+            _check_tensor(cache.k, "cache.k", device)
+            _check_tensor(cache.v, "cache.v", device)
 
 
 def _slots_code(slots, tokens, device):
@@ -1077,20 +1105,20 @@ def convrot_cache_write(k, v, slots, cache: KVCache, stream=None) -> None:
     device = _on_gpu(k, "k")
     if getattr(_forward, "_current_level", 0) >= 0:
         _check_tangents(k, v, *cache)
-    fields, heads, dim, kept = _cache_fields(cache, device)
-    k_strides, v_strides = _token_rows(k, "k", heads, dim, device), _token_rows(v, "v", heads, dim, device)
-    dtype, tokens = k.dtype, k.shape[0]
-    if v.dtype != dtype or v.shape[0] != tokens:
-        raise ValueError("k and v must have one shape and type")
+    dtype = k.dtype
     code = _half_code(dtype, "k")
-    if kept is not None and kept != dtype:
-        raise TypeError(f"the cache keeps {kept} rows, k and v are {dtype}")
+    _check_cache(cache, device, dtype, "k")
+    heads, dim = cache.heads, cache.head_dim
+    k_strides, v_strides = _token_rows(k, "k", heads, dim, device), _token_rows(v, "v", heads, dim, device)
+    tokens = k.shape[0]
+    if v.dtype is not dtype or v.shape[0] != tokens:
+        raise ValueError("k and v must have one shape and type")
     slots_code = _slots_code(slots, tokens, device)
 
     def call(raw):
-        _call("convrot_cache_write", CACHE_ARGS.pack(*fields, k.data_ptr(), v.data_ptr(), slots.data_ptr(), tokens,
-                                                     *k_strides, *v_strides, slots_code, code), raw)
-        _written(*cache)
+        _call("convrot_cache_write", cache._fields + _ROWS_FIELDS.pack(
+            k.data_ptr(), v.data_ptr(), slots.data_ptr(), tokens, *k_strides, *v_strides, slots_code, code), raw)
+        cache._written()
 
     return _launch(device, stream, call, (k, v, slots, *cache))
 
@@ -1100,17 +1128,18 @@ def convrot_cache_read(cache: KVCache, slots, dtype=None, k=None, v=None, stream
     the cache.  dtype: bfloat16 (also the default of a quantized cache) or float16; a
     cache that keeps rows as they are reads back its own.  k, v given are
     written.  ``stream``: as in ``convrot_residual_norm``."""
-    device = _on_gpu(cache[0], "cache.k")
+    if cache.__class__ is not KVCache:
+        raise TypeError("cache must be a KVCache")
+    device = cache.device
     if getattr(_forward, "_current_level", 0) >= 0:
         _check_tangents(k, v, *cache)
-    fields, heads, dim, kept = _cache_fields(cache, device)
     for t in (k, v):
         if dtype is None and t is not None:
             dtype = t.dtype
-    dtype = dtype or kept or _torch.bfloat16
+    dtype = dtype or cache.kept or _torch.bfloat16
     code = _half_code(dtype, "dtype")
-    if kept is not None and kept != dtype:
-        raise TypeError(f"the cache keeps {kept} rows, not {dtype}")
+    _check_cache(cache, device, dtype, "dtype")
+    heads, dim = cache.heads, cache.head_dim
     if not isinstance(slots, _torch.Tensor):
         raise TypeError("slots must be a torch tensor")
     tokens = slots.numel()
@@ -1120,13 +1149,15 @@ def convrot_cache_read(cache: KVCache, slots, dtype=None, k=None, v=None, stream
         outs, strides = [], []
         for name, t in (("k", k), ("v", v)):
             if t is None:
-                t = _torch.empty((tokens, heads, dim), dtype=dtype, device=slots.device)
-            strides += _token_rows(t, name, heads, dim, device)
-            if t.shape[0] != tokens or t.dtype != dtype:
-                raise ValueError(f"{name} must have {tokens} rows of {dtype}")
+                t = slots.new_empty((tokens, heads, dim), dtype=dtype)
+                strides += (heads * dim, dim)
+            else:
+                strides += _token_rows(t, name, heads, dim, device)
+                if t.shape[0] != tokens or t.dtype is not dtype:
+                    raise ValueError(f"{name} must have {tokens} rows of {dtype}")
             outs.append(t)
-        _call("convrot_cache_read", CACHE_ARGS.pack(*fields, outs[0].data_ptr(), outs[1].data_ptr(), slots.data_ptr(), tokens,
-                                                    *strides, slots_code, code), raw)
+        _call("convrot_cache_read", cache._fields + _ROWS_FIELDS.pack(
+            outs[0].data_ptr(), outs[1].data_ptr(), slots.data_ptr(), tokens, *strides, slots_code, code), raw)
         if k is not None or v is not None:
             _written(k, v)
         return outs[0], outs[1]
@@ -1134,19 +1165,23 @@ def convrot_cache_read(cache: KVCache, slots, dtype=None, k=None, v=None, stream
     return _launch(device, stream, call, (slots, k, v, *cache))
 
 
-def _workspace(name, args, workspace, device):
-    """(address, bytes, what keeps it) of the call's workspace, allocated unless given."""
-    if workspace is None:
-        need = _SZ(0)
-        _call(name, args, ctypes.byref(need))
-        if need.value == 0:
-            return None, 0, None
-        workspace = _torch.empty(need.value, dtype=_torch.uint8, device=f"cuda:{device}")
-    else:
+def _call_with_workspace(name, args, workspace, device, raw):
+    """The call, with the workspace given, or one allocated if it needs any."""
+    if workspace is not None:
         _check_tensor(workspace, "workspace", device)
         if workspace.dtype is not _torch.uint8 or not workspace.is_contiguous():
             raise ValueError("workspace must be a dense uint8 tensor")
-    return workspace.data_ptr(), workspace.numel(), workspace
+        _call(name, args, workspace.data_ptr(), workspace.numel(), raw)
+        return
+    lib = _lib or load()
+    rc = getattr(lib, name)(args, None, 0, raw)
+    if rc == CONVROT_EWORKSPACE:    # refused before anything was launched
+        need = _SZ(0)
+        _call(name + "_workspace_bytes", args, ctypes.byref(need))
+        space = _torch.empty(need.value, dtype=_torch.uint8, device=f"cuda:{device}")
+        rc = getattr(lib, name)(args, space.data_ptr(), need.value, raw)
+    if rc != CONVROT_OK:
+        raise ConvRotError(rc, name)
 
 
 def _table(t, name, dims, device):
@@ -1162,7 +1197,7 @@ def _table(t, name, dims, device):
 def _output(out, q, want, name, shape, dtype, device):
     """The output given (checked), a new one, or None."""
     if out is None:
-        return _torch.empty(shape, dtype=dtype, device=q.device) if want else None
+        return q.new_empty(shape, dtype=dtype) if want else None
     _check_tensor(out, name, device)
     if out.shape != shape or out.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {out.dtype} {tuple(out.shape)}")
@@ -1190,13 +1225,12 @@ def convrot_attention_paged(q, cache: KVCache, page_table, lengths, *, scale=Non
         _check_tangents(q, out, lse, *cache)
     shape, dtype = q.shape, q.dtype
     code = _half_code(dtype, "q")
-    fields, heads, dim, kept = _cache_fields(cache, device)
+    _check_cache(cache, device, dtype, "q")
+    heads, dim = cache.heads, cache.head_dim
     if len(shape) != 3 or shape[2] != dim or (dim > 1 and q.stride(2) != 1):
         raise ValueError(f"q must be [batch, q_heads, {dim}] and dense in its last dimension, got {tuple(shape)}")
     if shape[1] % heads:
         raise ValueError(f"{shape[1]} query heads do not share {heads} key heads evenly")
-    if kept is not None and kept != dtype:
-        raise TypeError(f"the cache keeps {kept} rows, q is {dtype}")
     table_ptr, lengths_ptr = _table(page_table, "page_table", 2, device), _table(lengths, "lengths", 1, device)
     if page_table.shape[0] != shape[0] or lengths.shape[0] != shape[0]:
         raise ValueError(f"page_table and lengths must have one row for each of the {shape[0]} sequences")
@@ -1209,11 +1243,11 @@ def convrot_attention_paged(q, cache: KVCache, page_table, lengths, *, scale=Non
         sums = _output(lse, q, want_lse, "lse", shape[:2], _torch.float32, device)
         if sums is not None and not sums.is_contiguous():
             raise ValueError("lse must be contiguous")
-        args = PAGED_ARGS.pack(*fields, q.data_ptr(), o.data_ptr(), 0 if sums is None else sums.data_ptr(), table_ptr,
-                               lengths_ptr, shape[0], page_table.shape[1], page_table.stride(0), q.stride(0), q.stride(1),
-                               o.stride(0), o.stride(1), shape[1], code, scale, 0)
-        ws_ptr, ws_bytes, _keep = _workspace("convrot_attention_paged_workspace_bytes", args, workspace, device)
-        _call("convrot_attention_paged", args, ws_ptr, ws_bytes, raw)
+        args = cache._fields + _PAGED_FIELDS.pack(
+            q.data_ptr(), o.data_ptr(), 0 if sums is None else sums.data_ptr(), table_ptr, lengths_ptr, shape[0],
+            page_table.shape[1], page_table.stride(0), q.stride(0), q.stride(1), o.stride(0), o.stride(1), shape[1],
+            code, scale, 0)
+        _call_with_workspace("convrot_attention_paged", args, workspace, device, raw)
         if out is not None or lse is not None:
             _written(out, lse)
         return o if sums is None else (o, sums)
@@ -1287,8 +1321,7 @@ def convrot_attention(q, k, v, *, q_starts=None, k_starts=None, causal: bool = F
         args = ATTENTION_ARGS.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), 0 if sums is None else sums.data_ptr(),
                                    q_starts_ptr, k_starts_ptr, batch, tokens, k_tokens, *steps(q, "q"), *steps(k, "k"),
                                    *steps(v, "v"), *steps(o, "out"), heads, k_heads, dim, 1 if causal else 0, code, scale)
-        ws_ptr, ws_bytes, _keep = _workspace("convrot_attention_workspace_bytes", args, workspace, device)
-        _call("convrot_attention", args, ws_ptr, ws_bytes, raw)
+        _call_with_workspace("convrot_attention", args, workspace, device, raw)
         if out is not None or lse is not None:
             _written(out, lse)
         return o if sums is None else (o, sums)

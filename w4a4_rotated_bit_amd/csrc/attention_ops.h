@@ -29,8 +29,10 @@ inline int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
 // ---- one token over the pages ----
 constexpr int kPagedHeads = 16;    // query heads of a key head that one workgroup takes (columns of a matrix product)
 constexpr int kPagedTile = 32;     // keys of a wave's step
-constexpr int kPagedWaves = 4;
-constexpr int kPagedUnit = kPagedTile * kPagedWaves;   // keys of a workgroup's step: the unit that work is shared out by
+constexpr int kPagedUnit = 128;    // keys that work is shared out by
+constexpr int kPagedWaves = 4;     // of a workgroup that has a share
+constexpr int kPagedWavesAlone = 8;     // of one that has a whole sequence
+constexpr int64_t kPagedAlone = 1024;   // most keys of such a sequence: a second launch takes longer than four steps
 constexpr int kPagedShares = 512;  // most workgroups that share the units: two on each compute unit
 
 struct PagedPlan {
@@ -47,7 +49,7 @@ inline PagedPlan paged_plan(const convrot_attention_paged_args& a)
     p.columns = a.cache.heads * ((group + kPagedHeads - 1) / kPagedHeads);
     p.slot = kPagedHeads * (padded_dim(a.cache.head_dim) + 2);
     const int64_t capacity = a.table_width * a.cache.page_size;
-    if (capacity <= 2 * kPagedUnit) return p;
+    if (capacity <= kPagedAlone) return p;
     const int64_t units = a.batch * p.columns * ((capacity + kPagedUnit - 1) / kPagedUnit);
     p.workgroups = (int)std::min<int64_t>(units, kPagedShares);
     return p;

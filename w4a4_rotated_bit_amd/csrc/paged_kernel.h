@@ -63,33 +63,33 @@ struct Place {
     int64_t before;     // units (a column) of the sequences before it
 };
 
-__device__ __forceinline__ int length_of(const PagedParams& p, int b)
+__device__ __forceinline__ int length_of(const PagedParams& p, int64_t b)
 {
-    return min(max(p.a.lengths_dev[b], 0), p.capacity);
+    return b < p.a.batch ? min(max(p.a.lengths_dev[b], 0), p.capacity) : 0;
 }
 __device__ __forceinline__ int units_of(int length) { return (length + kPagedUnit - 1) / kPagedUnit; }
 
-__device__ __forceinline__ int64_t all_units(const PagedParams& p)
+// The first 64 sequences' units are in the lanes of `mine`: most calls have no more,
+// and read the lengths once.
+__device__ __forceinline__ int64_t all_units(const PagedParams& p, int mine)
 {
-    const int lane = __lane_id();
-    int64_t sum = 0;
-    for (int b = 0; b < p.a.batch; b += 64) sum += wave_sum(b + lane < p.a.batch ? units_of(length_of(p, b + lane)) : 0);
+    int64_t sum = wave_sum(mine);
+    for (int64_t b = 64; b < p.a.batch; b += 64) sum += wave_sum(units_of(length_of(p, b + __lane_id())));
     return sum;
 }
 
 // The sequence that holds unit `at` of the line in which each unit counts `columns` times.
-__device__ __forceinline__ Place find_unit(const PagedParams& p, int64_t at)
+__device__ __forceinline__ Place find_unit(const PagedParams& p, int mine, int64_t at)
 {
-    const int lane = __lane_id();
     int64_t before = 0;
-    for (int b = 0;; b += 64) {
-        const int n = b + lane < p.a.batch ? units_of(length_of(p, b + lane)) : 0;
+    for (int64_t b = 0;; b += 64) {
+        const int n = b == 0 ? mine : units_of(length_of(p, b + __lane_id()));
         const int sum = wave_scan(n);
         const uint64_t past = __ballot((before + sum) * p.columns > at);
         if (past) {
             const int l = __builtin_ctzll(past);
             const int units = __builtin_amdgcn_readlane(n, l);
-            return Place{b + l, units, before + __builtin_amdgcn_readlane(sum, l) - units};
+            return Place{(int)b + l, units, before + __builtin_amdgcn_readlane(sum, l) - units};
         }
         before += __builtin_amdgcn_readlane(sum, 63);
     }
@@ -130,11 +130,12 @@ struct Tile {
     uint32_t ks[2][S::K_SCALES], vs[8][S::SETS];
 };
 
-template <typename T, int KIND, int DIM>
-__global__ __launch_bounds__(64 * kPagedWaves, 2) void paged_kernel(PagedParams p)
+// NW: waves of a workgroup.
+template <typename T, int KIND, int DIM, int NW>
+__global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void paged_kernel(PagedParams p)
 {
     using S = Shape<KIND, DIM>;
-    constexpr int NW = kPagedWaves, PITCH = DIM + 4, TILES = S::SETS * S::WIDE;
+    constexpr int PITCH = DIM + 4, TILES = S::SETS * S::WIDE;
     __shared__ float stats[NW][kPagedHeads][2];
     __shared__ __attribute__((aligned(16))) float outs[NW][kPagedHeads][PITCH];
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -145,12 +146,13 @@ __global__ __launch_bounds__(64 * kPagedWaves, 2) void paged_kernel(PagedParams 
     Place at{};
     int column, first;
     if (p.workgroups) {
-        const int64_t units = all_units(p) * p.columns;
+        const int mine = units_of(length_of(p, lane));
+        const int64_t units = all_units(p, mine) * p.columns;
         const int shares = sharing(p, units);
         if ((int)blockIdx.x >= shares) return;
         u = share_begin(units, shares, blockIdx.x);
         last = share_begin(units, shares, blockIdx.x + 1);
-        at = find_unit(p, u);
+        at = find_unit(p, mine, u);
         const int64_t rest = u - at.before * p.columns;
         column = (int)(rest / at.units);
         first = (int)(rest % at.units);
@@ -204,8 +206,8 @@ __global__ __launch_bounds__(64 * kPagedWaves, 2) void paged_kernel(PagedParams 
         const uint8_t* key_scales = kr.scales_dev + head * kr.scale_head_stride;
         const uint8_t* val_scales = vr.scales_dev + head * vr.scale_head_stride;
         // this wave's steps: t0, t0 + NW, ... below end; those of the whole share when it has none
-        const int end = __builtin_amdgcn_readfirstlane(min((first + take) * NW, (length + kPagedTile - 1) / kPagedTile));
-        const int t0 = first * NW + wave;
+        const int end = __builtin_amdgcn_readfirstlane(min((first + take) * (kPagedUnit / kPagedTile), (length + kPagedTile - 1) / kPagedTile));
+        const int t0 = first * (kPagedUnit / kPagedTile) + wave;
 
         // The pages of a step's four groups of eight keys (a page has eight places at least);
         // behind the last key its page.
@@ -467,13 +469,15 @@ __global__ __launch_bounds__(256) void paged_join_kernel(PagedParams p, int pitc
     const int head = column / p.groups, part = column % p.groups;
     const int heads = min(p.group - part * kPagedHeads, kPagedHeads), q_head = head * p.group + part * kPagedHeads;
     const int dim = p.a.cache.head_dim, lane = __lane_id(), wave = threadIdx.x / 64;
-    const int mine = units_of(length_of(p, b));
+    const int here = units_of(length_of(p, lane));
+    const int mine = b < 64 ? __builtin_amdgcn_readlane(here, b) : units_of(length_of(p, b));
     int w0 = 0, count = 0, shares = 0;
     int64_t units = 0, u0 = 0;
     if (mine > 0) {
-        int64_t before = 0;
-        for (int c = 0; c < p.a.batch; c += 64) {
-            const int n = c + lane < p.a.batch ? units_of(length_of(p, c + lane)) : 0;
+        int64_t before = wave_sum(lane < b ? here : 0);
+        units = wave_sum(here);
+        for (int64_t c = 64; c < p.a.batch; c += 64) {
+            const int n = units_of(length_of(p, c + lane));
             units += wave_sum(n);
             before += wave_sum(c + lane < b ? n : 0);
         }
@@ -487,13 +491,25 @@ __global__ __launch_bounds__(256) void paged_join_kernel(PagedParams p, int pitc
     // the first part is its workgroup's first one if that workgroup begins here
     const bool begins = count > 0 && share_begin(units, shares, w0) == u0;
     const auto slot = [&](int i) { return p.partial + (2 * (int64_t)(w0 + i) + (i == 0 && !begins ? 1 : 0)) * p.slot; };
+    // four channels a thread; threads left over share the parts.  The first four parts
+    // are asked for here, the others where they are summed.
+    const int items = heads * (dim / 4), groups = max(256 / items, 1);
+    const int first = (int)threadIdx.x % min(items, 256), g = groups > 1 ? threadIdx.x / items : 0;
+    F4 early[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        early[k] = g + k * groups < count && g < groups ? *(const F4*)(slot(g + k * groups) + 2 * kPagedHeads + first / (dim / 4) * pitch + first % (dim / 4) * 4) : F4{0, 0, 0, 0};
     // a wave a head: what each part counts for
     for (int h = wave; h < heads; h += 4) {
-        float most = -kInf, total = 0.f;
-        for (int i = lane; i < count; i += 64) most = fmaxf(most, slot(i)[2 * h]);
+        const float m0 = lane < count ? slot(lane)[2 * h] : -kInf, l0 = lane < count ? slot(lane)[2 * h + 1] : 0.f;
+        float most = m0;
+        for (int i = lane + 64; i < count; i += 64) most = fmaxf(most, slot(i)[2 * h]);
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) most = fmaxf(most, __shfl_xor(most, d));
-        for (int i = lane; i < count; i += 64) {
+        const float f0 = m0 == -kInf ? 0.f : exp2_fast(m0 - most);
+        factors[h][lane] = f0;
+        float total = l0 * f0;
+        for (int i = lane + 64; i < count; i += 64) {
             const float m = slot(i)[2 * h], f = m == -kInf ? 0.f : exp2_fast(m - most);
             factors[h][i] = f;
             total += slot(i)[2 * h + 1] * f;
@@ -505,15 +521,18 @@ __global__ __launch_bounds__(256) void paged_join_kernel(PagedParams p, int pitc
         }
     }
     __syncthreads();
-    // four channels a thread; threads left over share the parts
-    const int items = heads * (dim / 4), groups = max(256 / items, 1);
     for (int i0 = 0; i0 < items; i0 += 256) {
-        const int item = i0 + (int)threadIdx.x % min(items, 256), g = groups > 1 ? threadIdx.x / items : 0;
-        const int h = item / (dim / 4), c = item % (dim / 4) * 4;
+        const int item = i0 + first, h = item / (dim / 4), c = item % (dim / 4) * 4;
         const bool on = item < items && g < groups;
         F4 out{0, 0, 0, 0};
         if (on) {
             int i = g;
+            if (i0 == 0) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (g + k * groups < count) out += early[k] * factors[h][g + k * groups];
+                i += 4 * groups;
+            }
             for (; i + 3 * groups < count; i += 4 * groups) {     // loads of four parts in flight
                 F4 v[4];
 #pragma unroll
@@ -538,13 +557,20 @@ __global__ __launch_bounds__(256) void paged_join_kernel(PagedParams p, int pitc
     }
 }
 
+template <typename T, int KIND, int DIM>
+void launch_paged_dim(const PagedParams& p, unsigned grid, hipStream_t s)
+{
+    constexpr int ALONE = DIM > 128 ? kPagedWaves : kPagedWavesAlone;    // registers for 256 channels leave one wave a SIMD
+    if (p.workgroups) paged_kernel<T, KIND, DIM, kPagedWaves><<<grid, 64 * kPagedWaves, 0, s>>>(p);
+    else paged_kernel<T, KIND, DIM, ALONE><<<grid, 64 * ALONE, 0, s>>>(p);
+}
 template <typename T, int KIND>
 void launch_paged_kind(const PagedParams& p, unsigned grid, hipStream_t s)
 {
     switch (padded_dim(p.a.cache.head_dim)) {
-    case 64: paged_kernel<T, KIND, 64><<<grid, 64 * kPagedWaves, 0, s>>>(p); break;
-    case 128: paged_kernel<T, KIND, 128><<<grid, 64 * kPagedWaves, 0, s>>>(p); break;
-    default: paged_kernel<T, KIND, 256><<<grid, 64 * kPagedWaves, 0, s>>>(p); break;
+    case 64: launch_paged_dim<T, KIND, 64>(p, grid, s); break;
+    case 128: launch_paged_dim<T, KIND, 128>(p, grid, s); break;
+    default: launch_paged_dim<T, KIND, 256>(p, grid, s); break;
     }
 }
 
