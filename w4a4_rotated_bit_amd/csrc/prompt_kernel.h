@@ -357,16 +357,20 @@ __global__ __launch_bounds__(64 * WAVES, WIDTH > 128 ? 1 : 2) void prompt_kernel
         U4 ring[RING], w[4];
         float sums[2] = {0.f, 0.f};
         // An element's three instructions, slots apart so that none waits for the one before
-        // it; its exponential belongs to the slot `at`.
+        // it.  Its exponential belongs to slot 1 + e (SCORES - 2) / EARLY, or behind the first
+        // EARLY ones to SCORES + (e - EARLY) (OUTS / 2) / (32 - EARLY); `upto` elements come
+        // before a slot.
+        const auto upto = [&](int slot) {
+            const int early = ((slot - 1) * EARLY + SCORES - 3) / (SCORES - 2), late = ((slot - SCORES) * (32 - EARLY) + OUTS / 2 - 1) / (OUTS / 2);
+            return (slot < 1 ? 0 : early < EARLY ? early : EARLY) + (slot <= SCORES ? 0 : late < 32 - EARLY ? late : 32 - EARLY);
+        };
         const auto weigh_in = [&](int slot) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                const int at = e < EARLY ? 1 + e * (SCORES - 2) / EARLY : SCORES + (e - EARLY) * OUTS / 2 / (32 - EARLY);
-                const float s = cur.s[e / 16][e % 16];
-                if (at - 1 == slot) cur.s[e / 16][e % 16] = __builtin_fmaf(s, scale, -from);
-                if (at == slot) cur.s[e / 16][e % 16] = exp2_fast(s);
-                if (at + 1 == slot) sums[e % 2] += s;
-            }
+            for (int e = upto(slot + 1); e < upto(slot + 2); ++e) cur.s[e / 16][e % 16] = __builtin_fmaf(cur.s[e / 16][e % 16], scale, -from);
+#pragma unroll
+            for (int e = upto(slot); e < upto(slot + 1); ++e) cur.s[e / 16][e % 16] = exp2_fast(cur.s[e / 16][e % 16]);
+#pragma unroll
+            for (int e = upto(slot - 1); e < upto(slot); ++e) sums[e % 2] += cur.s[e / 16][e % 16];
         };
         const auto read = [&](int i) {     // what slot i multiplies
             if (i < SCORES) return key(keys, i / 2, i % 2);
@@ -379,10 +383,9 @@ __global__ __launch_bounds__(64 * WAVES, WIDTH > 128 ? 1 : 2) void prompt_kernel
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (next.value == kLast) {
 #pragma unroll
-            for (int i = 0; i < SCORES; ++i) {
-                weigh_in(i);
-                if (i == SCORES - 1) w[0] = weights(cur, 0), w[1] = weights(cur, 1);
-            }
+            for (int i = 0; i < SCORES; ++i) weigh_in(i);
+            w[0] = weights(cur, 0);
+            w[1] = weights(cur, 1);
         } else {
 #pragma unroll
             for (int i = 0; i < SCORES; ++i) {
