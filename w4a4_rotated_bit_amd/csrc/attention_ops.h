@@ -90,10 +90,24 @@ inline PromptPlan prompt_plan(const convrot_attention_args& a)
     // where tiles end in the middle (seven ragged sequences of up to 3001: 226 against 206).
     p.waves = prompt_direct(a) && a.head_dim > 96 && a.head_dim <= 128 && a.q_tokens >= 4096 * (packed ? a.batch : 1) && tiles(8 * kPromptRows) * a.q_heads >= 512 ? 8 : 4;
     p.tiles = tiles(p.waves * kPromptRows);
-    // Few queries against many keys: the keys of a tile go to several workgroups, as
-    // many as fill the chip (two on each compute unit), 256 keys each at least.
+    // Few queries against many keys: the keys of a tile go to several workgroups, 256 keys
+    // each at least, as many as fill the chip (two on each compute unit) and as it pays:
+    // a step of 64 keys takes 1.4 us, or 2 us where two workgroups share a unit, a second
+    // launch 6 us, and partial results are written and read at some 4 TB/s.  (233 queries of
+    // 9 heads of 72 against 13243 keys: 27 us in 19 parts, 240 us in one; 1024 causal
+    // queries of 32 heads of 128: 41 us in two parts, 24 us in one.)
     const int64_t groups = std::max<int64_t>(p.tiles * a.q_heads, 1);
-    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({512 / groups, a.k_tokens / 256, kPromptSplits}));
+    const double steps = (double)a.k_tokens / (packed ? std::max<int64_t>(a.batch, 1) : 1) / kPromptKeys;
+    const double part = (double)(packed ? 1 : a.batch) * a.q_tokens * a.q_heads * a.head_dim * 8 / 4e6;
+    double best = 1e300;
+    p.splits = 1;
+    for (int s = 1; s == 1 || (s <= kPromptSplits && groups * s <= 512 && 4 * s <= steps); ++s) {
+        const double us = steps / s * (groups * s > 256 ? 2.0 : 1.4) + (s > 1 ? 6 + part * s : 0);
+        if (us < best) {
+            best = us;
+            p.splits = s;
+        }
+    }
     p.rows = p.splits * (packed ? 1 : a.batch) * a.q_tokens * a.q_heads;
     return p;
 }
