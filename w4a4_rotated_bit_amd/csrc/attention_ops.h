@@ -56,13 +56,12 @@ inline PagedPlan paged_plan(const convrot_attention_paged_args& a)
 }
 
 // ---- whole prompts ----
-constexpr int kPromptRows = 32;    // queries of a wave
+constexpr int kPromptRows = 128;   // queries of a workgroup: four waves of 32
 constexpr int kPromptKeys = 64;    // keys of a step
 constexpr int kPromptSplits = 64;  // most workgroups that share a tile's keys: a lane each when they are joined
 
 struct PromptPlan {
-    int waves;        // of a workgroup: its tile has 32 queries for each
-    int64_t tiles;    // most tiles that the sequences can have
+    int64_t tiles;    // most tiles of kPromptRows queries that the sequences can have
     int splits;       // workgroups that share the keys of a tile
     int64_t rows;     // rows of partial results: splits * batch entries * q_tokens * q_heads
     int64_t bytes(int head_dim) const { return splits > 1 ? rows * (head_dim + 2) * 4 : 0; }
@@ -82,14 +81,9 @@ inline PromptPlan prompt_plan(const convrot_attention_args& a)
 {
     PromptPlan p{};
     const bool packed = a.q_starts_dev != nullptr;
-    const auto tiles = [&](int64_t rows) {   // packed: sum of ceil(len / rows) over the sequences, for any lengths
-        return packed ? (a.q_tokens + (rows - 1) * std::min(a.batch, a.q_tokens)) / rows : a.batch * ((a.q_tokens + rows - 1) / rows);
-    };
-    // Eight waves share a copy of the keys among 256 queries, where there are enough of
-    // them in each sequence (16384 causal queries of 32 heads: 2010 against 2050 us) and not
-    // where tiles end in the middle (seven ragged sequences of up to 3001: 226 against 206).
-    p.waves = prompt_direct(a) && a.head_dim > 96 && a.head_dim <= 128 && a.q_tokens >= 4096 * (packed ? a.batch : 1) && tiles(8 * kPromptRows) * a.q_heads >= 512 ? 8 : 4;
-    p.tiles = tiles(p.waves * kPromptRows);
+    // packed: sum of ceil(len / 128) over the sequences, for any lengths
+    p.tiles = packed ? (a.q_tokens + (kPromptRows - 1) * std::min(a.batch, a.q_tokens)) / kPromptRows
+                     : a.batch * ((a.q_tokens + kPromptRows - 1) / kPromptRows);
     // Few queries against many keys: the keys of a tile go to several workgroups, 256 keys
     // each at least, as many as fill the chip (two on each compute unit) and as it pays:
     // a step of 64 keys takes 1.4 us, or 2 us where two workgroups share a unit, a second

@@ -48,7 +48,7 @@ struct PromptParams {
     convrot_attention_args a;
     float* partial;      // outputs [splits][rows][head_dim], then maximum and sum [splits][rows][2]
     int64_t tiles, rows;
-    int splits, waves, group, direct;   // waves a workgroup; heads a key head; whether rows can be copied 16 bytes at a time
+    int splits, group, direct;   // heads a key head; whether rows can be copied 16 bytes at a time
     float scale;         // times log2(e)
 };
 
@@ -63,20 +63,20 @@ __device__ __forceinline__ int starts_at(const int* starts, int64_t b, int64_t r
 {
     return min(max(starts[b], 0), (int)rows);
 }
-__device__ __forceinline__ int tiles_of(const PromptParams& p, int64_t b, int rows)
+__device__ __forceinline__ int tiles_of(const PromptParams& p, int64_t b)
 {
     if (b >= p.a.batch) return 0;
     const int n = starts_at(p.a.q_starts_dev, b + 1, p.a.q_tokens) - starts_at(p.a.q_starts_dev, b, p.a.q_tokens);
-    return (max(n, 0) + rows - 1) / rows;
+    return (max(n, 0) + kPromptRows - 1) / kPromptRows;
 }
 
 // Tile t of all sequences'.  Up to 64 sequences, the tiles with the highest numbers
 // come first: under a causal mask they have the most keys, and what starts last
 // should be short.  More sequences follow one another.
-__device__ __forceinline__ bool find_prompt(const PromptParams& p, int64_t t, int rows, Prompt& x)
+__device__ __forceinline__ bool find_prompt(const PromptParams& p, int64_t t, Prompt& x)
 {
     if (!p.a.q_starts_dev) {
-        const int per = (int)((p.a.q_tokens + rows - 1) / rows);
+        const int per = (int)((p.a.q_tokens + kPromptRows - 1) / kPromptRows);
         x.b = (int)(t % p.a.batch);
         x.tile = per - 1 - (int)(t / p.a.batch);
         x.q0 = x.k0 = 0;
@@ -86,10 +86,10 @@ __device__ __forceinline__ bool find_prompt(const PromptParams& p, int64_t t, in
     }
     const int lane = __lane_id();
     if (p.a.batch <= 64) {
-        const int n = tiles_of(p, lane, rows);
+        const int n = tiles_of(p, lane);
         const auto from = [&](int level) { return wave_sum(max(n - level, 0)); };   // tiles numbered `level` or more
         if (t >= from(0)) return false;
-        int low = 0, high = (int)((p.a.q_tokens + rows - 1) / rows), above = 0;     // from(low) > t >= from(high) = above
+        int low = 0, high = (int)((p.a.q_tokens + kPromptRows - 1) / kPromptRows), above = 0;     // from(low) > t >= from(high) = above
         while (high - low > 1) {
             const int mid = (low + high) / 2, count = from(mid);
             if (count > t) low = mid;
@@ -105,7 +105,7 @@ __device__ __forceinline__ bool find_prompt(const PromptParams& p, int64_t t, in
         int rank = (int)t;
         for (;; b += 64) {
             if (b >= p.a.batch) return false;
-            const int n = tiles_of(p, b + lane, rows), sum = wave_scan(n), all = __builtin_amdgcn_readlane(sum, 63);
+            const int n = tiles_of(p, b + lane), sum = wave_scan(n), all = __builtin_amdgcn_readlane(sum, 63);
             if (rank < all) {
                 const int l = __builtin_ctzll(__ballot(sum > rank));
                 x.b = (int)b + l;
@@ -150,17 +150,15 @@ __device__ __forceinline__ U4 descriptor(const char* base, uint32_t bytes)
     return d;
 }
 
-// WIDTH: channels computed with, those of a head and zeros behind them.  WAVES: of 32
-// queries each.  DIRECT: keys and values are copied straight to shared
+// WIDTH: channels computed with, those of a head and zeros behind them.  DIRECT: keys and values are copied straight to shared
 // memory; otherwise (rows that do not begin with a multiple of 16 bytes, or overlap) by
 // way of registers.
-template <typename T, int WIDTH, int WAVES, bool DIRECT>
-__global__ __launch_bounds__(64 * WAVES, WIDTH > 128 ? 1 : 2) void prompt_kernel(PromptParams p)
+template <typename T, int WIDTH, bool DIRECT>
+__global__ __launch_bounds__(256, WIDTH > 128 ? 1 : 2) void prompt_kernel(PromptParams p)
 {
     constexpr int DIM = WIDTH <= 64 ? 64 : WIDTH <= 128 ? 128 : 256;     // of a row in shared memory: the permutations need a power of two
     constexpr int KEYS = kPromptKeys, ROW = 2 * DIM, PIECES = DIM / 8;   // bytes and 16-byte pieces of a row
-    constexpr int STAGE = KEYS * ROW, COPIES = KEYS * PIECES / (64 * WAVES), STEPS = WIDTH / 16, TILES = WIDTH / 32;
-    constexpr int ROWS = 32 * WAVES;
+    constexpr int STAGE = KEYS * ROW, COPIES = KEYS * PIECES / 256, STEPS = WIDTH / 16, TILES = WIDTH / 32;
     __shared__ __attribute__((aligned(16))) char shared[2][2][STAGE];    // keys, values; stages
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int col = lane % 32, half = lane / 32;
@@ -181,9 +179,9 @@ __global__ __launch_bounds__(64 * WAVES, WIDTH > 128 ? 1 : 2) void prompt_kernel
         t = id / p.a.q_heads;
     }
     Prompt x;
-    if (!find_prompt(p, t, ROWS, x)) return;
+    if (!find_prompt(p, t, x)) return;
     const int b = __builtin_amdgcn_readfirstlane(x.b), nq = __builtin_amdgcn_readfirstlane(x.nq), nk = __builtin_amdgcn_readfirstlane(x.nk);
-    const int first_row = __builtin_amdgcn_readfirstlane(x.tile) * ROWS;
+    const int first_row = __builtin_amdgcn_readfirstlane(x.tile) * kPromptRows;
     const int row = first_row + wave * 32 + col;        // this lane's query
     const int64_t kb = p.a.q_starts_dev ? 0 : b;        // batch entries lie apart unless packed
     const T* q_row = (const T*)p.a.q_dev + kb * p.a.q_batch_stride + (x.q0 + min(row, nq - 1)) * p.a.q_token_stride + head * p.a.q_head_stride;
@@ -192,7 +190,7 @@ __global__ __launch_bounds__(64 * WAVES, WIDTH > 128 ? 1 : 2) void prompt_kernel
 
     // keys that the rows see: row i those up to i + nk - nq under a causal mask
     const int shift = nk - nq;
-    const int last_row = min(first_row + ROWS, nq) - 1;
+    const int last_row = min(first_row + kPromptRows, nq) - 1;
     const int most = p.a.causal ? min(max(last_row + shift + 1, 0), nk) : nk;            // that any row sees
     const int least = p.a.causal ? min(max(first_row + shift + 1, 0), nk) : nk;          // that every row sees
     const int steps = (most + KEYS - 1) / KEYS;
@@ -609,7 +607,7 @@ __global__ __launch_bounds__(256) void prompt_join_kernel(PromptParams p)
 template <typename T, int WIDTH>
 void launch_prompt_width(const PromptParams& p, unsigned grid, hipStream_t s)
 {
-    p.direct ? prompt_kernel<T, WIDTH, 4, true><<<grid, 256, 0, s>>>(p) : prompt_kernel<T, WIDTH, 4, false><<<grid, 256, 0, s>>>(p);
+    p.direct ? prompt_kernel<T, WIDTH, true><<<grid, 256, 0, s>>>(p) : prompt_kernel<T, WIDTH, false><<<grid, 256, 0, s>>>(p);
 }
 template <typename T>
 void launch_prompt_dim(const PromptParams& p, unsigned grid, hipStream_t s)
@@ -617,7 +615,6 @@ void launch_prompt_dim(const PromptParams& p, unsigned grid, hipStream_t s)
     const int width = (p.a.head_dim + 31) / 32;
     if (width <= 2) launch_prompt_width<T, 64>(p, grid, s);
     else if (width == 3) launch_prompt_width<T, 96>(p, grid, s);
-    else if (width == 4 && p.waves == 8) prompt_kernel<T, 128, 8, true><<<grid, 512, 0, s>>>(p);
     else if (width == 4) launch_prompt_width<T, 128>(p, grid, s);
     else if (width <= 6) launch_prompt_width<T, 192>(p, grid, s);
     else launch_prompt_width<T, 256>(p, grid, s);
@@ -633,7 +630,6 @@ void launch_prompt_typed(const convrot_attention_args& a, const PromptPlan& plan
     p.partial = partial;
     p.tiles = plan.tiles;
     p.splits = plan.splits;
-    p.waves = plan.waves;
     p.rows = plan.rows / plan.splits;
     p.group = a.q_heads / a.k_heads;
     p.direct = prompt_direct(a);
