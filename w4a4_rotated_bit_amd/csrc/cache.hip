@@ -82,7 +82,7 @@ __global__ __launch_bounds__(256) void cache_kernel(CacheParams p)
         if constexpr (KIND >= CONVROT_CACHE_E4M3)
             scale = r.scales + page * r.scale_page + head * r.scale_head + place * r.scale_token + c / 4;
         if constexpr (WRITE) {
-            const auto v = load_chunk<uint16_t, 8>(dense);
+            const auto v = load_once<uint16_t, 8>(dense);
             if constexpr (KIND < CONVROT_CACHE_E4M3) {
                 *(U4*)(row + c * 16) = __builtin_bit_cast(U4, v);
             } else {
@@ -114,7 +114,7 @@ __global__ __launch_bounds__(256) void cache_kernel(CacheParams p)
                 }
             }
             typedef uint16_t H8 __attribute__((ext_vector_type(8)));
-            store_chunk<uint16_t, 8>(dense, __builtin_bit_cast(H8, v));
+            store_once<uint16_t, 8>(dense, __builtin_bit_cast(H8, v));
         }
     }
 }

@@ -377,7 +377,14 @@ __global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void paged_kernel(Paged
         };
 
         // Steps in registers in turn; a step's pages are asked for before its rows.
-        if (t0 < end) {
+        if (t0 + NW >= end) {
+            if (t0 < end) {     // one step: nothing to ask for ahead
+                Tile<KIND, DIM> x;
+                const Pages pages = pages_of(t0);
+                load(x, t0, pages);
+                step(x, t0, pages);
+            }
+        } else {
             constexpr int HELD = S::HELD;
             Tile<KIND, DIM> x[HELD];
             Pages pages[HELD];
