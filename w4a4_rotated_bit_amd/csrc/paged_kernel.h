@@ -104,6 +104,16 @@ __device__ __forceinline__ int share_of(int64_t units, int workgroups, int64_t u
     return (int)(((u + 1) * workgroups - 1) / units);
 }
 
+// Rows of 16-bit values are read with the hint that they are used once (in whole
+// lines: eight sequences of 16384 keys of 128 channels 104 -> 95 us); quantized ones,
+// whose loads take parts of a line, without (of 256 channels 125 against 154 us).
+template <bool ONCE, typename V>
+__device__ __forceinline__ V read_row(const char* at)
+{
+    if constexpr (ONCE) return __builtin_nontemporal_load((const V*)at);
+    else return *(const V*)at;
+}
+
 // The raw bytes of 32 keys and values, as a lane holds them.
 // DIM: padded width, 64, 128 or 256.
 template <int KIND, int DIM>
@@ -252,11 +262,11 @@ __global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void paged_kernel(Paged
 #pragma unroll
                 for (int i = 0; i < K_LOADS; ++i) {
                     if constexpr (K_PART == 16) {
-                        const U4 r = *(const U4*)(k_rows + k_off[i]);
+                        const U4 r = read_row<!S::QUANT, U4>(k_rows + k_off[i]);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) x.k[h][4 * i + j] = r[j];
                     } else {
-                        const U2 r = *(const U2*)(k_rows + k_off[i]);
+                        const U2 r = read_row<!S::QUANT, U2>(k_rows + k_off[i]);
                         x.k[h][0] = r[0];
                         x.k[h][1] = r[1];
                     }
@@ -268,10 +278,10 @@ __global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void paged_kernel(Paged
                         const char* at_v = v_rows + j * vr.token_stride + v_off[set];
                         uint32_t(&d)[S::V_WORDS] = x.v[4 * h + j][set];
                         if constexpr (S::V_BYTES == 16) {
-                            const U4 r = *(const U4*)at_v;
+                            const U4 r = read_row<!S::QUANT, U4>(at_v);
                             d[0] = r[0], d[1] = r[1], d[2] = r[2], d[3] = r[3];
                         } else if constexpr (S::V_BYTES == 8) {
-                            const U2 r = *(const U2*)at_v;
+                            const U2 r = read_row<!S::QUANT, U2>(at_v);
                             d[0] = r[0], d[1] = r[1];
                         } else if constexpr (S::V_BYTES == 4) {
                             d[0] = *(const uint32_t*)at_v;
