@@ -638,6 +638,34 @@ def test_attention_empty_calls(gpu):
     assert B.convrot_attention(q, none, none, q_starts=zero).shape == q.shape      # no sequences
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("batch,T,hidden,head_dim", [(1, 130, 256, 128), (3, 77, 192, 64)])
+def test_blocks_with_the_librarys_attention(gpu, batch, T, hidden, head_dim):
+    """The blocks' attention against the formula on the heads that they make, and the blocks
+    against themselves: the attended values, their bf16 roundings and sums are all that differ."""
+    from w4a4_rotated_bit_amd.flux_block import Block, ConditionedBlock, picture, rel_err, tokens
+    plain = ConditionedBlock(hidden, head_dim=head_dim).to(torch.bfloat16).cuda()
+    blk = ConditionedBlock(hidden, head_dim=head_dim, attention="library").to(torch.bfloat16).cuda()
+    x = tokens(batch * T, hidden).view(batch, T, hidden).cuda()
+    vec, pos = tokens(batch, hidden, seed=9).cuda(), picture(T, batch).cuda()
+    with torch.no_grad():
+        q, k, v = blk.qkv(x).view(batch, T, 3, blk.heads, head_dim).unbind(2)
+        got = B.convrot_attention(q, k, v)
+        for b in range(batch):
+            rows = [t[b].double().cpu().transpose(0, 1) for t in (q, k, v)]
+            want, bound, _, _ = attended(*rows, head_dim ** -0.5, None, torch.bfloat16)
+            close(got[b].transpose(0, 1), want, bound)
+        # the attended values fall to another step of 2^-8 at most here and there, and so
+        # may what is computed from them: the two sums, the norm between, the projections' outputs
+        assert rel_err(blk(x, vec, pos), plain(x, vec, pos)) <= 6 * 2.0 ** -8
+        one = Block(hidden, head_dim, attention="library").to(torch.bfloat16).cuda()
+        two = Block(hidden, head_dim).to(torch.bfloat16).cuda()
+        one.modulation, two.modulation = one.modulation.float(), two.modulation.float()
+        assert rel_err(one(x[0]), two(x[0])) <= 6 * 2.0 ** -8
+    with pytest.raises(ValueError):
+        Block(hidden, head_dim, attention="other")
+
+
 # ---- refusals ---------------------------------------------------------------------
 
 CACHE = dict(k_rows=P, k_scales=P + (1 << 20), k_page=1 << 12, k_head=1 << 10, k_token=64, k_spage=256, k_shead=64, k_stoken=4,

@@ -27,12 +27,14 @@ positions it, with the library's operators between its linears:
     x = x + gate1 * proj(attention);  h = LayerNorm(x) * (1 + scale2) + shift2
     x = x + gate2 * down(gelu_tanh(up(h)))
 The modulation runs in GroupedLinear, each residual update and the norm after
-it in one call, the norm and rotation of all heads in another; the attention
-and the GELU stay the harness.
+it in one call, the norm and rotation of all heads in another; the GELU stays
+the harness.  The attention of either block is the harness's too unless it is
+made with attention="library" (--attention library): then it is one call on the
+heads where the projection left them.
 
     python -m w4a4_rotated_bit_amd.flux_block [--tokens 1536] [--hidden 3072]
         [--rotation sylvester|regular] [--group-size 256] [--iters 20]
-        [--conditioned] [--batch 1]
+        [--conditioned] [--batch 1] [--attention torch|library]
 """
 from __future__ import annotations
 
@@ -48,10 +50,13 @@ from .module import ConvRotLinear, GroupedLinear, convert_linears
 
 
 class Block(torch.nn.Module):
-    def __init__(self, hidden: int, head_dim: int = 128, seed: int = 0):
+    def __init__(self, hidden: int, head_dim: int = 128, seed: int = 0, attention: str = "torch"):
         super().__init__()
         if hidden % head_dim:
             raise ValueError("hidden must be a multiple of the head size")
+        if attention not in ("torch", "library"):
+            raise ValueError(f"unknown attention {attention!r}")
+        self.attention = attention
         self.hidden, self.head_dim, self.heads = hidden, head_dim, hidden // head_dim
         self.qkv = torch.nn.Linear(hidden, 3 * hidden)
         self.proj = torch.nn.Linear(hidden, hidden)
@@ -75,10 +80,13 @@ class Block(torch.nn.Module):
         T, H = x.shape
         shift, scale = self.modulation[0], self.modulation[1]
         h = (self._norm(x) * (1 + scale) + shift).to(torch.bfloat16)
-        qkv = self.qkv(h).float().reshape(T, 3, self.heads, self.head_dim)
-        q, k, v = (qkv[:, i].transpose(0, 1).contiguous() for i in range(3))   # [heads, T, D] each
-        s = torch.bmm(q, k.transpose(1, 2).contiguous()) / self.head_dim ** 0.5
-        a = torch.bmm(torch.softmax(s, dim=-1), v).transpose(0, 1).reshape(T, H)
+        qkv = self.qkv(h).reshape(1, T, 3, self.heads, self.head_dim)
+        if self.attention == "library":
+            a = binding.convrot_attention(*qkv.unbind(2)).reshape(T, H)
+        else:
+            q, k, v = (qkv[0, :, i].float().transpose(0, 1).contiguous() for i in range(3))   # [heads, T, D] each
+            s = torch.bmm(q, k.transpose(1, 2).contiguous()) / self.head_dim ** 0.5
+            a = torch.bmm(torch.softmax(s, dim=-1), v).transpose(0, 1).reshape(T, H)
         x = (x.float() + self.proj(a.to(torch.bfloat16)).float()).to(torch.bfloat16)
         u = torch.nn.functional.gelu(self.up(self._norm(x).to(torch.bfloat16)).float(), approximate="tanh")
         return (x.float() + self.down(u.to(torch.bfloat16)).float()).to(torch.bfloat16)
@@ -87,8 +95,8 @@ class Block(torch.nn.Module):
 class ConditionedBlock(Block):
     """Block with a modulation of each batch entry, gates, and positioned heads."""
 
-    def __init__(self, hidden: int, head_dim: int = 128, seed: int = 0, axes=None):
-        super().__init__(hidden, head_dim, seed)
+    def __init__(self, hidden: int, head_dim: int = 128, seed: int = 0, axes=None, attention: str = "torch"):
+        super().__init__(hidden, head_dim, seed, attention)
         if axes is None:    # an eighth for the index, the rest halved for row and column
             index = head_dim // 16 * 2
             row = (head_dim - index) // 4 * 2
@@ -126,7 +134,8 @@ class ConditionedBlock(Block):
         q, k, v = self.qkv(h).view(B, T, 3, self.heads, self.head_dim).unbind(2)
         q, k = binding.convrot_rope(q, k, positions, self.freq, self.axis, qk_norm=True, q_weight=self.q_weight,
                                     k_weight=self.k_weight)
-        x, h = binding.convrot_residual_norm(x, self.proj(self._attend(q, k, v)), gate=gate1, scale=scale2, shift=shift2)
+        a = binding.convrot_attention(q, k, v).reshape(B, T, H) if self.attention == "library" else self._attend(q, k, v)
+        x, h = binding.convrot_residual_norm(x, self.proj(a), gate=gate1, scale=scale2, shift=shift2)
         return binding.convrot_residual_norm(x, self._feed_forward(h), gate=gate2, want_h=False)[0]
 
     def plain(self, x: torch.Tensor, vec: torch.Tensor, positions: torch.Tensor) -> torch.Tensor:
@@ -185,8 +194,8 @@ def time_ms(fn, x: torch.Tensor, iters: int) -> float:
 
 @torch.no_grad()
 def run(T: int = 1536, hidden: int = 3072, group_size: int = 256, rotation: str = "sylvester",
-        iters: int = 20) -> dict:
-    dense = Block(hidden).cuda().to(torch.bfloat16)
+        iters: int = 20, attention: str = "torch") -> dict:
+    dense = Block(hidden, attention=attention).cuda().to(torch.bfloat16)
     dense.modulation = dense.modulation.float()
     quant = copy.deepcopy(dense)
     swapped = convert_linears(quant, group_size, rotation)
@@ -211,8 +220,8 @@ def run(T: int = 1536, hidden: int = 3072, group_size: int = 256, rotation: str 
 
 @torch.no_grad()
 def run_conditioned(T: int = 1536, hidden: int = 3072, batch: int = 1, group_size: int = 256,
-                    rotation: str = "sylvester", iters: int = 20) -> dict:
-    dense = ConditionedBlock(hidden).cuda().to(torch.bfloat16)
+                    rotation: str = "sylvester", iters: int = 20, attention: str = "torch") -> dict:
+    dense = ConditionedBlock(hidden, attention=attention).cuda().to(torch.bfloat16)
     quant = copy.deepcopy(dense)
     swapped = convert_linears(quant, group_size, rotation, include=lambda name: name != "modulation_linear")
     if sorted(swapped) != ["down", "proj", "qkv", "up"]:
@@ -244,14 +253,16 @@ def main(argv=None) -> int:
     ap.add_argument("--iters", type=int, default=20)
     ap.add_argument("--conditioned", action="store_true", help="the modulated, gated and positioned block")
     ap.add_argument("--batch", type=int, default=1, help="batch entries of the conditioned block")
+    ap.add_argument("--attention", default="torch", choices=("torch", "library"))
     args = ap.parse_args(argv)
     if not torch.cuda.is_available():
         print("a GPU is required", file=sys.stderr)
         return 2
     if args.conditioned:
-        print(json.dumps(run_conditioned(args.tokens, args.hidden, args.batch, args.group_size, args.rotation, args.iters)))
+        print(json.dumps(run_conditioned(args.tokens, args.hidden, args.batch, args.group_size, args.rotation, args.iters,
+                                         args.attention)))
         return 0
-    print(json.dumps(run(args.tokens, args.hidden, args.group_size, args.rotation, args.iters)))
+    print(json.dumps(run(args.tokens, args.hidden, args.group_size, args.rotation, args.iters, args.attention)))
     return 0
 
 
