@@ -437,8 +437,9 @@ int convrot_validate_quantize_weight_grouped(const void* W_dev, int64_t N, int64
 #define CONVROT_CACHE_E4M3 6
 #define CONVROT_CACHE_E2M1 7
 
-/* The rows of the keys or of the values; strides in bytes, multiples of 16, and
- * rows_dev 16-byte aligned.  A row is head_dim values of the cache's kind. */
+/* The rows of the keys or of the values; strides in bytes, those of rows multiples
+ * of 16, and rows_dev 16-byte aligned; token strides at most 2^27.  A row is head_dim
+ * values of the cache's kind. */
 typedef struct {
     void* rows_dev;              /* [pages][heads][page_size] rows             */
     uint8_t* scales_dev;         /* head_dim / 32 bytes a row; NULL for BF16, F16 */

@@ -598,6 +598,67 @@ def test_attention_graphs_streams_and_repeats(gpu):
 
 
 @pytest.mark.gpu
+def test_attention_workspaces_of_captured_graphs(gpu):
+    """Calls that join partial results, captured in two graphs that are replayed in turn and
+    beside eager calls, each with a workspace of its own: none meets another's."""
+    page, hk, hq, dim = 64, 2, 8, 128
+    cache = new_cache(130, page, hk, dim, "same", "bf16", seed=1)
+    runs = []
+    for g in range(2):
+        table = torch.randperm(130, generator=torch.Generator().manual_seed(g)).int().view(2, 65).cuda()
+        lengths = torch.tensor([4100, 777 + g], dtype=torch.int32, device="cuda")
+        q = rand((2, hq, dim), 10 + g, torch.bfloat16).cuda()
+        pq, pk, pv = (rand((1, n, h, dim), 20 + 3 * g + i, torch.bfloat16).cuda() for i, (n, h) in enumerate(((40, hq), (3000, hk), (3000, hk))))
+        runs.append((lambda q=q, table=table, lengths=lengths: B.convrot_attention_paged(q, cache, table, lengths),
+                     lambda pq=pq, pk=pk, pv=pv: B.convrot_attention(pq, pk, pv, causal=True), lengths))
+    want = [(a(), b()) for a, b, _ in runs]
+    graphs, outs = [], []
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for a, b, _ in runs:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            outs.append((a(), b()))
+        graphs.append(graph)
+    for step in range(4):
+        for g in ((0, 1), (1, 0))[step % 2]:
+            graphs[g].replay()
+        eager = [(a(), b()) for a, b, _ in runs]
+        torch.cuda.synchronize()
+        for g in range(2):
+            assert torch.equal(outs[g][0], eager[g][0]) and torch.equal(outs[g][1], want[g][1]) and torch.equal(eager[g][1], want[g][1])
+        assert step or torch.equal(eager[0][0], want[0][0])
+        runs[step % 2][2][0] = 4100 - 1000 * step      # lengths are read when a graph runs
+
+
+@pytest.mark.gpu
+def test_prompt_broadcast_keys(gpu):
+    """Keys and values of stride 0: one token's for all, one batch entry's for all, one head's for all."""
+    n, dim = 150, 64
+    q, one, two = (rand(s, 1 + i, torch.bfloat16) for i, s in enumerate(((2, n, 4, dim), (1, n, 1, dim), (2, n, 1, dim))))
+    for kv in (one.cuda().expand(2, n, 2, dim), one[:, :1].cuda().expand(2, n, 2, dim), two.cuda().expand(2, n, 4, dim)):
+        assert 0 in kv.stride()
+        for causal in (False, True):
+            out = B.convrot_attention(q.cuda(), kv, kv, causal=causal)
+            for b in range(2):
+                rows = [t[b].double().transpose(0, 1) for t in (q, kv.cpu(), kv.cpu())]
+                want, bound, _, _ = attended(*rows, dim ** -0.5, 0 if causal else None, torch.bfloat16)
+                close(out[b].transpose(0, 1), want, bound)
+
+
+@pytest.mark.gpu
+def test_caches_keep_their_memory(gpu):
+    """A handle keeps the memory that it was made of."""
+    cache = B.new_kv_cache(4, 8, 2, 64, torch.bfloat16)
+    x = rand((32, 2, 64), 1, torch.bfloat16).cuda()
+    slots = torch.arange(32, device="cuda")
+    cache.k.data = torch.empty(0, dtype=torch.bfloat16, device="cuda")
+    others = [torch.full((4, 2, 8, 64), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(8)]
+    B.convrot_cache_write(x, x, slots, cache)
+    assert torch.equal(B.convrot_cache_read(cache, slots)[0], x) and all((t == 7).all() for t in others)
+
+
+@pytest.mark.gpu
 def test_attention_outputs_and_workspaces_given(gpu):
     q, k, v = (rand((2, 90, 4, 64), 1 + i, torch.bfloat16).cuda() for i in range(3))
     wide = torch.full((2, 4, 90, 64), 7.0, dtype=torch.bfloat16, device="cuda")
@@ -676,7 +737,7 @@ SAME = dict(k_scales=0, v_scales=0, kind=1, k_page=1 << 14, k_head=1 << 12, k_to
 BAD_CACHE = [{"pages": 0}, {"pages": 1 << 31}, {"page_size": 4}, {"page_size": 24}, {"page_size": 1 << 17}, {"heads": 0}, {"heads": 65536},
              {"head_dim": 0}, {"head_dim": 48}, {"head_dim": 288}, {"kind": 3}, {"kind": 0}, {"k_rows": 0}, {"v_rows": 0},
              {"k_rows": P + 8}, {"k_scales": 0}, {"v_scales": 0}, {"k_token": 72}, {"v_head": 1000}, {"k_page": -4096}, {"k_token": -64},
-             {"k_spage": -1}, {"k_page": 1 << 51}, {**SAME, "k_scales": P}, {**SAME, "head_dim": 12}]
+             {"k_spage": -1}, {"k_page": 1 << 51}, {"k_token": (1 << 27) + 16}, {"v_stoken": (1 << 27) + 1}, {**SAME, "k_scales": P}, {**SAME, "head_dim": 12}]
 
 
 @pytest.mark.parametrize("kw,write,read", [

@@ -42,10 +42,10 @@ bool known_cache(const convrot_kv_cache& c)
     for (const convrot_cache_rows* r : {&c.k, &c.v}) {
         if (!r->rows_dev || !aligned(r->rows_dev, 16)) return false;
         if ((r->page_stride | r->head_stride | r->token_stride) % 16) return false;
-        if (!reaches(c.pages, r->page_stride) || !reaches(c.heads, r->head_stride) || !reaches(c.page_size, r->token_stride)) return false;
+        if (!reaches(c.pages, r->page_stride) || !reaches(c.heads, r->head_stride) || !within(r->token_stride, 0, kMaxCacheTokenStride)) return false;
         if ((r->scales_dev != nullptr) != quantized) return false;
         if (quantized && (!reaches(c.pages, r->scale_page_stride) || !reaches(c.heads, r->scale_head_stride) ||
-                          !reaches(c.page_size, r->scale_token_stride)))
+                          !within(r->scale_token_stride, 0, kMaxCacheTokenStride)))
             return false;
     }
     return true;

@@ -78,11 +78,12 @@ __device__ __forceinline__ int64_t all_units(const PagedParams& p, int mine)
     return sum;
 }
 
-// The sequence that holds unit `at` of the line in which each unit counts `columns` times.
+// The sequence that holds unit `at` of the line in which each unit counts `columns` times
+// (none, with no units, only where lengths are written while they are read).
 __device__ __forceinline__ Place find_unit(const PagedParams& p, int mine, int64_t at)
 {
     int64_t before = 0;
-    for (int64_t b = 0;; b += 64) {
+    for (int64_t b = 0; b < p.a.batch; b += 64) {
         const int n = b == 0 ? mine : units_of(length_of(p, b + __lane_id()));
         const int sum = wave_scan(n);
         const uint64_t past = __ballot((before + sum) * p.columns > at);
@@ -93,6 +94,7 @@ __device__ __forceinline__ Place find_unit(const PagedParams& p, int mine, int64
         }
         before += __builtin_amdgcn_readlane(sum, 63);
     }
+    return Place{0, 0, 0};
 }
 
 // Every workgroup that shares has a unit: what lies between the first and the
@@ -163,6 +165,7 @@ __global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void paged_kernel(Paged
         u = share_begin(units, shares, blockIdx.x);
         last = share_begin(units, shares, blockIdx.x + 1);
         at = find_unit(p, mine, u);
+        if (at.units == 0) return;
         const int64_t rest = u - at.before * p.columns;
         column = (int)(rest / at.units);
         first = (int)(rest % at.units);
@@ -469,8 +472,10 @@ __global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void paged_kernel(Paged
         first = 0;
         if (++column == p.columns) {
             column = 0;
-            do at.units = units_of(length_of(p, ++at.b));
-            while (at.units == 0);
+            do {
+                if (++at.b >= p.a.batch) return;
+                at.units = units_of(length_of(p, at.b));
+            } while (at.units == 0);
         }
     }
 }

@@ -182,6 +182,7 @@ __global__ __launch_bounds__(256, WIDTH > 128 ? 1 : 2) void prompt_kernel(Prompt
     if (!find_prompt(p, t, x)) return;
     const int b = __builtin_amdgcn_readfirstlane(x.b), nq = __builtin_amdgcn_readfirstlane(x.nq), nk = __builtin_amdgcn_readfirstlane(x.nk);
     const int first_row = __builtin_amdgcn_readfirstlane(x.tile) * kPromptRows;
+    if (first_row >= nq) return;     // starts written while they are read
     const int row = first_row + wave * 32 + col;        // this lane's query
     const int64_t kb = p.a.q_starts_dev ? 0 : b;        // batch entries lie apart unless packed
     const T* q_row = (const T*)p.a.q_dev + kb * p.a.q_batch_stride + (x.q0 + min(row, nq - 1)) * p.a.q_token_stride + head * p.a.q_head_stride;
