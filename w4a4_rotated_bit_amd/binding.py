@@ -549,6 +549,7 @@ _GROUPS = (32, 64, 128)
 _torch = None   # the module, its types' codes and its current device and stream, from the first call on
 _forward = None   # its forward differentiation
 _types = {}
+_kinds = {}   # of a cache's rows: code, bytes and values of an element
 _current_device = _raw_stream = None
 
 
@@ -557,6 +558,8 @@ def _use_torch():
     import torch
     import torch.autograd.forward_ad as _forward
     _types.update({torch.bfloat16: CONVROT_BF16, torch.float16: CONVROT_F16, torch.float32: CONVROT_F32})
+    _kinds.update({torch.bfloat16: (CONVROT_BF16, 2, 1), torch.float16: (CONVROT_F16, 2, 1),
+                   torch.float8_e4m3fn: (CONVROT_CACHE_E4M3, 1, 1), torch.uint8: (CONVROT_CACHE_E2M1, 1, 2)})
     # The handles themselves: torch.cuda.current_stream builds an object around
     # one, which takes longer than a launch.
     _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
@@ -977,45 +980,49 @@ class KVCache:
 
     def __init__(self, k, v, k_scales=None, v_scales=None):
         device = _on_gpu(k, "cache.k")
-        for name, t in (("cache.k", k), ("cache.v", v)):
-            _check_tensor(t, name, device)
+        if k.requires_grad or not isinstance(v, _torch.Tensor) or v.get_device() != device or v.requires_grad:
+            _check_tensor(k, "cache.k", device)
+            _check_tensor(v, "cache.v", device)
         shape, dtype = k.shape, k.dtype
-        if len(shape) != 4 or v.shape != shape or v.dtype != dtype:
+        if len(shape) != 4 or v.shape != shape or v.dtype is not dtype:
             raise ValueError("the cache's k and v must be [pages, heads, page_size, ...] of one shape and type, got "
                              f"{tuple(shape)} {dtype} and {tuple(v.shape)} {v.dtype}")
         pages, heads, page_size, last = shape
-        if dtype is _torch.float8_e4m3fn:
-            kind, size, dim, kept = CONVROT_CACHE_E4M3, 1, last, None
-        elif dtype is _torch.uint8:
-            kind, size, dim, kept = CONVROT_CACHE_E2M1, 1, 2 * last, None
-        elif dtype is _torch.bfloat16:
-            kind, size, dim, kept = CONVROT_BF16, 2, last, dtype
-        elif dtype is _torch.float16:
-            kind, size, dim, kept = CONVROT_F16, 2, last, dtype
-        else:
-            raise TypeError(f"a cache keeps bfloat16, float16, float8_e4m3fn or uint8 (e2m1) rows, not {dtype}")
-        fields = []
-        for name, rows, scales in (("k", k, k_scales), ("v", v, v_scales)):
-            page, head, token, one = rows.stride()
-            if one != 1 and last > 1:
-                raise ValueError(f"cache.{name} must be dense in its last dimension")
-            at, steps = 0, (0, 0, 0)
-            if kept is None:
-                _check_tensor(scales, f"cache.{name}_scales", device)
-                if scales.dtype is not _torch.uint8 or scales.shape != (pages, heads, page_size, dim // 32):
-                    raise ValueError(f"cache.{name}_scales must be uint8 [pages, heads, page_size, head_dim / 32], got "
-                                     f"{scales.dtype} {tuple(scales.shape)}")
-                *steps, one = scales.stride()
-                if one != 1 and dim > 32:
-                    raise ValueError(f"cache.{name}_scales must be dense in its last dimension")
-                at = scales.data_ptr()
-            elif scales is not None:
+        try:
+            kind, size, values = _kinds[dtype]
+        except KeyError:
+            raise TypeError("a cache keeps bfloat16, float16, float8_e4m3fn or uint8 (e2m1) rows, not "
+                            f"{dtype}") from None
+        kp, kh, kt, one = k.stride()
+        vp, vh, vt, same = v.stride()
+        if (one != 1 or same != 1) and last > 1:
+            raise ValueError("the cache's k and v must be dense in their last dimension")
+        dim = last * values
+        if size == 2:
+            if k_scales is not None or v_scales is not None:
                 raise ValueError("a cache that keeps rows as they are has no scales")
-            fields += (rows.data_ptr(), at, page * size, head * size, token * size, *steps)
+            ks = vs = 0
+            steps = more = (0, 0, 0, 1)
+            self.kept = dtype
+            self._memory = k.untyped_storage(), v.untyped_storage()
+        else:
+            _check_tensor(k_scales, "cache.k_scales", device)
+            _check_tensor(v_scales, "cache.v_scales", device)
+            want = (pages, heads, page_size, dim // 32)
+            if k_scales.shape != want or v_scales.shape != want or not k_scales.dtype is v_scales.dtype is _torch.uint8:
+                raise ValueError("the cache's scales must be uint8 [pages, heads, page_size, head_dim / 32], got "
+                                 f"{k_scales.dtype} {tuple(k_scales.shape)} and {v_scales.dtype} {tuple(v_scales.shape)}")
+            steps, more = k_scales.stride(), v_scales.stride()
+            if (steps[3] != 1 or more[3] != 1) and dim > 32:
+                raise ValueError("the cache's scales must be dense in their last dimension")
+            ks, vs = k_scales.data_ptr(), v_scales.data_ptr()
+            self.kept = None
+            self._memory = k.untyped_storage(), v.untyped_storage(), k_scales.untyped_storage(), v_scales.untyped_storage()
         self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
-        self.heads, self.head_dim, self.kept, self.device = heads, dim, kept, device
-        self._fields = CACHE_FIELDS.pack(*fields, pages, page_size, heads, dim, kind)
-        self._memory = [t.untyped_storage() for t in (k, v, k_scales, v_scales) if t is not None]
+        self.heads, self.head_dim, self.device = heads, dim, device
+        self._fields = CACHE_FIELDS.pack(
+            k.data_ptr(), ks, kp * size, kh * size, kt * size, steps[0], steps[1], steps[2],
+            v.data_ptr(), vs, vp * size, vh * size, vt * size, more[0], more[1], more[2], pages, page_size, heads, dim, kind)
 
     def __iter__(self):
         return iter((self.k, self.v, self.k_scales, self.v_scales))
@@ -1146,16 +1153,16 @@ def convrot_cache_read(cache: KVCache, slots, dtype=None, k=None, v=None, stream
     slots_code = _slots_code(slots, tokens, device)
 
     def call(raw):
-        outs, strides = [], []
-        for name, t in (("k", k), ("v", v)):
-            if t is None:
-                t = slots.new_empty((tokens, heads, dim), dtype=dtype)
-                strides += (heads * dim, dim)
-            else:
-                strides += _token_rows(t, name, heads, dim, device)
-                if t.shape[0] != tokens or t.dtype is not dtype:
+        outs, strides = [k, v], (heads * dim, dim, heads * dim, dim)
+        if k is None and v is None:
+            outs = [slots.new_empty((tokens, heads, dim), dtype=dtype) for _ in range(2)]
+        else:
+            for i, name in enumerate("kv"):
+                if outs[i] is None:
+                    outs[i] = slots.new_empty((tokens, heads, dim), dtype=dtype)
+                elif outs[i].shape[:1] != (tokens,) or outs[i].dtype is not dtype:
                     raise ValueError(f"{name} must have {tokens} rows of {dtype}")
-            outs.append(t)
+            strides = _token_rows(outs[0], "k", heads, dim, device) + _token_rows(outs[1], "v", heads, dim, device)
         _call("convrot_cache_read", cache._fields + _ROWS_FIELDS.pack(
             outs[0].data_ptr(), outs[1].data_ptr(), slots.data_ptr(), tokens, *strides, slots_code, code), raw)
         if k is not None or v is not None:
