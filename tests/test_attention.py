@@ -316,6 +316,16 @@ def test_paged_shares(gpu, lengths):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["same", "e4m3", "e2m1"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
+def test_paged_short_tables(gpu, kind, dtype, dim):
+    """Tables of up to 384 keys: a sequence and key head are one workgroup's, without a second launch."""
+    check_paged([1, 0, 31, 33, 128, 255, 256, 257, 300], kind, dtype, q_heads=6, k_heads=3, dim=dim, seed=dim + 1)
+    check_paged([350, 8, 0], kind, dtype, q_heads=20, k_heads=1, dim=dim, page=8, seed=dim + 2)
+
+
+@pytest.mark.gpu
 def test_paged_large_and_ordered_scores(gpu):
     check_paged([700, 33, 128], "same", q_std=30.0, seed=1)
     check_paged([700, 33, 128], "e2m1", "f16", q_std=30.0, seed=2)
@@ -339,7 +349,8 @@ def test_paged_large_and_ordered_scores(gpu):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", ["same", "e4m3", "e2m1"])
-def test_paged_unseen_places_stay_out(gpu, kind):
+@pytest.mark.parametrize("wide", [0, 60])      # more columns of the table: shares of the keys
+def test_paged_unseen_places_stay_out(gpu, kind, wide):
     """NaN in every place that no sequence holds, in the rest of its last page, and on
     pages that its table does not name; entries that are no page hide their places."""
     page, heads, dim, n = 16, 2, 64, 83
@@ -347,7 +358,7 @@ def test_paged_unseen_places_stay_out(gpu, kind):
     k, v = (rand((n, heads, dim), 1 + i, torch.bfloat16) for i in (0, 1))
     bad = torch.full((12 * page, heads, dim), math.nan, dtype=torch.bfloat16, device="cuda")
     B.convrot_cache_write(bad, bad, torch.arange(12 * page, device="cuda"), cache)
-    table = torch.tensor([[7, 2, 9, -1, 4, 11, 3]], dtype=torch.int32)
+    table = torch.tensor([[7, 2, 9, -1, 4, 11, 3] + [-1] * wide], dtype=torch.int32)
     slots = torch.tensor([int(table[0, i // page]) * page + i % page if table[0, i // page] >= 0 else -1 for i in range(n)])
     B.convrot_cache_write(k.cuda(), v.cuda(), slots.cuda(), cache)
     q = rand((1, 4, dim), 5, torch.bfloat16)
@@ -357,7 +368,7 @@ def test_paged_unseen_places_stay_out(gpu, kind):
     close(out[0], want[:, 0], bound[:, 0])
     close(lse[0], want_lse[:, 0], lse_bound[:, 0])
     # no page is one of the cache's; lengths beyond the table, and below zero
-    none = torch.tensor([[-1, 12, 2 ** 31 - 1, -2 ** 31]] * 3, dtype=torch.int32, device="cuda")
+    none = torch.tensor([[-1, 12, 2 ** 31 - 1, -2 ** 31] + [-1] * wide] * 3, dtype=torch.int32, device="cuda")
     out, lse = B.convrot_attention_paged(q.expand(3, 4, dim).contiguous().cuda(), cache, none,
                                          torch.tensor([60, 2 ** 31 - 1, -7], dtype=torch.int32, device="cuda"), want_lse=True)
     assert not out.any() and (lse == -math.inf).all()

@@ -33,7 +33,10 @@ constexpr int kPagedTile = 32;     // keys of a wave's step
 constexpr int kPagedUnit = 128;    // keys that work is shared out by
 constexpr int kPagedWaves = 4;     // of a workgroup that has a share
 constexpr int kPagedWavesAlone = 8;     // of one that has a whole sequence
-constexpr int64_t kPagedAlone = 1024;   // most keys of such a sequence: a second launch takes longer than four steps
+// Most keys of such a sequence, by the width of the page table.  250 bf16 keys of 8 heads of
+// 128 take 6.8 us alone and 10.1 in shares that a second launch joins (128 such
+// sequences 34 and 37), 500 keys 10.6 and 10.3 (64 and 57).
+constexpr int64_t kPagedAlone = 384;
 constexpr int kPagedShares = 512;  // most workgroups that share the units: two on each compute unit
 
 struct PagedPlan {
