@@ -418,8 +418,8 @@ int convrot_validate_quantize_weight_grouped(const void* W_dev, int64_t N, int64
 /*
  *   o[h] = sum_j p[h][j] v[j] / sum_j p[h][j],  p[h][j] = exp(scale q[h] . k[j])
  * over the keys that a query sees.  Query heads share key heads in order: head
- * h reads key head h / (q_heads / k_heads).  A query that sees no key has o = 0
- * and lse = -infinity.  Scores, the softmax's running maximum and sum and the
+ * h reads key head h / (q_heads / k_heads).  A query that sees no key, or none of
+ * a score above -infinity, has o = 0 and lse = -infinity.  Scores, the softmax's running maximum and sum and the
  * outputs are held in binary32; p is rounded to the type of the heads before it
  * multiplies v.  lse (natural logarithm of sum_j p[h][j]) is optional.
  * Kernels are launched on the caller's stream and keep no state; a workspace
@@ -479,7 +479,9 @@ int convrot_validate_cache_read(const convrot_cache_args* args_host);
 /* One new token of each sequence against the cache: sequence b's keys are the
  * first lengths[b] places of the pages page_table[b][0], [1], ... (its own new key
  * among them, written before).  A length beyond the table's width counts as that
- * width, a negative one as 0; places of a page outside the cache are not seen. */
+ * width, a negative one as 0; places of a page outside the cache are not seen.
+ * batch times the cache's heads, each counted once for every 16 query heads that
+ * it serves, is at most 8388607. */
 typedef struct {
     convrot_kv_cache cache;
     const void* q_dev;           /* [batch][q_heads][head_dim]                 */
@@ -508,7 +510,8 @@ int convrot_validate_attention_paged(const convrot_attention_paged_args* args_ho
  * sequence are left as they were.  Without (both NULL) batch entries of q_tokens
  * queries and k_tokens keys lie batch strides apart.  causal: the last query sees
  * every key, the one before it all but the last, and so on; a query left without
- * a key has o = 0. */
+ * a key has o = 0.  Tiles of 128 queries (of each sequence, its last one begun)
+ * times q_heads are at most 16777215. */
 typedef struct {
     const void *q_dev, *k_dev, *v_dev;   /* [batch][tokens][heads][head_dim], packed: [tokens][heads][head_dim] */
     void* o_dev;

@@ -375,6 +375,40 @@ def test_paged_unseen_places_stay_out(gpu, kind, wide):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dim", [8, 40, 64, 72, 96, 128, 136, 200, 256])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_infinite_scores(gpu, dim, dtype):
+    """Keys whose product with a query is -infinity count for nothing, in heads of any width;
+    one of +infinity leaves no number, and so does a query that holds none, times a scale of 0 too."""
+    dt, n, heads = TYPES[dtype], 150, 2
+    q, k, v = (rand((rows, heads, dim), dim + i, dt) for i, rows in enumerate((3, n, n)))
+    q[:, :, 0] = 1
+    q[2, :, 0] = -1
+    k[::3, :, 0] = -math.inf
+    kept_keys = torch.arange(n) % 3 != 0
+    want, bound, want_lse, lse_bound = attended(*(t.double().transpose(0, 1) for t in (q[:2], k[kept_keys], v[kept_keys])), dim ** -0.5,
+                                                None, dt)
+    table = torch.arange(10, dtype=torch.int32).expand(3, 10).contiguous()
+    for extra in (0, 50):   # one workgroup a sequence, shares of the keys
+        cache = new_cache(10, 16, heads, dim, "same", dtype)
+        B.convrot_cache_write(k.cuda(), v.cuda(), torch.arange(n, device="cuda"), cache)
+        wide = torch.cat([table, torch.full((3, extra), -1, dtype=torch.int32)], 1).cuda()
+        lengths = torch.full((3,), n, dtype=torch.int32, device="cuda")
+        paged = B.convrot_attention_paged(q.cuda(), cache, wide, lengths, want_lse=True)
+        prompt = B.convrot_attention(q[None].cuda(), k[None].cuda(), v[None].cuda(), want_lse=True)
+        for out, lse in (paged, (prompt[0][0], prompt[1][0])):
+            close(out[:2].transpose(0, 1), want, bound)
+            close(lse[:2].T, want_lse, lse_bound)
+            assert out[2].isnan().all()
+    q[1, 0, dim - 1] = math.nan
+    k[::3, :, 0] = 1
+    out = B.convrot_attention(q[None].cuda(), k[None].cuda(), v[None].cuda(), scale=0.0)[0]
+    assert out[1, 0].isnan().all() and out.isnan().sum() == dim
+    want, bound, _, _ = attended(*(t.double().transpose(0, 1) for t in (q[::2], k, v)), 0.0, None, dt)
+    close(out[::2].transpose(0, 1), want, bound)
+
+
+@pytest.mark.gpu
 def test_paged_lengths_beyond_the_table(gpu):
     a = check_paged([64, 640], "same", page=16, table_extra=0, seed=3)
     cache = new_cache(46, 16, 2, 128, "same", "bf16", seed=3)
@@ -670,6 +704,20 @@ def test_caches_keep_their_memory(gpu):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["e2m1", "same"])
+def test_caches_of_resized_memory_are_refused(gpu, kind):
+    x = rand((2, 2, 64), 1, torch.bfloat16).cuda()
+    slots = torch.arange(2, device="cuda")
+    for i in range(4 if kind == "e2m1" else 2):
+        cache = new_cache(4, 8, 2, 64, kind, "bf16", seed=1)
+        tuple(cache)[i].untyped_storage().resize_(0)
+        for call in (lambda: B.convrot_cache_write(x, x, slots, cache), lambda: B.convrot_cache_read(cache, slots),
+                     lambda: B.convrot_attention_paged(x, cache, slots.int()[:, None], slots.int())):
+            with pytest.raises(ValueError):
+                call()
+
+
+@pytest.mark.gpu
 def test_attention_outputs_and_workspaces_given(gpu):
     q, k, v = (rand((2, 90, 4, 64), 1 + i, torch.bfloat16).cuda() for i in range(3))
     wide = torch.full((2, 4, 90, 64), 7.0, dtype=torch.bfloat16, device="cuda")
@@ -784,7 +832,10 @@ def test_cache_refusals(kw, write, read):
     ({"lengths": P + (40 << 20) + 1}, False), ({"q": 0}, False), ({"o": 0}, False), ({"q": P + (16 << 20) + 1}, False), ({"lse": P + (34 << 20) + 2}, False),
     ({"o_head_stride": 64}, False), ({"o_batch_stride": 0}, False), ({"q_batch_stride": 0}, True), ({"q_head_stride": -1}, False),
     ({"o": P + (16 << 20)}, False), ({"o": P}, False), ({"lse": P + (2 << 20)}, False), ({"lse": P + (32 << 20)}, False),
-    ({"o": P + (36 << 20)}, False), ({"lse": P + (40 << 20)}, False), (SAME, True), ({**SAME, "dtype": 2}, False),
+    ({"o": P + (36 << 20)}, False), ({"lse": P + (40 << 20)}, False),
+    *[({"batch": 2048, "q_heads": n, "heads": n, "k_page": 1 << 24, "v_page": 1 << 24, "q": 1 << 40, "o": 2 << 40, "o_batch_stride": 1 << 20,
+        "k_rows": 3 << 40, "v_rows": 4 << 40, "k_scales": 5 << 40, "v_scales": 6 << 40, "lse": 7 << 40}, n < 4096) for n in (4095, 4096)],
+    (SAME, True), ({**SAME, "dtype": 2}, False),
     *[(kw, False) for kw in BAD_CACHE],
 ])
 def test_paged_refusals(kw, ok):
@@ -818,6 +869,8 @@ def test_paged_refusals(kw, ok):
     ({"o_token_stride": 0}, False), ({"k_head_stride": 0, "k_batch_stride": 0}, True), ({"v_batch_stride": -1}, False), ({"o": P}, False),
     ({"o": P + (16 << 20)}, False), ({"lse": P + (48 << 20)}, False), ({"lse": P}, False),
     ({"q_starts": P + (48 << 20), "k_starts": P + (65 << 20)}, False),
+    *[({"batch": 4096, "q_heads": n, "k_heads": 1, "q": 1 << 40, "o": 2 << 40, "o_batch_stride": 1 << 25, "o_token_stride": 1 << 18,
+        "lse": 3 << 40}, n < 4096) for n in (4095, 4096)],
 ])
 def test_prompt_refusals(kw, ok):
     import ctypes

@@ -974,9 +974,10 @@ class KVCache:
     of 8, or of 32 with scales.  ``new_kv_cache`` allocates one.
 
     The tensors' places are taken when it is made, and their memory is kept as long as
-    it lives: a tensor that is set to other storage later needs a new KVCache."""
+    it lives: a tensor that is set to other storage later needs a new KVCache, and so does
+    a storage that is resized (its calls are refused)."""
 
-    __slots__ = ("k", "v", "k_scales", "v_scales", "heads", "head_dim", "kept", "device", "_fields", "_memory")
+    __slots__ = ("k", "v", "k_scales", "v_scales", "heads", "head_dim", "kept", "device", "_fields", "_memory", "_at")
 
     def __init__(self, k, v, k_scales=None, v_scales=None):
         device = _on_gpu(k, "cache.k")
@@ -1018,6 +1019,7 @@ class KVCache:
             ks, vs = k_scales.data_ptr(), v_scales.data_ptr()
             self.kept = None
             self._memory = k.untyped_storage(), v.untyped_storage(), k_scales.untyped_storage(), v_scales.untyped_storage()
+        self._at = [m.data_ptr() for m in self._memory]
         self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
         self.heads, self.head_dim, self.device = heads, dim, device
         self._fields = CACHE_FIELDS.pack(
@@ -1060,6 +1062,8 @@ def _check_cache(cache, device, dtype, what):
         raise TypeError("cache must be a KVCache")
     if cache.device != device:
         raise ValueError(f"the cache is on cuda:{cache.device}, {what} on cuda:{device}")
+    if [m.data_ptr() for m in cache._memory] != cache._at:
+        raise ValueError("the cache's memory was resized: it needs a new KVCache")
     kept = cache.kept
     if kept is not None:
         if kept is not dtype:

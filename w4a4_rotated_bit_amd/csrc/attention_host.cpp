@@ -108,7 +108,7 @@ int check_paged(const convrot_attention_paged_args* args, bool* empty)
     if (!within(a.table_width, 0, kMaxPlaces / a.cache.page_size) || !reaches(a.batch, a.table_stride)) return CONVROT_EINVAL;
     if (!reaches(a.batch, a.q_batch_stride) || !reaches(a.batch, a.o_batch_stride)) return CONVROT_EINVAL;
     if (!reaches(a.q_heads, a.q_head_stride) || !reaches(a.q_heads, a.o_head_stride)) return CONVROT_EINVAL;
-    if (a.batch * (int64_t)paged_plan(a).columns > 0x7fffffff) return CONVROT_EINVAL;   // workgroups of one launch
+    if (a.batch * (int64_t)paged_plan(a).columns > kMaxThreads / (64 * kPagedWavesAlone)) return CONVROT_EINVAL;
     if (a.batch == 0) {
         *empty = true;
         return CONVROT_OK;
@@ -157,7 +157,7 @@ int check_prompt(const convrot_attention_args* args, bool* empty)
     for (int64_t s : {a.k_head_stride, a.v_head_stride})
         if (!reaches(a.k_heads, s)) return CONVROT_EINVAL;
     const PromptPlan plan = prompt_plan(a);
-    if (plan.tiles * a.q_heads * plan.splits > 0x7fffffff) return CONVROT_EINVAL;   // workgroups of one launch
+    if (plan.tiles * a.q_heads * plan.splits > kMaxThreads / (2 * kPromptRows)) return CONVROT_EINVAL;   // two threads a query
     if (a.batch == 0 || a.q_tokens == 0) {
         *empty = true;
         return CONVROT_OK;

@@ -16,6 +16,7 @@ constexpr int64_t kMaxBatch = 65535;
 constexpr int64_t kMaxPlaces = (int64_t)1 << 30;   // of one sequence in a cache
 constexpr int64_t kMaxTokenStride = ((int64_t)1 << 24) - 1;   // 64 rows stay within 32-bit byte offsets
 constexpr int64_t kMaxCacheTokenStride = (int64_t)1 << 27;   // bytes: 16 rows stay within 32-bit offsets
+constexpr int64_t kMaxThreads = 0xffffffff;   // of one launch
 constexpr int kBlock = 32;                  // channels that share a scale
 
 inline bool cache_quantized(int kind) { return kind == CONVROT_CACHE_E4M3 || kind == CONVROT_CACHE_E2M1; }

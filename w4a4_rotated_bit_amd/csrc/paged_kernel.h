@@ -188,6 +188,8 @@ __global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void paged_kernel(Paged
     // Offsets of this lane's bytes from the first of 16 rows: row `col` of the keys, rows
     // 4 quad .. of the values.  What lies beyond the head is not read: its first bytes
     // stand for it, times a query's zeros, or for outputs that nobody reads.
+    // (Infinities among them would leave no number: 16-bit values are cleared, and `inside`
+    // makes a block's scale the smallest.)
     const convrot_cache_rows &kr = p.a.cache.k, &vr = p.a.cache.v;
     constexpr int K_PART = S::K_WORDS * 4 < 16 ? S::K_WORDS * 4 : 16;   // bytes of a load, all inside the head or beyond it
     constexpr int K_LOADS = S::K_WORDS * 4 / K_PART;
@@ -209,6 +211,10 @@ __global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void paged_kernel(Paged
         const int c = quad * S::LANE + i * kBlock;
         ks_off[i] = col * (uint32_t)kr.scale_token_stride + (c < dim ? c / kBlock : 0);
     }
+
+    uint32_t inside[(S::LANE + kBlock - 1) / kBlock];
+#pragma unroll
+    for (int i = 0; i < (S::LANE + kBlock - 1) / kBlock; ++i) inside[i] = quad * S::LANE + i * kBlock < dim ? ~0u : 0u;
 
     for (;;) {
         const int b = __builtin_amdgcn_readfirstlane(at.b), units = __builtin_amdgcn_readfirstlane(at.units);
@@ -320,15 +326,23 @@ __global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void paged_kernel(Paged
 
         const auto step = [&](Tile<KIND, DIM>& x, int t, const Pages& pages) {
             float s[8];
+            if constexpr (!S::QUANT) {
+                if (__builtin_expect(dim < DIM, 0)) {
+#pragma unroll
+                    for (int i = 0; i < S::K_WORDS; ++i)
+                        if (i / 4 * 32 + quad * 8 >= dim) x.k[0][i] = x.k[1][i] = 0;
+                }
+            }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 F4 acc{0, 0, 0, 0};
 #pragma unroll
                 for (int i = 0; i < S::STEPS; ++i) {
                     U4 a;
+                    const uint32_t in = inside[i * 8 / kBlock];
                     if constexpr (!S::QUANT) a = U4{x.k[h][4 * i], x.k[h][4 * i + 1], x.k[h][4 * i + 2], x.k[h][4 * i + 3]};
-                    else if constexpr (KIND == CONVROT_CACHE_E4M3) a = Unpack<T>::e4m3(x.k[h][2 * i], x.k[h][2 * i + 1], block_scale(x.ks[h][i * 8 / kBlock]));
-                    else a = Unpack<T>::e2m1(x.k[h][i], block_scale(x.ks[h][i * 8 / kBlock]));
+                    else if constexpr (KIND == CONVROT_CACHE_E4M3) a = Unpack<T>::e4m3(x.k[h][2 * i], x.k[h][2 * i + 1], block_scale(x.ks[h][i * 8 / kBlock] & in));
+                    else a = Unpack<T>::e2m1(x.k[h][i], block_scale(x.ks[h][i * 8 / kBlock] & in));
                     acc = Mfma16<T>::run(a, q[i], acc);
                 }
 #pragma unroll

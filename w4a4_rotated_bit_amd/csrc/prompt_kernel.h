@@ -209,15 +209,24 @@ __global__ __launch_bounds__(256, WIDTH > 128 ? 1 : 2) void prompt_kernel(Prompt
     const int open = least / KEYS;                      // steps without a mask
     const int limit = p.a.causal ? min(row + shift, nk - 1) : nk - 1;    // this lane's last key
 
-    // The scale's sign goes to the queries (exactly), and a scale of 0 makes them
-    // zeros: scores grow with the products.
+    // The scale's sign goes to the queries (exactly), and a scale of 0 is multiplied into
+    // them: scores grow with the products.
     const float scale = p.scale == 0.f ? 1.f : fabsf(p.scale);
     const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
     U4 q[STEPS];
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
         const int c = i * 16 + half * 8;
-        q[i] = c < dim && p.scale != 0.f ? __builtin_bit_cast(U4, load_chunk<uint16_t, 8>((const uint16_t*)q_row + c)) ^ flip : U4{0, 0, 0, 0};
+        q[i] = c < dim ? __builtin_bit_cast(U4, load_chunk<uint16_t, 8>((const uint16_t*)q_row + c)) ^ flip : U4{0, 0, 0, 0};
+        if (p.scale == 0.f) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                typedef T T2 __attribute__((ext_vector_type(2)));
+                const uint32_t word = q[i][k];
+                const T2 pair = __builtin_bit_cast(T2, word);
+                q[i][k] = pack2<T>((float)pair[0] * 0.f, (float)pair[1] * 0.f);
+            }
+        }
     }
 
     // copies: piece s of a stage holds piece (s % PIECES) ^ (row's permutation) of row s / PIECES
