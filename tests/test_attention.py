@@ -326,6 +326,15 @@ def test_paged_short_tables(gpu, kind, dtype, dim):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["same", "e4m3", "e2m1"])
+@pytest.mark.parametrize("lengths,heads", [([700, 0, 1, 33] * 130, 2), ([450, 3, 0, 129, 64] * 120, 1), ([0] * 590 + [900], 1),
+                                           ([2, 0, 385] * 400, 1)])
+def test_paged_many_sequences(gpu, kind, lengths, heads):
+    """More than the chip has room for, one workgroup each, and shares of several hundred."""
+    check_paged(lengths, kind, q_heads=3 * heads, k_heads=heads, dim=64, page=32, seed=len(lengths))
+
+
+@pytest.mark.gpu
 def test_paged_large_and_ordered_scores(gpu):
     check_paged([700, 33, 128], "same", q_std=30.0, seed=1)
     check_paged([700, 33, 128], "e2m1", "f16", q_std=30.0, seed=2)

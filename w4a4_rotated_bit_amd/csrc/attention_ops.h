@@ -38,6 +38,12 @@ constexpr int kPagedWavesAlone = 8;     // of one that has a whole sequence
 // 128 take 6.8 us alone and 10.1 in shares that a second launch joins (128 such
 // sequences 34 and 37), 500 keys 10.6 and 10.3 (64 and 57).
 constexpr int64_t kPagedAlone = 384;
+// With as many sequences and columns the chip is full without shares, and tables may be
+// longer (and four waves a workgroup do, which work on longer parts): 256 sequences of 1 to
+// 2000 e2m1 keys of 8 heads 93 us and 138 in shares, 128 of 1000 bf16 keys 98 and 101; where one
+// of 2000 keys stands among 255 of 100, 42 and 35.
+constexpr int64_t kPagedMany = 1024;
+constexpr int64_t kPagedAloneMany = 2048;
 constexpr int kPagedShares = 512;  // most workgroups that share the units: two on each compute unit
 
 struct PagedPlan {
@@ -54,7 +60,7 @@ inline PagedPlan paged_plan(const convrot_attention_paged_args& a)
     p.columns = a.cache.heads * ((group + kPagedHeads - 1) / kPagedHeads);
     p.slot = kPagedHeads * (padded_dim(a.cache.head_dim) + 2);
     const int64_t capacity = a.table_width * a.cache.page_size;
-    if (capacity <= kPagedAlone) return p;
+    if (capacity <= (a.batch * p.columns < kPagedMany ? kPagedAlone : kPagedAloneMany)) return p;
     const int64_t units = a.batch * p.columns * ((capacity + kPagedUnit - 1) / kPagedUnit);
     p.workgroups = (int)std::min<int64_t>(units, kPagedShares);
     return p;

@@ -72,16 +72,27 @@ struct Place {
 
 __device__ __forceinline__ int length_of(const PagedParams& p, int64_t b)
 {
-    return b < p.a.batch ? min(max(p.a.lengths_dev[b], 0), p.capacity) : 0;
+    const int n = p.a.lengths_dev[min(b, p.a.batch - 1)];    // read by every lane, so that many are under way
+    return b < p.a.batch ? min(max(n, 0), p.capacity) : 0;
 }
 __device__ __forceinline__ int units_of(int length) { return (length + kPagedUnit - 1) / kPagedUnit; }
+// The lanes' sequences of four times 64 from b on: at most 2^23 units each.
+struct Quad {
+    int n[4];
+    __device__ __forceinline__ Quad(const PagedParams& p, int64_t b)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) n[i] = units_of(length_of(p, b + 64 * i + __lane_id()));
+    }
+    __device__ __forceinline__ uint32_t sum() const { return (uint32_t)wave_sum(n[0] + n[1] + n[2] + n[3]); }
+};
 
 // The first 64 sequences' units are in the lanes of `mine`: most calls have no more,
 // and read the lengths once.
 __device__ __forceinline__ int64_t all_units(const PagedParams& p, int mine)
 {
     int64_t sum = wave_sum(mine);
-    for (int64_t b = 64; b < p.a.batch; b += 64) sum += wave_sum(units_of(length_of(p, b + __lane_id())));
+    for (int64_t b = 64; b < p.a.batch; b += 256) sum += Quad(p, b).sum();
     return sum;
 }
 
@@ -90,18 +101,32 @@ __device__ __forceinline__ int64_t all_units(const PagedParams& p, int mine)
 __device__ __forceinline__ Place find_unit(const PagedParams& p, int mine, int64_t at)
 {
     int64_t before = 0;
-    for (int64_t b = 0; b < p.a.batch; b += 64) {
-        const int n = b == 0 ? mine : units_of(length_of(p, b + __lane_id()));
+    Place found{};
+    const auto search = [&](int n, int64_t b) {
         const int sum = wave_scan(n);
         const uint64_t past = __ballot((before + sum) * p.columns > at);
         if (past) {
             const int l = __builtin_ctzll(past);
             const int units = __builtin_amdgcn_readlane(n, l);
-            return Place{(int)b + l, units, before + __builtin_amdgcn_readlane(sum, l) - units};
+            found = Place{(int)b + l, units, before + __builtin_amdgcn_readlane(sum, l) - units};
+            return true;
         }
         before += __builtin_amdgcn_readlane(sum, 63);
+        return false;
+    };
+    if (search(mine, 0)) return found;
+    for (int64_t b = 64; b < p.a.batch; b += 256) {
+        const Quad q(p, b);
+        const uint32_t sum = q.sum();
+        if ((before + sum) * p.columns <= at) {
+            before += sum;
+            continue;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (search(q.n[i], b + 64 * i)) return found;
     }
-    return Place{0, 0, 0};
+    return found;
 }
 
 // Every workgroup that shares has a unit: what lies between the first and the
@@ -519,10 +544,12 @@ __global__ __launch_bounds__(256) void paged_join_kernel(PagedParams p, int pitc
     if (mine > 0) {
         int64_t before = wave_sum(lane < b ? here : 0);
         units = wave_sum(here);
-        for (int64_t c = 64; c < p.a.batch; c += 64) {
-            const int n = units_of(length_of(p, c + lane));
-            units += wave_sum(n);
-            before += wave_sum(c + lane < b ? n : 0);
+        for (int64_t c = 64; c < p.a.batch; c += 256) {
+            Quad q(p, c);
+            units += q.sum();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) q.n[i] = c + 64 * i + lane < b ? q.n[i] : 0;
+            before += q.sum();
         }
         units *= p.columns;
         shares = sharing(p, units);
@@ -604,7 +631,7 @@ template <typename T, int KIND, int DIM>
 void launch_paged_dim(const PagedParams& p, unsigned grid, hipStream_t s)
 {
     constexpr int ALONE = DIM > 128 ? kPagedWaves : kPagedWavesAlone;    // registers for 256 channels leave one wave a SIMD
-    if (p.workgroups) paged_kernel<T, KIND, DIM, kPagedWaves><<<grid, 64 * kPagedWaves, 0, s>>>(p);
+    if (p.workgroups || grid >= kPagedMany) paged_kernel<T, KIND, DIM, kPagedWaves><<<grid, 64 * kPagedWaves, 0, s>>>(p);
     else paged_kernel<T, KIND, DIM, ALONE><<<grid, 64 * ALONE, 0, s>>>(p);
 }
 template <typename T, int KIND>
