@@ -421,7 +421,8 @@ int convrot_validate_quantize_weight_grouped(const void* W_dev, int64_t N, int64
  * h reads key head h / (q_heads / k_heads).  A query that sees no key, or none of
  * a score above -infinity, has o = 0 and lse = -infinity.  Scores, the softmax's running maximum and sum and the
  * outputs are held in binary32; p is rounded to the type of the heads before it
- * multiplies v.  lse (natural logarithm of sum_j p[h][j]) is optional.
+ * multiplies v, to half a step of each in bf16; in f16 to half a step of those that are 2^-25 of a
+ * query's largest one or more, and to 2^-36 of that one below.  lse (natural logarithm of sum_j p[h][j]) is optional.
  * Kernels are launched on the caller's stream and keep no state; a workspace
  * is written and read within one call, and holds nothing between calls.
  */

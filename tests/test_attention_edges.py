@@ -1,0 +1,98 @@
+"""Attention and its paged cache where they are easily wrong, against the formula in binary64.
+
+u = 2^-24 is half a step of binary32 relative to the value; a softmax weight and an
+output are each rounded to the heads' type (half a step, finfo.eps / 2 of it).  Weights
+in f16 are 2^11 where the largest is 1, so the half step of its subnormals, 2^-25, is
+2^-36 of that one."""
+import math
+
+import pytest
+import torch
+
+from w4a4_rotated_bit_amd import binding as B
+
+from .test_attention import new_cache
+from .test_block_ops import TYPES, U, close, half_step, rand
+
+FLAT = {torch.float16: 2.0 ** -36, torch.bfloat16: 0.0}   # half a step of the smallest weights
+
+
+def formula(q, k, v, scale, dtype, seen=None):
+    """(out, its bound, lse, its bound) of q [rows, dim], k, v [keys, dim] in binary64."""
+    n, dim = k.shape
+    s = (q @ k.T) * scale
+    slack = (dim + 4) * U * (q.abs() @ k.abs().T) * abs(scale) + 8 * U * (1 + s.abs())
+    if seen is not None:
+        s, slack = s.masked_fill(~seen, -math.inf), slack.masked_fill(~seen, 0.0)
+    w = torch.softmax(s, -1)
+    lost = slack.amax(-1, keepdim=True)
+    out = w @ v
+    share = torch.exp(s.amax(-1, keepdim=True) - torch.logsumexp(s, -1, keepdim=True))    # of the largest weight
+    bound = (w @ v.abs()) * (2 * lost + torch.finfo(dtype).eps / 2 + 2 * (n + 16) * U)
+    bound = bound + FLAT[dtype] * share * ((torch.ones_like(s) if seen is None else seen.double()) @ v.abs())
+    lse = torch.logsumexp(s, -1)
+    return out, bound + half_step(dtype, out.abs() + bound), lse, lost[:, 0] + (n + 16) * U + 4 * U * (1 + lse.abs())
+
+
+def paged(q, k, v, scale, page=16, wide=0):
+    """q [rows, dim] as that many query heads of one key head over a cache of k, v [keys, dim]."""
+    n, dim = k.shape
+    pages = -(-n // page)
+    cache = B.new_kv_cache(pages, page, 1, dim, k.dtype)
+    B.convrot_cache_write(k[:, None].cuda(), v[:, None].cuda(), torch.arange(n, device="cuda"), cache)
+    table = torch.full((1, pages + wide), -1, dtype=torch.int32)
+    table[0, :pages] = torch.arange(pages)
+    out, lse = B.convrot_attention_paged(q[None].cuda(), cache, table.cuda(), torch.tensor([n], dtype=torch.int32, device="cuda"),
+                                         scale=scale, want_lse=True)
+    return out[0], lse[0]
+
+
+def prompt(q, k, v, scale, causal=False):
+    out, lse = B.convrot_attention(q[None, :, None].cuda(), k[None, :, None].cuda(), v[None, :, None].cuda(), scale=scale,
+                                   causal=causal, want_lse=True)
+    return out[0, :, 0], lse[0, :, 0]
+
+
+# ---- weights far below the largest ---------------------------------------------------
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("gap", [10.0, 15.0, 17.0, 17.5, 19.0])
+@pytest.mark.parametrize("where", ["first", "last", "often"])
+def test_many_keys_far_below_one_of_no_value(gpu, dtype, gap, where):
+    """A key that takes nearly all of the weight and whose value is zero: the output is what
+    many small weights leave."""
+    dt, dim = TYPES[dtype], 64
+    for n, rows, call in ((32768, 5, prompt), (32768, 130, prompt), (700, 3, prompt), (380, 4, paged), (30000, 4, paged)):
+        q, k = torch.zeros((rows, dim), dtype=dt), torch.zeros((n, dim), dtype=dt)
+        v = (1 + rand((n, dim), 1, torch.float32, 0.25)).to(dt)
+        q[:, 0], k[:, 1] = 1, rand((n,), 2, dt, 0.5)
+        q[:, 1] = 1
+        top = {"first": slice(0, 1), "last": slice(n - 1, n), "often": slice(0, n, 32)}[where]
+        k[top, 0], k[top, 1], v[top] = gap, 0, 0
+        got, lse = call(q, k, v, 1.0)
+        want, bound, want_lse, lse_bound = formula(q.double(), k.double(), v.double(), 1.0, dt)
+        close(got, want, bound, f"{call.__name__} of {n} keys")
+        close(lse, want_lse, lse_bound, f"lse of {n} keys")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_scores_that_rise_step_by_step(gpu, dtype):
+    """Steps of keys whose scores rise by less and by more than the running reference's room."""
+    dt, n, dim = TYPES[dtype], 640, 64
+    for rise in (1.0, 2.5, 2.75, 3.0, 5.5, 8.0, 10.25, 10.5, 11.0):    # 4, 8 and 15 in base 2 are 2.77, 5.55 and 10.4
+        q, k = torch.zeros((40, dim), dtype=dt), torch.zeros((n, dim), dtype=dt)
+        q[:, 0], k[:, 0] = 1, (torch.arange(n) // 64 * rise).to(dt)
+        v = rand((n, dim), 3, dt)
+        for call, rows in ((prompt, 40), (paged, 3)):
+            got, lse = call(q[:rows], k, v, 1.0)
+            want, bound, want_lse, lse_bound = formula(q[:rows].double(), k.double(), v.double(), 1.0, dt)
+            close(got, want, bound, f"{call.__name__}, {rise} a step")
+            close(lse, want_lse, lse_bound, f"{call.__name__}, lse")
+        got, lse = prompt(q, k, v, 1.0, causal=True)
+        seen = torch.arange(n)[None] <= torch.arange(40)[:, None] + n - 40
+        want, bound, want_lse, lse_bound = formula(q.double(), k.double(), v.double(), 1.0, dt, seen)
+        close(got, want, bound, "causal")
+        close(lse, want_lse, lse_bound, "causal, lse")

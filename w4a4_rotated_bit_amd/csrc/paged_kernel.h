@@ -9,9 +9,8 @@
 // which that operand wants by channel, are loaded by row, eight channels of
 // eight keys a lane, and transposed within the lane's registers.  No value
 // crosses shared memory before the waves' results are joined.
-// The running maximum of a head only moves when a score exceeds it by 2^8
-// (a factor that binary32 sums and 16-bit weights of the softmax bear), so most
-// steps rescale nothing.
+// The reference of a head's weights only moves when a score exceeds it by so much that
+// 16-bit weights ask for it (Reference), so most steps rescale nothing.
 //
 // Bound by the bytes of the keys and values: one to three steps' rows are under way
 // while one is computed, and a row costs no address arithmetic but that of its
@@ -27,7 +26,7 @@
 // Work is shared out in units of 128 keys, over all sequences and key heads in
 // one line that the workgroups cut into equal parts: the lengths are known on
 // the GPU alone.  A workgroup's part may end inside a sequence; such ends go to
-// the workspace as partial results (maximum, sum, unscaled outputs) and a second
+// the workspace as partial results (reference, sum, unscaled outputs) and a second
 // launch joins them (5 us).  No atomics: the same bits on every run.
 #pragma once
 #include <hip/hip_runtime.h>
@@ -394,8 +393,8 @@ __global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void paged_kernel(Paged
             float most = s[0];
 #pragma unroll
             for (int j = 1; j < 8; ++j) most = fmaxf(most, s[j]);
-            if (__ballot(most > m + 8.f)) {
-                const float next = fmaxf(m, max4(most));
+            if (__ballot(most > m + Reference<T>::kRoom)) {
+                const float next = fmaxf(m, max4(most) - Reference<T>::kLift);
                 const float f = next == -kInf ? 0.f : exp2_fast(m - next);
                 sum *= f;
 #pragma unroll
@@ -408,7 +407,7 @@ __global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void paged_kernel(Paged
                 s[j] = exp2_fast(s[j] - base);
                 sum += s[j];
             }
-            // weights rounded to T: at most half a step of each, as the outputs are
+            // weights rounded to T, as the outputs are (Reference)
             const U4 w{pack2<T>(s[0], s[1]), pack2<T>(s[2], s[3]), pack2<T>(s[4], s[5]), pack2<T>(s[6], s[7])};
 #pragma unroll
             for (int set = 0; set < S::SETS; ++set) {
@@ -503,7 +502,7 @@ __global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void paged_kernel(Paged
                 store_chunk<uint16_t, 4>((uint16_t*)p.a.o_dev + b * p.a.o_batch_stride + (q_head + h) * p.a.o_head_stride + c,
                                          __builtin_bit_cast(H4, packed));
                 if (c == 0 && p.a.lse_dev)
-                    p.a.lse_dev[(int64_t)b * p.a.q_heads + q_head + h] = total == 0.f ? -kInf : (most + __log2f(total)) * kLn2;
+                    p.a.lse_dev[(int64_t)b * p.a.q_heads + q_head + h] = log_sum<T>(most, total);
             } else {
                 *(F4*)(slot + 2 * kPagedHeads + h * DIM + c) = out;
                 if (c == 0) {
@@ -587,7 +586,7 @@ __global__ __launch_bounds__(256) void paged_join_kernel(PagedParams p, int pitc
         total = lane_sum<64>(total);
         if (lane == 0) {
             scales[h] = total == 0.f ? 0.f : 1.f / total;
-            if (p.a.lse_dev) p.a.lse_dev[(int64_t)b * p.a.q_heads + q_head + h] = total == 0.f ? -kInf : (most + __log2f(total)) * kLn2;
+            if (p.a.lse_dev) p.a.lse_dev[(int64_t)b * p.a.q_heads + q_head + h] = log_sum<T>(most, total);
         }
     }
     __syncthreads();

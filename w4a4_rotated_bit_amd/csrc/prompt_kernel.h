@@ -56,7 +56,7 @@ struct Mfma32<_Float16> {
 
 struct PromptParams {
     convrot_attention_args a;
-    float* partial;      // outputs [splits][rows][head_dim], then maximum and sum [splits][rows][2]
+    float* partial;      // outputs [splits][rows][head_dim], then reference and sum [splits][rows][2]
     int64_t tiles, rows;
     int splits, group, direct;   // heads a key head; whether rows can be copied 16 bytes at a time
     float scale;         // times log2(e)
@@ -320,10 +320,10 @@ __global__ __launch_bounds__(256, WIDTH > 128 ? 1 : 2) void prompt_kernel(Prompt
             for (int i = 0; i < 16; ++i)
                 if (kt * 32 + 8 * (i / 4) + i % 4 > mine) x.s[kt][i] = -kInf;
     };
-    // The running maximum moves when one of these scores exceeds it by 2^8.
+    // The reference of the weights moves when one of these scores leaves its room.
     const auto raise = [&](float top) {
-        if (__ballot(top > m + 8.f)) {
-            const float next = fmaxf(m, max32(top));
+        if (__ballot(top > m + Reference<T>::kRoom)) {
+            const float next = fmaxf(m, max32(top) - Reference<T>::kLift);
             const float f = next == -kInf ? 0.f : exp2_fast(m - next);
             sum *= f;
 #pragma unroll
@@ -341,7 +341,7 @@ __global__ __launch_bounds__(256, WIDTH > 128 ? 1 : 2) void prompt_kernel(Prompt
         x.s[e / 16][e % 16] = exp2_fast(__builtin_fmaf(x.s[e / 16][e % 16], scale, -from));
         sum += x.s[e / 16][e % 16];
     };
-    // weights rounded to T: at most half a step of each, as the outputs are
+    // weights rounded to T, as the outputs are (Reference)
     const auto weights = [&](const Scores& x, int n) {
         const F16v& s = x.s[n / 2];
         const int e = n % 2 * 8;
@@ -569,7 +569,7 @@ __global__ __launch_bounds__(256, WIDTH > 128 ? 1 : 2) void prompt_kernel(Prompt
             if (ch < dim) store_chunk<uint16_t, 8>(out + ch, __builtin_bit_cast(H8, all));
         }
     if (half == 0 && p.a.lse_dev)
-        p.a.lse_dev[(kb * p.a.q_tokens + out_row) * p.a.q_heads + head] = sum == 0.f ? -kInf : (m + __log2f(sum)) * kLn2;
+        p.a.lse_dev[(kb * p.a.q_tokens + out_row) * p.a.q_heads + head] = log_sum<T>(m, sum);
 }
 
 // The partial results of each row and head, joined: a wave a row of a head.
@@ -587,7 +587,7 @@ __global__ __launch_bounds__(256) void prompt_join_kernel(PromptParams p)
         b = row / p.a.q_tokens;
         at = row % p.a.q_tokens;
     }
-    // a lane a part: its maximum, sum, and what it counts for
+    // a lane a part: its reference, sum, and what it counts for
     const float* stats = p.partial + p.splits * p.rows * dim + 2 * (lane * p.rows + r);
     const float m = lane < p.splits ? stats[0] : -kInf, l = lane < p.splits ? stats[1] : 0.f;
     float most = m;
@@ -621,7 +621,7 @@ __global__ __launch_bounds__(256) void prompt_join_kernel(PromptParams p)
     if (lane < per)
         store_chunk<uint16_t, 4>((uint16_t*)p.a.o_dev + b * p.a.o_batch_stride + at * p.a.o_token_stride + head * p.a.o_head_stride + c,
                                  __builtin_bit_cast(H4, U2{pack2<T>(sum[0] * s, sum[1] * s), pack2<T>(sum[2] * s, sum[3] * s)}));
-    if (lane == 0 && p.a.lse_dev) p.a.lse_dev[r] = total == 0.f ? -kInf : (most + __log2f(total)) * kLn2;
+    if (lane == 0 && p.a.lse_dev) p.a.lse_dev[r] = log_sum<T>(most, total);
 }
 
 template <typename T, int WIDTH>
