@@ -96,3 +96,61 @@ def test_scores_that_rise_step_by_step(gpu, dtype):
         want, bound, want_lse, lse_bound = formula(q.double(), k.double(), v.double(), 1.0, dt, seen)
         close(got, want, bound, "causal")
         close(lse, want_lse, lse_bound, "causal, lse")
+
+
+# ---- scores whose steps in binary32 are large ------------------------------------------
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,power", [(t, p) for t in ("f16", "bf16") for p in (20, 24, 27, 29, 40, 100) if p < 30 or t == "bf16"])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_large_scores(gpu, dtype, sign, power):
+    """Scores so far apart that the largest takes all of the weight, or two of one size half each;
+    magnitudes at which binary32 no longer tells a score from the next whole number."""
+    dt, n, dim = TYPES[dtype], 450, 64
+    for seed in range(4):
+        top = (7 + 53 * seed) % n
+        q, k = torch.zeros((130, dim), dtype=dt), torch.zeros((n, dim), dtype=dt)
+        q[:, 0] = sign * 2.0 ** (power // 2) * (1 + torch.arange(130) % 8 / 8)
+        steps = torch.randint(1, 64, (n,), generator=torch.Generator().manual_seed(seed)) / 128
+        k[:, 0] = 2.0 ** (power - power // 2) * (1 + (steps if sign < 0 else 0.75 - steps))
+        k[top, 0] = 2.0 ** (power - power // 2) * (1.875 if sign > 0 else 1.0)
+        twin = (top + 200) % n
+        if seed % 2:
+            k[twin] = k[top]
+        v = rand((n, dim), 5 + seed, dt)
+        want = ((v[top].double() + v[twin].double()) / 2 if seed % 2 else v[top].double()).expand(130, dim)
+        bound = half_step(dt, want.abs()) + (4 * U + torch.finfo(dt).eps / 2) * (v[top].double().abs() + v[twin].double().abs())
+        want_lse = q[:, 0].double() * k[top, 0].double() + math.log(1 + seed % 2)
+        for call, rows in ((prompt, 130), (prompt, 3), (paged, 3)):
+            got, lse = call(q[:rows], k, v, 1.0)
+            close(got, want[:rows], bound[:rows], f"{call.__name__}, {rows} rows, key {top}")
+            close(lse, want_lse[:rows], 8 * U * (1 + want_lse[:rows].abs()), "lse")
+        got, lse = prompt(q, k, v, 1.0, causal=True)        # rows from the one whose last key is `top` on see it
+        first = max(top if not seed % 2 else max(top, twin), n - 130) - (n - 130)
+        close(got[first:], want[first:], bound[first:], f"causal, key {top}")
+        close(lse[first:], want_lse[first:], 8 * U * (1 + want_lse[first:].abs()), "causal, lse")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("base", [22, 24, 25, 26, 27, 28])
+def test_scores_one_step_of_binary32_apart(gpu, dtype, base):
+    """Scores in base 2 of 2^base and a few steps of binary32 more: the reference of the weights
+    may not lag by a rounding of its own."""
+    dt, n, dim = TYPES[dtype], 384, 64
+    scale = 0.6931471805599453      # times log2(e), both in binary32: 1
+    assert (torch.tensor(scale) * torch.tensor(1.4426950408889634)).item() == 1.0
+    step = 2.0 ** (base - 23)
+    q, k = torch.zeros((3, dim), dtype=dt), torch.zeros((n, dim), dtype=dt)
+    q[:, 0], q[:, 1] = 2.0 ** (base - 13), 1
+    k[:, 0] = 2.0 ** 13
+    for ramp in ((torch.arange(n) // 64).float(), (torch.arange(n) // 256 + 1).float(), 6 - (torch.arange(n) // 64).float()):
+        k[:, 1] = ramp * step
+        v = rand((n, dim), base, dt)
+        w = torch.softmax(ramp.double() * step * math.log(2.0), 0)
+        want = (w @ v.double()).expand(3, dim)
+        bound = (w @ v.double().abs()) * (torch.finfo(dt).eps / 2 + 2 * (n + 16) * U) + FLAT[dt] * v.double().abs().sum(0)
+        bound = bound + half_step(dt, want.abs() + bound)
+        for call in (prompt, paged):
+            close(call(q, k, v, scale)[0], want, bound, f"{call.__name__} {ramp[:2].tolist()}")

@@ -172,6 +172,26 @@ template <>
 struct Reference<_Float16> {
     static constexpr float kLift = 11.f, kRoom = 15.f;
 };
+// From here on binary32 holds every second whole number at most.  The lift would be
+// rounded there to as much as leaves f16's range, and nothing needs it: weights that are
+// neither 0 nor 1 are 2^-2 or less and few.
+constexpr float kCoarse = 0x1p24f;
+// The reference for a largest score.
+template <typename T>
+__device__ __forceinline__ float reference(float most)
+{
+    if constexpr (Reference<T>::kLift == 0.f) return most;
+    return fabsf(most) < kCoarse ? most - Reference<T>::kLift : most;
+}
+// Whether a score leaves the room of its reference.  The difference of neighbouring numbers
+// is exact, where a sum of the reference and its room is rounded by up to half a step: to
+// bf16, which bears more than 2^8 too, that is all the same.
+template <typename T>
+__device__ __forceinline__ bool leaves_room(float most, float m)
+{
+    if constexpr (Reference<T>::kLift == 0.f) return most > m + Reference<T>::kRoom;
+    return most - m > Reference<T>::kRoom;
+}
 // The natural logarithm of a sum of weights.
 template <typename T>
 __device__ __forceinline__ float log_sum(float m, float sum)

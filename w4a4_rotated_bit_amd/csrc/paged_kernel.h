@@ -393,8 +393,8 @@ __global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void paged_kernel(Paged
             float most = s[0];
 #pragma unroll
             for (int j = 1; j < 8; ++j) most = fmaxf(most, s[j]);
-            if (__ballot(most > m + Reference<T>::kRoom)) {
-                const float next = fmaxf(m, max4(most) - Reference<T>::kLift);
+            if (__ballot(leaves_room<T>(most, m))) {
+                const float next = fmaxf(m, reference<T>(max4(most)));
                 const float f = next == -kInf ? 0.f : exp2_fast(m - next);
                 sum *= f;
 #pragma unroll
@@ -404,6 +404,7 @@ __global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void paged_kernel(Paged
             const float base = m == -kInf ? 0.f : m;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
+#pragma clang fp contract(off)     // the score is the rounded one that the reference was taken from
                 s[j] = exp2_fast(s[j] - base);
                 sum += s[j];
             }

@@ -322,8 +322,8 @@ __global__ __launch_bounds__(256, WIDTH > 128 ? 1 : 2) void prompt_kernel(Prompt
     };
     // The reference of the weights moves when one of these scores leaves its room.
     const auto raise = [&](float top) {
-        if (__ballot(top > m + Reference<T>::kRoom)) {
-            const float next = fmaxf(m, max32(top) - Reference<T>::kLift);
+        if (__ballot(leaves_room<T>(top, m))) {
+            const float next = fmaxf(m, reference<T>(max32(top)));
             const float f = next == -kInf ? 0.f : exp2_fast(m - next);
             sum *= f;
 #pragma unroll
@@ -337,8 +337,11 @@ __global__ __launch_bounds__(256, WIDTH > 128 ? 1 : 2) void prompt_kernel(Prompt
         for (int i = 1; i < 16; ++i) top = fmaxf(fmaxf(top, x.s[0][i]), x.s[1][i]);
         return top * scale;
     };
+    // the careful pass's weights: of the rounded score that the reference was taken from
     const auto weigh = [&](Scores& x, int e, float from) {
-        x.s[e / 16][e % 16] = exp2_fast(__builtin_fmaf(x.s[e / 16][e % 16], scale, -from));
+#pragma clang fp contract(off)
+        const float s = x.s[e / 16][e % 16] * scale;
+        x.s[e / 16][e % 16] = exp2_fast(s - from);
         sum += x.s[e / 16][e % 16];
     };
     // weights rounded to T, as the outputs are (Reference)
@@ -469,17 +472,24 @@ __global__ __launch_bounds__(256, WIDTH > 128 ? 1 : 2) void prompt_kernel(Prompt
         step(j, std::integral_constant<int, kLast>{}, cur, out);
     }
 
-    // Weights of 0 times a masked value that is no number leave no number behind:
-    // then the rows are computed once more, step by step, with values that are no
-    // numbers left out of the products, and counted for the queries that see them:
-    // 1 for an infinity, 128 for a negative one, 16384 for a NaN, each at most 64 times.
-    if (p.a.causal && open < end && begin < end) {
-        float check = 0.f;
+    // The careful pass.  Weights of 0 times a masked value that is no number leave no number
+    // behind; and the exponent's fma takes the exact score, where the reference is a rounded
+    // one: beyond kCoarse that leaves more than half between them, and weights that overflow
+    // or vanish.  In either case the rows are computed once more, step by step, from rounded
+    // scores, with values that are no numbers left out of the products, and counted for the
+    // queries that see them: 1 for an infinity, 128 for a negative one, 16384 for a NaN, each
+    // at most 64 times.
+    if (begin < end) {
+        bool again = fabsf(m) >= kCoarse && m != -kInf;
+        if (p.a.causal && open < end) {
+            float check = 0.f;
 #pragma unroll
-        for (int c = 0; c < TILES; ++c)
+            for (int c = 0; c < TILES; ++c)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) check += o[c][e] * 0.f;
-        if (__syncthreads_or(!(check == 0.f))) {
+                for (int e = 0; e < 16; ++e) check += o[c][e] * 0.f;
+            again |= !(check == 0.f);
+        }
+        if (__syncthreads_or(again)) {
             constexpr uint16_t one = __builtin_bit_cast(uint16_t, (T)1.f), many = __builtin_bit_cast(uint16_t, (T)128.f),
                                most16 = __builtin_bit_cast(uint16_t, (T)16384.f), top16 = __builtin_bit_cast(uint16_t, (T)kInf);
             m = -kInf;
