@@ -494,7 +494,7 @@ typedef struct {
     int64_t q_batch_stride, q_head_stride, o_batch_stride, o_head_stride;   /* elements */
     int q_heads;                 /* a multiple of the cache's heads, at most 65535 */
     int dtype;                   /* of q and o: BF16 or F16, that of the cache where it keeps rows as they are */
-    float scale;
+    float scale;                 /* a number, and times log2(e) in binary32 too */
     int reserved;                /* 0                                          */
 } convrot_attention_paged_args;
 /* Bytes of the workspace (16-byte aligned; 0: NULL will do). */
@@ -527,7 +527,7 @@ typedef struct {
     int head_dim;                /* 8 .. 256, a multiple of 8                  */
     int causal;                  /* 0 or 1                                     */
     int dtype;                   /* BF16 or F16                                */
-    float scale;
+    float scale;                 /* a number, and times log2(e) in binary32 too */
 } convrot_attention_args;
 int convrot_attention_workspace_bytes(const convrot_attention_args* args_host, size_t* bytes_host);
 int convrot_attention(const convrot_attention_args* args_host, void* workspace_dev, size_t ws_bytes, void* stream);

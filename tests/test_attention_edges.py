@@ -4,6 +4,7 @@ u = 2^-24 is half a step of binary32 relative to the value; a softmax weight and
 output are each rounded to the heads' type (half a step, finfo.eps / 2 of it).  Weights
 in f16 are 2^11 where the largest is 1, so the half step of its subnormals, 2^-25, is
 2^-36 of that one."""
+import ctypes
 import math
 
 import pytest
@@ -12,7 +13,7 @@ import torch
 from w4a4_rotated_bit_amd import binding as B
 
 from .test_attention import new_cache
-from .test_block_ops import TYPES, U, close, half_step, rand
+from .test_block_ops import TYPES, U, close, half_step, packed, rand
 
 FLAT = {torch.float16: 2.0 ** -36, torch.bfloat16: 0.0}   # half a step of the smallest weights
 
@@ -154,3 +155,46 @@ def test_scores_one_step_of_binary32_apart(gpu, dtype, base):
         bound = bound + half_step(dt, want.abs() + bound)
         for call in (prompt, paged):
             close(call(q, k, v, scale)[0], want, bound, f"{call.__name__} {ramp[:2].tolist()}")
+
+
+# ---- refusals ------------------------------------------------------------------------
+
+P = 1 << 32
+BF16_CACHE = dict(k_rows=P, k_scales=0, k_page=1 << 14, k_head=1 << 12, k_token=256, k_spage=0, k_shead=0, k_stoken=0,
+                  v_rows=P + (2 << 20), v_scales=0, v_page=1 << 14, v_head=1 << 12, v_token=256, v_spage=0, v_shead=0, v_stoken=0,
+                  pages=100, page_size=16, heads=4, head_dim=128, kind=1)
+
+
+def paged_args(**kw):
+    return packed(B.PAGED_ARGS, dict(**BF16_CACHE, q=P + (16 << 20), o=P + (32 << 20), lse=P + (34 << 20), table=P + (36 << 20),
+                                     lengths=P + (40 << 20), batch=3, table_width=64, table_stride=64, q_batch_stride=1024, q_head_stride=128,
+                                     o_batch_stride=1024, o_head_stride=128, q_heads=8, dtype=1, scale=0.1, reserved=0), kw)
+
+
+def prompt_args(**kw):
+    return packed(B.ATTENTION_ARGS, dict(q=P, k=P + (16 << 20), v=P + (32 << 20), o=P + (48 << 20), lse=P + (56 << 20), q_starts=P + (60 << 20),
+                                         k_starts=P + (61 << 20), batch=2, q_tokens=40, k_tokens=4000, q_batch_stride=0, q_token_stride=512,
+                                         q_head_stride=64, k_batch_stride=0, k_token_stride=256, k_head_stride=64, v_batch_stride=0,
+                                         v_token_stride=256, v_head_stride=64, o_batch_stride=0, o_token_stride=512, o_head_stride=64,
+                                         q_heads=8, k_heads=4, head_dim=64, causal=1, dtype=1, scale=0.1), kw)
+
+
+CALLS = [("convrot_attention_paged", paged_args), ("convrot_attention", prompt_args)]
+
+
+def workspace_bytes(lib, name, args):
+    need = ctypes.c_size_t(0)
+    assert getattr(lib, name + "_workspace_bytes")(args, ctypes.byref(need)) == B.CONVROT_OK
+    return need.value
+
+
+@pytest.mark.parametrize("name,args", CALLS)
+@pytest.mark.parametrize("scale,ok", [(2.3e38, True), (-2.3e38, True), (2.4e38, False), (-2.4e38, False), (3.4e38, False), (1e-45, True)])
+def test_scales_that_overflow_in_base_2_are_refused(name, args, scale, ok):
+    """Scores are computed times scale log2(e), which has to be a number of binary32 too."""
+    lib = B.load()
+    n = workspace_bytes(lib, name, args())
+    a = args(scale=scale)
+    assert getattr(lib, "convrot_validate_" + name[8:])(a, P + (128 << 20), n) == (B.CONVROT_OK if ok else B.CONVROT_EINVAL)
+    if not ok:
+        assert getattr(lib, name)(a, P + (128 << 20), n, None) == B.CONVROT_EINVAL

@@ -102,7 +102,7 @@ int check_paged(const convrot_attention_paged_args* args, bool* empty)
     *empty = false;
     if (!args) return CONVROT_EINVAL;
     const convrot_attention_paged_args& a = *args;
-    if (!half_type(a.dtype) || a.reserved || !isfinite(a.scale)) return CONVROT_EINVAL;
+    if (!half_type(a.dtype) || a.reserved || !isfinite(a.scale * kLog2e)) return CONVROT_EINVAL;
     if (!known_cache(a.cache) || (!cache_quantized(a.cache.kind) && a.cache.kind != a.dtype)) return CONVROT_EINVAL;
     if (!within(a.batch, 0, kMaxBatch) || !within(a.q_heads, 1, kMaxHeads) || a.q_heads % a.cache.heads) return CONVROT_EINVAL;
     if (!within(a.table_width, 0, kMaxPlaces / a.cache.page_size) || !reaches(a.batch, a.table_stride)) return CONVROT_EINVAL;
@@ -139,7 +139,7 @@ int check_prompt(const convrot_attention_args* args, bool* empty)
     *empty = false;
     if (!args) return CONVROT_EINVAL;
     const convrot_attention_args& a = *args;
-    if (!half_type(a.dtype) || !within(a.causal, 0, 1) || !isfinite(a.scale)) return CONVROT_EINVAL;
+    if (!half_type(a.dtype) || !within(a.causal, 0, 1) || !isfinite(a.scale * kLog2e)) return CONVROT_EINVAL;
     if (!within(a.batch, 0, kMaxBatch) || !within(a.q_tokens, 0, kMaxRows) || !within(a.k_tokens, 0, kMaxRows)) return CONVROT_EINVAL;
     if (!within(a.q_heads, 1, kMaxHeads) || !within(a.k_heads, 1, kMaxHeads) || a.q_heads % a.k_heads) return CONVROT_EINVAL;
     if (!within(a.head_dim, 8, kMaxHeadWidth) || a.head_dim % 8) return CONVROT_EINVAL;

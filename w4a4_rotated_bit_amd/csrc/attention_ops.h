@@ -18,6 +18,7 @@ constexpr int64_t kMaxTokenStride = ((int64_t)1 << 24) - 1;   // 64 rows stay wi
 constexpr int64_t kMaxCacheTokenStride = (int64_t)1 << 27;   // bytes: 16 rows stay within 32-bit offsets
 constexpr int64_t kMaxThreads = 0xffffffff;   // of one launch
 constexpr int kBlock = 32;                  // channels that share a scale
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 inline bool cache_quantized(int kind) { return kind == CONVROT_CACHE_E4M3 || kind == CONVROT_CACHE_E2M1; }
 // bytes of a row of `dim` values
@@ -140,7 +141,6 @@ typedef uint32_t U4 __attribute__((ext_vector_type(4)));
 typedef uint32_t U2 __attribute__((ext_vector_type(2)));
 
 constexpr float kInf = __builtin_inff();
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
