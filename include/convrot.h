@@ -424,7 +424,8 @@ int convrot_validate_quantize_weight_grouped(const void* W_dev, int64_t N, int64
  * multiplies v, to half a step of each in bf16; in f16 to half a step of those that are 2^-25 of a
  * query's largest one or more, and to 2^-36 of that one below.  lse (natural logarithm of sum_j p[h][j]) is optional.
  * Kernels are launched on the caller's stream and keep no state; a workspace
- * is written and read within one call, and holds nothing between calls.
+ * is written and read within one call, holds nothing between calls, and is apart
+ * from every tensor of its call.
  */
 #define CONVROT_I64 5
 /* How a cache keeps its rows: as they are (BF16, F16), or in blocks of 32

@@ -198,3 +198,32 @@ def test_scales_that_overflow_in_base_2_are_refused(name, args, scale, ok):
     assert getattr(lib, "convrot_validate_" + name[8:])(a, P + (128 << 20), n) == (B.CONVROT_OK if ok else B.CONVROT_EINVAL)
     if not ok:
         assert getattr(lib, name)(a, P + (128 << 20), n, None) == B.CONVROT_EINVAL
+
+
+@pytest.mark.parametrize("name,args", CALLS)
+def test_workspaces_that_meet_a_tensor_are_refused(name, args):
+    """A workspace is written while inputs are read, and read while outputs are written."""
+    lib = B.load()
+    a = args()
+    n = workspace_bytes(lib, name, a)
+    assert n
+    check = getattr(lib, "convrot_validate_" + name[8:])
+    if name == "convrot_attention_paged":
+        tensors = [(P, 99 * (1 << 14) + 4 * (1 << 12)), (P + (2 << 20), 99 * (1 << 14) + 4 * (1 << 12)), (P + (16 << 20), 2 * 3 * 1024),
+                   (P + (32 << 20), 2 * 3 * 1024), (P + (34 << 20), 4 * 3 * 8), (P + (36 << 20), 4 * 3 * 64), (P + (40 << 20), 4 * 3)]
+    else:
+        tensors = [(P, 2 * 40 * 512), (P + (16 << 20), 2 * 4000 * 256), (P + (32 << 20), 2 * 4000 * 256), (P + (48 << 20), 2 * 40 * 512),
+                   (P + (56 << 20), 4 * 40 * 8), (P + (60 << 20), 4 * 3), (P + (61 << 20), 4 * 3)]
+    far = P + (128 << 20)
+    for i, (at, size) in enumerate(tensors):
+        last = (at + size - 1) // 16 * 16        # the first byte of the workspace in the last of the tensor's
+        for space in (at, last, (at - n) // 16 * 16 + 16):
+            assert check(a, space, n) == B.CONVROT_EINVAL, (i, space)
+            assert getattr(lib, name)(a, space, n, None) == B.CONVROT_EINVAL
+    assert check(a, far, n) == B.CONVROT_OK
+    # right behind the output, and right before the last tensor: 591360 and 1597440 bytes lie between neighbours; what
+    # is longer than it needs to be may reach into it
+    at, size = tensors[3]
+    assert check(a, -(-(at + size) // 16) * 16, n) == B.CONVROT_OK
+    end = tensors[-1][0] - -(-n // 16) * 16
+    assert check(a, end, n) == check(a, end, n + 4096) == B.CONVROT_OK

@@ -96,6 +96,28 @@ int check_cache_call(const convrot_cache_args* args, bool write)
     return CONVROT_OK;
 }
 
+struct PagedBlocks {
+    Block q, o, lse, lengths, table;
+    explicit PagedBlocks(const convrot_attention_paged_args& a)
+        : q(heads(a, a.q_dev, a.q_batch_stride, a.q_head_stride)), o(heads(a, a.o_dev, a.o_batch_stride, a.o_head_stride)),
+          lse(a.lse_dev, a.batch * a.q_heads, 4), lengths(a.lengths_dev, a.batch, 4), table(a.page_table_dev, a.table_width, 4)
+    {
+        table.add(a.batch, a.table_stride, 4);
+    }
+    static Block heads(const convrot_attention_paged_args& a, const void* at, int64_t batch, int64_t head)
+    {
+        Block b(at, a.cache.head_dim, 2);
+        b.add(a.batch, batch, 2);
+        b.add(a.q_heads, head, 2);
+        return b;
+    }
+    // Whether `out` is apart from everything that the call reads.
+    bool apart_from_inputs(const convrot_kv_cache& cache, const Block& out) const
+    {
+        return apart(q, out) && apart(lengths, out) && (!table.at || apart(table, out)) && apart_from(cache, out);
+    }
+};
+
 // Everything but the workspace; *empty: nothing to do.
 int check_paged(const convrot_attention_paged_args* args, bool* empty)
 {
@@ -116,23 +138,40 @@ int check_paged(const convrot_attention_paged_args* args, bool* empty)
     if (!a.q_dev || !a.o_dev || !a.lengths_dev || (a.table_width && !a.page_table_dev)) return CONVROT_EINVAL;
     if (!aligned(a.q_dev, 2) || !aligned(a.o_dev, 2) || !aligned(a.lse_dev, 4)) return CONVROT_EINVAL;
     if (!aligned(a.lengths_dev, 4) || !aligned(a.page_table_dev, 4)) return CONVROT_EINVAL;
-    const auto heads = [&](const void* at, int64_t batch, int64_t head) {
-        Block b(at, a.cache.head_dim, 2);
-        b.add(a.batch, batch, 2);
-        b.add(a.q_heads, head, 2);
-        return b;
-    };
-    const Block q = heads(a.q_dev, a.q_batch_stride, a.q_head_stride), o = heads(a.o_dev, a.o_batch_stride, a.o_head_stride);
-    const Block lse(a.lse_dev, a.batch * a.q_heads, 4), lengths(a.lengths_dev, a.batch, 4);
-    Block table(a.page_table_dev, a.table_width, 4);
-    table.add(a.batch, a.table_stride, 4);
-    if (!o.injective()) return CONVROT_EINVAL;
-    for (const Block* out : {&o, &lse}) {
-        if (!out->at) continue;
-        if (!apart(q, *out) || !apart(lengths, *out) || (table.at && !apart(table, *out)) || !apart_from(a.cache, *out)) return CONVROT_EINVAL;
-    }
-    return !lse.at || apart(o, lse) ? CONVROT_OK : CONVROT_EINVAL;
+    const PagedBlocks b(a);
+    if (!b.o.injective()) return CONVROT_EINVAL;
+    for (const Block* out : {&b.o, &b.lse})
+        if (out->at && !b.apart_from_inputs(a.cache, *out)) return CONVROT_EINVAL;
+    return !b.lse.at || apart(b.o, b.lse) ? CONVROT_OK : CONVROT_EINVAL;
 }
+
+struct PromptBlocks {
+    Block q, k, v, o, lse, q_starts, k_starts;
+    explicit PromptBlocks(const convrot_attention_args& a)
+        : q(rows(a, a.q_dev, a.q_tokens, a.q_heads, a.q_batch_stride, a.q_token_stride, a.q_head_stride)),
+          k(rows(a, a.k_dev, a.k_tokens, a.k_heads, a.k_batch_stride, a.k_token_stride, a.k_head_stride)),
+          v(rows(a, a.v_dev, a.k_tokens, a.k_heads, a.v_batch_stride, a.v_token_stride, a.v_head_stride)),
+          o(rows(a, a.o_dev, a.q_tokens, a.q_heads, a.o_batch_stride, a.o_token_stride, a.o_head_stride)),
+          lse(a.lse_dev, entries(a) * a.q_tokens * a.q_heads, 4), q_starts(a.q_starts_dev, a.batch + 1, 4),
+          k_starts(a.k_starts_dev, a.batch + 1, 4)
+    {
+    }
+    static int64_t entries(const convrot_attention_args& a) { return a.q_starts_dev ? 1 : a.batch; }
+    static Block rows(const convrot_attention_args& a, const void* at, int64_t tokens, int heads, int64_t batch_s, int64_t token_s, int64_t head_s)
+    {
+        Block b(at, a.head_dim, 2);
+        b.add(entries(a), batch_s, 2);
+        b.add(tokens, token_s, 2);
+        b.add(heads, head_s, 2);
+        return b;
+    }
+    // Whether `out` is apart from everything that the call reads.
+    bool apart_from_inputs(const convrot_attention_args& a, const Block& out) const
+    {
+        if (!apart(q, out) || (a.k_tokens && (!apart(k, out) || !apart(v, out)))) return false;
+        return !q_starts.at || (apart(q_starts, out) && apart(k_starts, out));
+    }
+};
 
 int check_prompt(const convrot_attention_args* args, bool* empty)
 {
@@ -145,7 +184,7 @@ int check_prompt(const convrot_attention_args* args, bool* empty)
     if (!within(a.head_dim, 8, kMaxHeadWidth) || a.head_dim % 8) return CONVROT_EINVAL;
     const bool packed = a.q_starts_dev != nullptr;
     if (packed != (a.k_starts_dev != nullptr)) return CONVROT_EINVAL;
-    const int64_t entries = packed ? 1 : a.batch;
+    const int64_t entries = PromptBlocks::entries(a);
     for (int64_t s : {a.q_batch_stride, a.k_batch_stride, a.v_batch_stride, a.o_batch_stride})
         if (!reaches(entries, s)) return CONVROT_EINVAL;
     for (int64_t s : {a.q_token_stride, a.o_token_stride})
@@ -166,34 +205,17 @@ int check_prompt(const convrot_attention_args* args, bool* empty)
     for (const void* p : {a.q_dev, a.k_dev, a.v_dev, (const void*)a.o_dev})
         if (!aligned(p, 2)) return CONVROT_EINVAL;
     if (!aligned(a.lse_dev, 4) || !aligned(a.q_starts_dev, 4) || !aligned(a.k_starts_dev, 4)) return CONVROT_EINVAL;
-    const auto block = [&](const void* at, int64_t tokens, int heads, int64_t batch_s, int64_t token_s, int64_t head_s) {
-        Block b(at, a.head_dim, 2);
-        b.add(entries, batch_s, 2);
-        b.add(tokens, token_s, 2);
-        b.add(heads, head_s, 2);
-        return b;
-    };
-    const Block q = block(a.q_dev, a.q_tokens, a.q_heads, a.q_batch_stride, a.q_token_stride, a.q_head_stride);
-    const Block k = block(a.k_dev, a.k_tokens, a.k_heads, a.k_batch_stride, a.k_token_stride, a.k_head_stride);
-    const Block v = block(a.v_dev, a.k_tokens, a.k_heads, a.v_batch_stride, a.v_token_stride, a.v_head_stride);
-    const Block o = block(a.o_dev, a.q_tokens, a.q_heads, a.o_batch_stride, a.o_token_stride, a.o_head_stride);
-    const Block lse(a.lse_dev, entries * a.q_tokens * a.q_heads, 4);
-    const Block starts[2] = {Block(a.q_starts_dev, a.batch + 1, 4), Block(a.k_starts_dev, a.batch + 1, 4)};
-    if (!o.injective()) return CONVROT_EINVAL;
-    for (const Block* out : {&o, &lse}) {
-        if (!out->at) continue;
-        if (!apart(q, *out)) return CONVROT_EINVAL;
-        if (a.k_tokens && (!apart(k, *out) || !apart(v, *out))) return CONVROT_EINVAL;
-        for (const Block& s : starts)
-            if (s.at && !apart(s, *out)) return CONVROT_EINVAL;
-    }
-    return !lse.at || apart(o, lse) ? CONVROT_OK : CONVROT_EINVAL;
+    const PromptBlocks b(a);
+    if (!b.o.injective()) return CONVROT_EINVAL;
+    for (const Block* out : {&b.o, &b.lse})
+        if (out->at && !b.apart_from_inputs(a, *out)) return CONVROT_EINVAL;
+    return !b.lse.at || apart(b.o, b.lse) ? CONVROT_OK : CONVROT_EINVAL;
 }
 
+// need > 0
 int check_workspace(const void* workspace, size_t have, int64_t need)
 {
-    if (need == 0) return CONVROT_OK;
-    if (!workspace || (int64_t)have < need) return CONVROT_EWORKSPACE;
+    if (!workspace || have < (size_t)need) return CONVROT_EWORKSPACE;
     return aligned(workspace, 16) ? CONVROT_OK : CONVROT_EINVAL;
 }
 
@@ -216,8 +238,12 @@ int convrot_attention_paged_workspace_bytes(const convrot_attention_paged_args* 
 int convrot_validate_attention_paged(const convrot_attention_paged_args* args, const void* workspace, size_t ws_bytes)
 {
     bool empty;
-    const int rc = check_paged(args, &empty);
-    return rc || empty ? rc : check_workspace(workspace, ws_bytes, paged_plan(*args).bytes());
+    int rc = check_paged(args, &empty);
+    const int64_t need = rc || empty ? 0 : paged_plan(*args).bytes();
+    if (need == 0 || (rc = check_workspace(workspace, ws_bytes, need))) return rc;
+    const PagedBlocks b(*args);
+    const Block space(workspace, need, 1);
+    return b.apart_from_inputs(args->cache, space) && apart(b.o, space) && (!b.lse.at || apart(b.lse, space)) ? CONVROT_OK : CONVROT_EINVAL;
 }
 
 int convrot_attention_workspace_bytes(const convrot_attention_args* args, size_t* bytes)
@@ -232,8 +258,12 @@ int convrot_attention_workspace_bytes(const convrot_attention_args* args, size_t
 int convrot_validate_attention(const convrot_attention_args* args, const void* workspace, size_t ws_bytes)
 {
     bool empty;
-    const int rc = check_prompt(args, &empty);
-    return rc || empty ? rc : check_workspace(workspace, ws_bytes, prompt_plan(*args).bytes(args->head_dim));
+    int rc = check_prompt(args, &empty);
+    const int64_t need = rc || empty ? 0 : prompt_plan(*args).bytes(args->head_dim);
+    if (need == 0 || (rc = check_workspace(workspace, ws_bytes, need))) return rc;
+    const PromptBlocks b(*args);
+    const Block space(workspace, need, 1);
+    return b.apart_from_inputs(*args, space) && apart(b.o, space) && (!b.lse.at || apart(b.lse, space)) ? CONVROT_OK : CONVROT_EINVAL;
 }
 
 }  // extern "C"
