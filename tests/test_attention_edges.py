@@ -227,3 +227,71 @@ def test_workspaces_that_meet_a_tensor_are_refused(name, args):
     assert check(a, -(-(at + size) // 16) * 16, n) == B.CONVROT_OK
     end = tensors[-1][0] - -(-n // 16) * 16
     assert check(a, end, n) == check(a, end, n + 4096) == B.CONVROT_OK
+
+
+# ---- the binding's checks, on host tensors -----------------------------------------------
+
+
+@pytest.fixture
+def host_calls(monkeypatch):
+    """The binding on host tensors: its checks run, the C call is recorded instead of made."""
+    B._use_torch()
+    calls = []
+    monkeypatch.setattr(B, "_on_gpu", lambda t, name: -1)
+    monkeypatch.setattr(B, "_check_tensor", lambda t, name, device: None)
+    monkeypatch.setattr(B, "_launch", lambda device, stream, call, tensors: call(0))
+    monkeypatch.setattr(B, "_call", lambda name, *args: calls.append(name))
+    monkeypatch.setattr(B, "_call_with_workspace", lambda name, *args: calls.append(name))
+    return calls
+
+
+def uses_of(cache, dtype=torch.bfloat16):
+    """The three calls that take a cache of two heads of 64 channels."""
+    x, slots = torch.zeros((2, 2, 64), dtype=dtype), torch.arange(2)
+    return [lambda: B.convrot_cache_write(x, x, slots, cache), lambda: B.convrot_cache_read(cache, slots, dtype=dtype),
+            lambda: B.convrot_attention_paged(x, cache, slots.int()[:, None], slots.int())]
+
+
+@pytest.mark.parametrize("kind", ["e2m1", "same"])
+@pytest.mark.parametrize("more", [-1, 1])
+def test_memory_resized_in_its_place_is_refused(host_calls, kind, more):
+    """A storage that got another size at the address that it had: an allocator may give the same
+    place out again, and the rest of it to others."""
+    class Storage:
+        def __init__(self, of, more):
+            self.at, self.size = of.data_ptr(), of.nbytes() + more
+
+        def data_ptr(self):
+            return self.at
+
+        def nbytes(self):
+            return self.size
+
+    for i in range(4 if kind == "e2m1" else 2):
+        cache = B.new_kv_cache(4, 8, 2, 64, "e2m1" if kind == "e2m1" else torch.bfloat16, device="cpu")
+        for use in uses_of(cache):
+            use()
+        made = len(host_calls)
+        memory = list(cache._memory)
+        memory[i] = Storage(memory[i], more)
+        cache._memory = tuple(memory)
+        for use in uses_of(cache):
+            with pytest.raises(ValueError, match="resized"):
+                use()
+        assert len(host_calls) == made == 3 * (i + 1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["e2m1", "same"])
+def test_smaller_memory_of_a_cache_is_refused(gpu, kind):
+    x, slots = rand((2, 2, 64), 1, torch.bfloat16).cuda(), torch.arange(2, device="cuda")
+    for i in range(4 if kind == "e2m1" else 2):
+        cache = new_cache(64, 64, 2, 64, kind, "bf16", seed=1)
+        storage = tuple(cache)[i].untyped_storage()
+        size = storage.nbytes()
+        for n in (0, size // 2):
+            storage.resize_(n)
+            for call in (lambda: B.convrot_cache_write(x, x, slots, cache), lambda: B.convrot_cache_read(cache, slots),
+                         lambda: B.convrot_attention_paged(x, cache, slots.int()[:, None], slots.int())):
+                with pytest.raises(ValueError, match="resized"):
+                    call()

@@ -1019,7 +1019,7 @@ class KVCache:
             ks, vs = k_scales.data_ptr(), v_scales.data_ptr()
             self.kept = None
             self._memory = k.untyped_storage(), v.untyped_storage(), k_scales.untyped_storage(), v_scales.untyped_storage()
-        self._at = [m.data_ptr() for m in self._memory]
+        self._at = [(m.data_ptr(), m.nbytes()) for m in self._memory]
         self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
         self.heads, self.head_dim, self.device = heads, dim, device
         self._fields = CACHE_FIELDS.pack(
@@ -1062,7 +1062,7 @@ def _check_cache(cache, device, dtype, what):
         raise TypeError("cache must be a KVCache")
     if cache.device != device:
         raise ValueError(f"the cache is on cuda:{cache.device}, {what} on cuda:{device}")
-    if [m.data_ptr() for m in cache._memory] != cache._at:
+    if [(m.data_ptr(), m.nbytes()) for m in cache._memory] != cache._at:    # an allocator may give the same place again
         raise ValueError("the cache's memory was resized: it needs a new KVCache")
     kept = cache.kept
     if kept is not None:
