@@ -6,6 +6,8 @@ in f16 are 2^11 where the largest is 1, so the half step of its subnormals, 2^-2
 2^-36 of that one."""
 import ctypes
 import math
+from contextlib import nullcontext
+from types import SimpleNamespace
 
 import pytest
 import torch
@@ -295,3 +297,68 @@ def test_smaller_memory_of_a_cache_is_refused(gpu, kind):
                          lambda: B.convrot_attention_paged(x, cache, slots.int()[:, None], slots.int())):
                 with pytest.raises(ValueError, match="resized"):
                     call()
+
+
+@pytest.mark.parametrize("kind", ["e2m1", "same"])
+@pytest.mark.parametrize("swapped", [False, True])
+def test_memory_of_a_call_on_another_stream_is_recorded_there(monkeypatch, kind, swapped):
+    """What the kernels read and write is kept until the stream is done: the memory that a cache's
+    handle was made of, also where one of its tensors was set to other memory since."""
+    B._use_torch()
+    monkeypatch.setattr(B, "_on_gpu", lambda t, name: 0)
+    monkeypatch.setattr(B, "_check_tensor", lambda t, name, device: None)
+    monkeypatch.setattr(B, "_call", lambda name, *args: None)
+    monkeypatch.setattr(B, "_call_with_workspace", lambda name, *args: None)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: nullcontext())
+    seen = []
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: seen.append((t.untyped_storage().data_ptr(), s)))
+    side = SimpleNamespace(device=SimpleNamespace(index=0), cuda_stream=7)
+    cache = B.new_kv_cache(4, 8, 2, 64, "e2m1" if kind == "e2m1" else torch.bfloat16, device="cpu")
+    held = [t.untyped_storage().data_ptr() for t in cache if t is not None]
+    if swapped:
+        cache.k.data = torch.empty_like(cache.k)
+    x, y, out = (torch.zeros((2, 2, 64), dtype=torch.bfloat16) for _ in range(3))
+    slots = torch.arange(2)
+    lse, table, lengths = torch.zeros((2, 2)), slots.int()[:, None].clone(), slots.int()
+    work, starts, ends = torch.zeros(16, dtype=torch.uint8), torch.tensor([0, 2], dtype=torch.int32), torch.tensor([0, 2], dtype=torch.int32)
+    z = torch.zeros_like(x)
+    for call, own in (
+            (lambda: B.convrot_cache_write(x, y, slots, cache, stream=side), (x, y, slots)),
+            (lambda: B.convrot_cache_read(cache, slots, k=x, v=y, stream=side), (slots, x, y)),
+            (lambda: B.convrot_attention_paged(x, cache, table, lengths, out=out, lse=lse, workspace=work, stream=side),
+             (x, table, lengths, out, lse, work)),
+            (lambda: B.convrot_attention(x, y, z, q_starts=starts, k_starts=ends, out=out, lse=lse, workspace=work, stream=side),
+             (x, y, z, starts, ends, out, lse, work))):
+        seen.clear()
+        call()
+        want = {t.untyped_storage().data_ptr() for t in own}
+        if len(own) < 8:
+            want |= set(held)
+        assert {at for at, _ in seen} == want and all(s is side for _, s in seen)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["e2m1", "same"])
+@pytest.mark.parametrize("swapped", [False, True])
+def test_caches_freed_while_another_stream_reads_them(gpu, kind, swapped):
+    """The last reference to a cache goes while a stream of its own is still to read it; what is
+    allocated next is written at once."""
+    side = torch.cuda.Stream()
+    slots = torch.arange(2048, device="cuda")
+    gate = rand((4096, 4096), 3).cuda()
+    for _ in range(3):
+        cache = new_cache(32, 64, 8, 128, kind, "bf16", seed=1)
+        want = B.convrot_cache_read(cache, slots)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                gate @ gate         # the read waits behind these
+        if swapped:
+            cache.k.data, cache.v.data = (torch.zeros_like(t) for t in (cache.k, cache.v))
+        got = B.convrot_cache_read(cache, slots, stream=side)
+        del cache
+        others = [torch.full((32, 8, 64, 128 if kind == "same" else 64), 77, dtype=torch.bfloat16 if kind == "same" else torch.uint8,
+                             device="cuda") for _ in range(6)]
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and all((t == 77).all() for t in others)

@@ -1033,6 +1033,12 @@ class KVCache:
         """Another cache with some of its tensors given."""
         return KVCache(**{"k": self.k, "v": self.v, "k_scales": self.k_scales, "v_scales": self.v_scales, **kw})
 
+    def record_stream(self, stream):
+        """Keeps the memory until ``stream`` is done with it, as a tensor's method does: that of
+        the handle, whatever its tensors were set to since."""
+        for m in self._memory:
+            _torch.empty(0, dtype=_torch.uint8, device=m.device).set_(m).record_stream(stream)
+
     def _written(self):
         kept = (self.k, self.v) if self.k_scales is None else (self.k, self.v, self.k_scales, self.v_scales)
         _torch.autograd.graph.increment_version(kept)
@@ -1131,7 +1137,7 @@ def convrot_cache_write(k, v, slots, cache: KVCache, stream=None) -> None:
             k.data_ptr(), v.data_ptr(), slots.data_ptr(), tokens, *k_strides, *v_strides, slots_code, code), raw)
         cache._written()
 
-    return _launch(device, stream, call, (k, v, slots, *cache))
+    return _launch(device, stream, call, (k, v, slots, cache))
 
 
 def convrot_cache_read(cache: KVCache, slots, dtype=None, k=None, v=None, stream=None):
@@ -1173,7 +1179,7 @@ def convrot_cache_read(cache: KVCache, slots, dtype=None, k=None, v=None, stream
             _written(k, v)
         return outs[0], outs[1]
 
-    return _launch(device, stream, call, (slots, k, v, *cache))
+    return _launch(device, stream, call, (slots, k, v, cache))
 
 
 def _call_with_workspace(name, args, workspace, device, raw):
@@ -1263,7 +1269,7 @@ def convrot_attention_paged(q, cache: KVCache, page_table, lengths, *, scale=Non
             _written(out, lse)
         return o if sums is None else (o, sums)
 
-    return _launch(device, stream, call, (q, page_table, lengths, out, lse, workspace, *cache))
+    return _launch(device, stream, call, (q, page_table, lengths, out, lse, workspace, cache))
 
 
 def convrot_attention(q, k, v, *, q_starts=None, k_starts=None, causal: bool = False, scale=None, out=None, lse=None,
