@@ -362,3 +362,17 @@ def test_caches_freed_while_another_stream_reads_them(gpu, kind, swapped):
                              device="cuda") for _ in range(6)]
         torch.cuda.synchronize()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and all((t == 77).all() for t in others)
+
+
+def test_empty_heads_are_refused(host_calls):
+    """No heads and heads of no channels reach the library's own check."""
+    none, x, n = torch.zeros((1, 2, 2, 0), dtype=torch.bfloat16), torch.zeros((2, 2, 64), dtype=torch.bfloat16), torch.ones(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="heads"):
+        B.convrot_attention_paged(x, B.KVCache(*(torch.zeros((4, 0, 8, 64), dtype=torch.bfloat16) for _ in range(2))), n[:, None], n)
+    assert not host_calls
+    B.convrot_attention_paged(x[..., :0], B.KVCache(*(torch.zeros((4, 2, 8, 0), dtype=torch.bfloat16) for _ in range(2))), n[:, None], n)
+    B.convrot_attention(none, none, none)
+    assert host_calls == ["convrot_attention_paged", "convrot_attention"]
+    lib = B.load()
+    for name, args in CALLS:
+        assert getattr(lib, name)(args(head_dim=0), P + (128 << 20), 1 << 30, None) == B.CONVROT_EINVAL

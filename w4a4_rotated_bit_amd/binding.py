@@ -1246,12 +1246,12 @@ def convrot_attention_paged(q, cache: KVCache, page_table, lengths, *, scale=Non
     heads, dim = cache.heads, cache.head_dim
     if len(shape) != 3 or shape[2] != dim or (dim > 1 and q.stride(2) != 1):
         raise ValueError(f"q must be [batch, q_heads, {dim}] and dense in its last dimension, got {tuple(shape)}")
-    if shape[1] % heads:
+    if heads == 0 or shape[1] % heads:
         raise ValueError(f"{shape[1]} query heads do not share {heads} key heads evenly")
     table_ptr, lengths_ptr = _table(page_table, "page_table", 2, device), _table(lengths, "lengths", 1, device)
     if page_table.shape[0] != shape[0] or lengths.shape[0] != shape[0]:
         raise ValueError(f"page_table and lengths must have one row for each of the {shape[0]} sequences")
-    scale = dim ** -0.5 if scale is None else float(scale)
+    scale = max(dim, 1) ** -0.5 if scale is None else float(scale)
 
     def call(raw):
         o = _output(out, q, True, "out", shape, dtype, device)
@@ -1322,7 +1322,7 @@ def convrot_attention(q, k, v, *, q_starts=None, k_starts=None, causal: bool = F
     k_tokens, k_heads, _ = k.shape[-3:]
     if k_heads == 0 or heads % k_heads:
         raise ValueError(f"{heads} query heads do not share {k_heads} key heads evenly")
-    scale = dim ** -0.5 if scale is None else float(scale)
+    scale = max(dim, 1) ** -0.5 if scale is None else float(scale)
 
     def steps(t, name):
         s = t.stride()
