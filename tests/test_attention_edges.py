@@ -376,3 +376,68 @@ def test_empty_heads_are_refused(host_calls):
     lib = B.load()
     for name, args in CALLS:
         assert getattr(lib, name)(args(head_dim=0), P + (128 << 20), 1 << 30, None) == B.CONVROT_EINVAL
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "same"])
+@pytest.mark.parametrize("which", [0, 1])
+def test_caches_that_ask_for_a_gradient_are_refused(host_calls, monkeypatch, kind, which):
+    """8-bit floating point rows can ask for one as 16-bit rows can."""
+    def check(t, name, device):
+        if t.requires_grad and torch.is_grad_enabled():
+            raise RuntimeError(f"{name} requires a gradient")
+
+    monkeypatch.setattr(B, "_check_tensor", check)
+    cache = B.new_kv_cache(4, 8, 2, 64, "e4m3" if kind == "e4m3" else torch.bfloat16, device="cpu")
+    (cache.k, cache.v)[which].requires_grad_()
+    for use in uses_of(cache):
+        with pytest.raises(RuntimeError, match="gradient"):
+            use()
+    assert not host_calls
+    with torch.no_grad():
+        for use in uses_of(cache)[1:]:
+            use()
+    assert len(host_calls) == 2
+
+
+def test_tangents_are_refused(host_calls):
+    """A tangent of forward differentiation would be lost as a gradient would be."""
+    import torch.autograd.forward_ad as fwd
+    cache = B.new_kv_cache(4, 8, 2, 64, torch.bfloat16, device="cpu")
+    x, slots, lse = torch.zeros((2, 2, 64), dtype=torch.bfloat16), torch.arange(2), torch.zeros((2, 2))
+    n = slots.int()
+    calls = [(lambda k, v, c: B.convrot_cache_write(k, v, slots, c), (x, x)),
+             (lambda k, v, c: B.convrot_cache_read(c, slots, k=k, v=v), (x, x)),
+             (lambda q, out, lse, c: B.convrot_attention_paged(q, c, n[:, None], n, out=out, lse=lse), (x, x.clone(), lse)),
+             (lambda q, k, v, out, lse, c: B.convrot_attention(q[None], k[None], v[None], out=out[None], lse=lse[None]),
+              (x, x, x, x.clone(), lse))]
+    for i, (call, args) in enumerate(calls):
+        with fwd.dual_level():
+            call(*args, cache)
+            made = len(host_calls)
+            for at in range(len(args)):
+                dual = fwd.make_dual(args[at].clone(), torch.ones_like(args[at]))
+                with pytest.raises(RuntimeError, match="tangent"):
+                    call(*args[:at], dual, *args[at + 1:], cache)
+            for name in ("k", "v") if i < 3 else ():
+                other = B.KVCache(cache.k, cache.v)
+                setattr(other, name, fwd.make_dual(getattr(cache, name).clone(), torch.ones_like(cache.k)))
+                with pytest.raises(RuntimeError, match="tangent"):
+                    call(*args, other)
+            assert len(host_calls) == made
+        call(*args, cache)
+
+
+def test_given_outputs_and_caches_count_as_written(host_calls):
+    """Autograd tells a saved tensor that was written since by its version."""
+    for kind in ("e2m1", "e4m3", torch.bfloat16):
+        cache = B.new_kv_cache(4, 8, 2, 64, kind, device="cpu")
+        x, slots, k, v, out, lse = (torch.zeros((2, 2, 64), dtype=torch.bfloat16), torch.arange(2), *(torch.zeros((2, 2, 64),
+                                    dtype=torch.bfloat16) for _ in range(3)), torch.zeros((2, 2)))
+        n = slots.int()
+        B.convrot_cache_write(x, x, slots, cache)
+        assert all(t is None or t._version == 1 for t in cache)
+        B.convrot_cache_read(cache, slots, k=k, v=v)
+        B.convrot_attention_paged(x, cache, n[:, None], n, out=out, lse=lse)
+        assert [t._version for t in (x, slots, k, v, out, lse)] == [0, 0, 1, 1, 1, 1] and all(t is None or t._version == 1 for t in cache)
+        B.convrot_attention(x[None], k[None], v[None], out=out[None], lse=lse[None])
+        assert [t._version for t in (x, k, v, out, lse)] == [0, 1, 1, 2, 2]

@@ -1071,12 +1071,11 @@ def _check_cache(cache, device, dtype, what):
     if [(m.data_ptr(), m.nbytes()) for m in cache._memory] != cache._at:    # an allocator may give the same place again
         raise ValueError("the cache's memory was resized: it needs a new KVCache")
     kept = cache.kept
-    if kept is not None:
-        if kept is not dtype:
-            raise TypeError(f"the cache keeps {kept} rows, {what} is {dtype}")
-        if cache.k.requires_grad or cache.v.requires_grad:
-            _check_tensor(cache.k, "cache.k", device)
-            _check_tensor(cache.v, "cache.v", device)
+    if kept is not None and kept is not dtype:
+        raise TypeError(f"the cache keeps {kept} rows, {what} is {dtype}")
+    if cache.k.requires_grad or cache.v.requires_grad:
+        _check_tensor(cache.k, "cache.k", device)
+        _check_tensor(cache.v, "cache.v", device)
 
 
 def _slots_code(slots, tokens, device):
