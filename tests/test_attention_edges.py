@@ -14,7 +14,7 @@ import torch
 
 from w4a4_rotated_bit_amd import binding as B
 
-from .test_attention import new_cache
+from .test_attention import check_prompt, new_cache
 from .test_block_ops import TYPES, U, close, half_step, packed, rand
 
 FLAT = {torch.float16: 2.0 ** -36, torch.bfloat16: 0.0}   # half a step of the smallest weights
@@ -441,3 +441,106 @@ def test_given_outputs_and_caches_count_as_written(host_calls):
         assert [t._version for t in (x, slots, k, v, out, lse)] == [0, 0, 1, 1, 1, 1] and all(t is None or t._version == 1 for t in cache)
         B.convrot_attention(x[None], k[None], v[None], out=out[None], lse=lse[None])
         assert [t._version for t in (x, k, v, out, lse)] == [0, 1, 1, 2, 2]
+
+
+# ---- prompts whose keys are shared, and joined -----------------------------------------------
+
+
+def parts_of(q_lens, k_lens, q_heads, k_heads, dim, packed_starts=True):
+    """How many workgroups share a tile's keys, from the workspace that a call asks for."""
+    lib, need = B.load(), ctypes.c_size_t(0)
+    batch, nq, nk = len(q_lens), sum(q_lens), sum(k_lens)
+    rows = nq * q_heads
+    if not packed_starts:
+        nq, nk = nq // batch, nk // batch
+    a = prompt_args(batch=batch, q_tokens=nq, k_tokens=nk, q_heads=q_heads, k_heads=k_heads, head_dim=dim, q_token_stride=q_heads * dim,
+                    q_head_stride=dim, o_token_stride=q_heads * dim, o_head_stride=dim, k_token_stride=k_heads * dim, k_head_stride=dim,
+                    v_token_stride=k_heads * dim, v_head_stride=dim, q=1 << 40, k=2 << 40, v=3 << 40, o=4 << 40, lse=5 << 40,
+                    **{} if packed_starts else dict(q_starts=0, k_starts=0, q_batch_stride=nq * q_heads * dim, o_batch_stride=nq * q_heads * dim,
+                                                    k_batch_stride=nk * k_heads * dim, v_batch_stride=nk * k_heads * dim))
+    assert lib.convrot_attention_workspace_bytes(a, ctypes.byref(need)) == B.CONVROT_OK
+    return need.value // (rows * (dim + 2) * 4) or 1
+
+
+SHARED = [   # queries and keys of each sequence, query heads, key heads, packed one behind the other, pad, place
+    ([40] * 2, [3000] * 2, 4, 2, False, 0, 0), ([40] * 3, [2000] * 3, 3, 3, False, 1, 0), ([130] * 2, [2500] * 2, 2, 1, False, 0, 3),
+    ([5, 33, 0], [6000, 300, 40], 6, 2, True, 0, 0), ([33, 0, 200], [2000, 2000, 199], 4, 1, True, 8, 0), ([3, 1], [4000, 5], 3, 1, True, 3, 5),
+    ([1] * 9, [30, 5000, 0, 64, 4000, 1, 300, 65, 900], 4, 2, True, 0, 1), ([1], [20000], 2, 1, True, 0, 0)]
+
+
+@pytest.mark.parametrize("dim", [8, 64, 256])
+@pytest.mark.parametrize("case", SHARED)
+def test_shared_keys_are_shared(case, dim):
+    q_lens, k_lens, hq, hk, packed_starts, _, _ = case
+    assert parts_of(q_lens, k_lens, hq, hk, dim, packed_starts) > 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim", [8, 40, 64, 96, 128, 136, 200, 256])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("case", SHARED)
+def test_prompts_of_shared_keys(gpu, case, dtype, dim):
+    q_lens, k_lens, hq, hk, packed_starts, pad, place = case
+    for causal in (False, True):
+        check_prompt(q_lens, k_lens, dtype, hq, hk, dim, causal, packed_starts, seed=dim + len(q_lens), pad=pad, place=place,
+                     behind=2 if packed_starts else 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim", [64, 200])
+def test_masked_places_of_shared_keys_stay_out(gpu, bad, dtype, dim):
+    """A value that is no number reaches the queries that see it and no other, in whichever part it lies."""
+    dt, nq, n = TYPES[dtype], 150, 3000
+    assert parts_of([nq], [n], 1, 1, dim) > 1
+    q, k, v = rand((nq, dim), 1, dt), rand((n, dim), 2, dt), rand((n, dim), 3, dt)
+    seen = torch.arange(n)[None] <= torch.arange(nq)[:, None] + n - nq
+    scale = dim ** -0.5
+    want, bound, want_lse, lse_bound = formula(q.double(), k.double(), v.double(), scale, dt, seen)
+    others = [c for c in range(dim) if c != 3]
+    for at in (n - 1, n - 2, n - 64, n - 130, n - 149, n - 150):
+        x = v.clone()
+        x[at, 3] = bad
+        out, lse = prompt(q, k, x, scale, causal=True)
+        sees = seen[:, at]
+        assert int(sees.sum()) == n - max(at, n - nq)
+        close(out[:, others], want[:, others], bound[:, others], f"key {at}")
+        close(out[~sees, 3], want[~sees, 3], bound[~sees, 3], f"key {at}, channel 3")
+        got = out[sees, 3].cpu().float()
+        assert got.isnan().all() if bad != bad else (got == bad).all()
+        close(lse, want_lse, lse_bound, "lse")
+        y = k.clone()
+        y[at, 3] = math.nan
+        out = prompt(q, y, v, scale, causal=True)[0]
+        close(out[~sees], want[~sees], bound[~sees], f"key {at} of NaN")
+        assert out[sees].isnan().all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_shared_keys_of_large_and_small_scores(gpu, dtype):
+    """Parts whose references are far apart, too large for whole numbers, or of keys that all count for nothing."""
+    dt, nq, n, dim = TYPES[dtype], 20, 4000, 64
+    q, k, v = torch.zeros((nq, dim), dtype=dt), torch.zeros((n, dim), dtype=dt), rand((n, dim), 3, dt)
+    q[:, 0] = 1
+    for column in ((torch.arange(n) // 500).float() * 3, 20 - (torch.arange(n) // 300).float() * 4, (torch.arange(n) % 2 - 1).float() * 300):
+        k[:, 0] = column.to(dt)
+        for causal in (False, True):
+            seen = torch.arange(n)[None] <= torch.arange(nq)[:, None] + n - nq if causal else None
+            want, bound, want_lse, lse_bound = formula(q.double(), k.double(), v.double(), 1.0, dt, seen)
+            out, lse = prompt(q, k, v, 1.0, causal=causal)
+            close(out, want, bound)
+            close(lse, want_lse, lse_bound)
+    k[:, 0] = -math.inf
+    k[1234, 0] = 1
+    out, lse = prompt(q, k, v, 1.0)
+    assert torch.equal(out.cpu(), v[1234].expand(nq, dim))
+    # a score of log2(e): half a step of it and of the scale (2 u), of its difference of 11 from an f16 reference (8 u),
+    # a step of the exponential and of the logarithm (4 u), and of the product with ln 2 (2 u)
+    close(lse, torch.ones(nq, dtype=torch.float64), torch.tensor(16 * U))
+    top = 2.0 ** 14
+    q[:, 0], k[:, 0] = top, -top
+    k[2000, 0] = top
+    out, lse = prompt(q, k, v, 1.0)     # 2^28 and -2^28
+    assert torch.equal(out.cpu(), v[2000].expand(nq, dim))
