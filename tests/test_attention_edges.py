@@ -14,7 +14,7 @@ import torch
 
 from w4a4_rotated_bit_amd import binding as B
 
-from .test_attention import check_prompt, new_cache
+from .test_attention import check_prompt, kept, new_cache, same
 from .test_block_ops import TYPES, U, close, half_step, packed, rand
 
 FLAT = {torch.float16: 2.0 ** -36, torch.bfloat16: 0.0}   # half a step of the smallest weights
@@ -544,3 +544,55 @@ def test_shared_keys_of_large_and_small_scores(gpu, dtype):
     k[2000, 0] = top
     out, lse = prompt(q, k, v, 1.0)     # 2^28 and -2^28
     assert torch.equal(out.cpu(), v[2000].expand(nq, dim))
+
+
+# ---- ends of the ranges -----------------------------------------------------------------------
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_cache_blocks_of_every_exponent(gpu, kind, dtype):
+    """Every exponent of the type as that of a block's largest value, the others up to 12 binades
+    below it; read in bf16, and in f16 where they were f16, the values are the format's own."""
+    dt, g = TYPES[dtype], torch.Generator().manual_seed(5)
+    exponents, bits = (255, 7) if dtype == "bf16" else (31, 10)
+    n = 32 if dtype == "bf16" else 256     # blocks of an exponent
+    e = torch.arange(exponents).repeat_interleave(n)[:, None] - torch.randint(0, 13, (exponents * n, 32), generator=g)
+    at = torch.randint(0, 32, (exponents * n, 1), generator=g)
+    e = e.scatter(1, at, torch.arange(exponents).repeat_interleave(n)[:, None]).clamp(min=0)
+    words = torch.randint(0, 2, e.shape, generator=g) << 15 | e << bits | torch.randint(0, 1 << bits, e.shape, generator=g)
+    x = (words - (words >> 15 << 16)).to(torch.int16).view(dt)
+    assert torch.isfinite(x.float()).all()
+    rows = x[:len(x) // 4 * 4].view(-1, 1, 128)
+    cache = B.new_kv_cache(-(-len(rows) // 64), 64, 1, 128, kind)
+    slots = torch.arange(len(rows), device="cuda")
+    B.convrot_cache_write(rows.cuda(), rows.flip(0).cuda(), slots, cache)
+    want, scales = kept(rows, kind)
+    assert torch.equal(cache.k_scales.cpu().view(-1, 4)[:len(rows)], scales.view(-1, 4))
+    for t in {torch.bfloat16, dt}:
+        k, v = B.convrot_cache_read(cache, slots, dtype=t)
+        same(k, want.to(t))
+        same(v, want.to(t).flip(0))
+        exact = want.to(t).double() == want
+        # beyond bf16's range only: 448 or 6 times the scale of the largest exponent
+        assert exact[want.abs() < 2.0 ** 127].all() and (t == torch.bfloat16 or exact.all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("place", [0, 1])      # copied straight to shared memory, and by way of registers
+def test_prompts_past_32_bit_offsets(gpu, place):
+    """Rows whose bytes lie past 32-bit offsets: queries, keys, values and outputs of a token 16 MB apart."""
+    n, heads, dim, step = 330, 2, 64, 1 << 23
+    memory = torch.empty(n * step + 1024, dtype=torch.bfloat16, device="cuda")
+    at = [torch.as_strided(memory, (n, heads, dim), (step, dim, 1), place + i * 128) for i in range(4)]
+    rows = [rand((n, heads, dim), 1 + i, torch.bfloat16) for i in range(3)]
+    for t, x in zip(at, rows):
+        t.copy_(x)
+    starts = torch.tensor([0, 130, n], dtype=torch.int32, device="cuda")
+    out = B.convrot_attention(*at[:3], q_starts=starts, causal=True, out=at[3])
+    for a, b in ((0, 130), (130, n)):
+        seen = torch.arange(b - a)[None] <= torch.arange(b - a)[:, None]
+        for h in range(heads):
+            want, bound, _, _ = formula(*(x[a:b, h].double() for x in rows), dim ** -0.5, torch.bfloat16, seen)
+            close(out[a:b, h], want, bound, f"rows from {a}, head {h}")
