@@ -463,7 +463,9 @@ typedef struct {
  * a write are distinct: what a place holds that two of them name is not
  * specified (every other place is right).  dtype: BF16 or F16, that of the cache
  * where it keeps rows as they are; rows of an e4m3 or e2m1 cache are read back
- * rounded to dtype (exact in BF16 but for magnitudes beyond its range). */
+ * rounded to dtype: exact in BF16 but for magnitudes beyond its range, and exact in F16
+ * where they were written from F16 rows; of others F16 loses bits below 2^-14 and makes
+ * infinities of what lies beyond 65504.  The attention reads them so, too. */
 typedef struct {
     convrot_kv_cache cache;
     void *k_dev, *v_dev;         /* [tokens][heads][head_dim]: read by a write, written by a read */

@@ -1141,8 +1141,9 @@ def convrot_cache_write(k, v, slots, cache: KVCache, stream=None) -> None:
 
 def convrot_cache_read(cache: KVCache, slots, dtype=None, k=None, v=None, stream=None):
     """(k, v) [tokens, heads, head_dim]: the rows at ``slots``, zeros for a slot outside
-    the cache.  dtype: bfloat16 (also the default of a quantized cache) or float16; a
-    cache that keeps rows as they are reads back its own.  k, v given are
+    the cache.  dtype: bfloat16 (also the default of a quantized cache) or float16, which
+    holds all of a quantized cache's values only where they were written from float16
+    rows; a cache that keeps rows as they are reads back its own.  k, v given are
     written.  ``stream``: as in ``convrot_residual_norm``."""
     if cache.__class__ is not KVCache:
         raise TypeError("cache must be a KVCache")
@@ -1225,7 +1226,8 @@ def convrot_attention_paged(q, cache: KVCache, page_table, lengths, *, scale=Non
     """softmax(scale q K^T) V for one new token of each sequence over a paged cache.
 
     q: bf16 or f16 [batch, q_heads, head_dim], any strides but a dense last one; q_heads a
-    multiple of the cache's heads, which they share in order.  page_table: int32
+    multiple of the cache's heads, which they share in order; f16 reads a quantized
+    cache's rows as ``convrot_cache_read`` does.  page_table: int32
     [batch, pages of a sequence]; lengths: int32 [batch], the keys of each sequence, its
     new one (written before) among them.  A length of 0 gives zeros; places of a page
     that is not in the cache are not seen.  scale: 1 / sqrt(head_dim) unless given.
@@ -1233,8 +1235,8 @@ def convrot_attention_paged(q, cache: KVCache, page_table, lengths, *, scale=Non
     float32 [batch, q_heads] the natural logarithm of the sum of exponentials.
     workspace: uint8, of ``convrot_attention_paged_workspace_bytes`` of the same
     call; allocated where none is given.  Calls that may run at the same time,
-    captured ones among them, need one each.  ``stream``: as in
-    ``convrot_residual_norm``."""
+    captured ones among them, need one each, apart from the call's other tensors.
+    ``stream``: as in ``convrot_residual_norm``."""
     device = _on_gpu(q, "q")
     _check_tensor(q, "q", device)
     if getattr(_forward, "_current_level", 0) >= 0:
@@ -1286,8 +1288,8 @@ def convrot_attention(q, k, v, *, q_starts=None, k_starts=None, causal: bool = F
     unless given.  Returns out of q's shape, with ``want_lse`` or a given lse (out, lse),
     lse float32 of q's shape without head_dim.  workspace: uint8, of
     ``convrot_attention_workspace_bytes`` of the same call; allocated where none is given.
-    Calls that may run at the same time, captured ones among them, need one each.
-    ``stream``: as in ``convrot_residual_norm``."""
+    Calls that may run at the same time, captured ones among them, need one each, apart
+    from the call's other tensors.  ``stream``: as in ``convrot_residual_norm``."""
     device = _on_gpu(q, "q")
     _check_tensor(q, "q", device)
     if getattr(_forward, "_current_level", 0) >= 0:

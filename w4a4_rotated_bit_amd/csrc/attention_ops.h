@@ -35,14 +35,16 @@ constexpr int kPagedTile = 32;     // keys of a wave's step
 constexpr int kPagedUnit = 128;    // keys that work is shared out by
 constexpr int kPagedWaves = 4;     // of a workgroup that has a share
 constexpr int kPagedWavesAlone = 8;     // of one that has a whole sequence
-// Most keys of such a sequence, by the width of the page table.  250 bf16 keys of 8 heads of
-// 128 take 6.8 us alone and 10.1 in shares that a second launch joins (128 such
-// sequences 34 and 37), 500 keys 10.6 and 10.3 (64 and 57).
+// Most keys of such a sequence, by the width of the page table: the lengths are known on
+// the GPU alone.  250 bf16 keys of 8 heads of 128 take 7.6 us alone and 10.2 in shares that
+// a second launch joins, as they do in a wider table (128 such sequences 32 and 37); 500
+// keys 10.6 alone and 10.8 (64 and 57).
 constexpr int64_t kPagedAlone = 384;
 // With as many sequences and columns the chip is full without shares, and tables may be
 // longer (and four waves a workgroup do, which work on longer parts): 256 sequences of 1 to
-// 2000 e2m1 keys of 8 heads 93 us and 138 in shares, 128 of 1000 bf16 keys 98 and 101; where one
-// of 2000 keys stands among 255 of 100, 42 and 35.
+// 2000 e2m1 keys of 8 heads 106 us and 140 in shares, 128 of 1000 bf16 keys 92 and 99, 4096
+// of 512 e2m1 keys of 2 heads 208 and 326; where one of 2000 keys stands among 255 of 100,
+// 42 and 34.
 constexpr int64_t kPagedMany = 1024;
 constexpr int64_t kPagedAloneMany = 2048;
 constexpr int kPagedShares = 512;  // most workgroups that share the units: two on each compute unit
@@ -96,12 +98,16 @@ inline PromptPlan prompt_plan(const convrot_attention_args& a)
     // packed: sum of ceil(len / 128) over the sequences, for any lengths
     p.tiles = packed ? (a.q_tokens + (kPromptRows - 1) * std::min(a.batch, a.q_tokens)) / kPromptRows
                      : a.batch * ((a.q_tokens + kPromptRows - 1) / kPromptRows);
-    // Few queries against many keys: the keys of a tile go to several workgroups, 256 keys
-    // each at least, as many as fill the chip (two on each compute unit) and as it pays:
-    // a step of 64 keys takes 1.4 us, or 2 us where two workgroups share a unit, a second
-    // launch 6 us, and partial results are written and read at some 4 TB/s.  (233 queries of
-    // 9 heads of 72 against 13243 keys: 27 us in 19 parts, 240 us in one; 1024 causal
-    // queries of 32 heads of 128: 41 us in two parts, 24 us in one.)
+    // Few queries against many keys: the keys of a tile go to several workgroups, as many as
+    // fill the chip (two on each compute unit) and as it pays: a step of 64 keys takes 1.4 us,
+    // or 2 us where two workgroups share a unit (measured with heads of 128, taken for all),
+    // a second launch 6 us, and partial results are written and read at some 4 TB/s.  (233
+    // queries of 9 heads of 72 against 13243 keys: 27 us in 19 parts, 240 us in one; 1024
+    // causal queries of 32 heads of 128: 41 us in two parts, 24 us in one.)  A tile's steps
+    // are counted without a mask, and of packed sequences, whose lengths are known on the GPU
+    // alone, by their mean, 256 keys a part at least: where one is far longer than the others
+    // it gets too few parts (one query each for 64 sequences of 4 heads, one with 100000 keys
+    // and 63 with 100: 2 parts and 920 us; the long one alone 57).
     const int64_t groups = std::max<int64_t>(p.tiles * a.q_heads, 1);
     const double steps = (double)a.k_tokens / (packed ? std::max<int64_t>(a.batch, 1) : 1) / kPromptKeys;
     const double part = (double)(packed ? 1 : a.batch) * a.q_tokens * a.q_heads * a.head_dim * 8 / 4e6;

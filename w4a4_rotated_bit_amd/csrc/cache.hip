@@ -7,12 +7,13 @@
 // multiply by the scale exactly; e2m1 saturates by itself, e4m3 is cut to its range
 // before.  No result depends on another block, and no sum is formed.
 //
-// Bound by memory.  A workgroup takes consecutive tokens of one head: what a prompt's
+// Bound by memory; few tokens by its latency, three loads one after the other: the slot, the
+// key's row, and the value's behind the key's stores.  A workgroup takes consecutive tokens of one head: what a prompt's
 // tokens leave in a page, and are read from, lies side by side there (64 bytes a row
 // of 128 e2m1 values), while the tokens' rows are whole lines.  These are loaded and
 // stored with the hint that they are used once (78 -> 63 us for both directions of
 // the sizes below).  32768 tokens of 8 heads of 128, e2m1: 35 us to write (170 MB, 4.9
-// TB/s), 25 us to read back (6.7 TB/s: the codes are still in the last cache); one token
+// TB/s), 26 to 28 us to read back (6 TB/s: the codes are still in the last cache); one token
 // 2.7 us each, a launch.
 #include <hip/hip_runtime.h>
 

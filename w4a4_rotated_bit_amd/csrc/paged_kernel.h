@@ -12,16 +12,18 @@
 // The reference of a head's weights only moves when a score exceeds it by so much that
 // 16-bit weights ask for it (Reference), so most steps rescale nothing.
 //
-// Bound by the bytes of the keys and values: one to three steps' rows are under way
-// while one is computed, and a row costs no address arithmetic but that of its
-// page, which is scalar (a lane's place among a step's rows never changes).  Rows
-// copied to shared memory instead, without registers, were slower (e2m1 131 against 76
-// us at the third size): every copy's addresses are the wave's work again.
-// Eight sequences of 16384 keys of 8 heads of 128, 32 query heads: bf16 94 us (5.7
-// TB/s), e4m3 69 us (4.0), e2m1 44 us (3.2; 12 us of it are two launches, their first
-// loads and the join); eight of 28 to 32 thousand keys in e2m1 77 us, the first kernel
-// 56 us of it when the last cache holds them (5.1 TB/s; vector instructions 40%
-// of its time).
+// Rows of 16 bits are bound by their bytes: one to three steps' rows are under way while
+// one is computed.  Quantized rows have half or a quarter of the bytes and the same
+// instructions.  A lane's place among a step's rows never changes, but pages, and rows
+// within them, are addressed by 64-bit scalar arithmetic: a step of 32 e2m1 keys takes
+// some 215 scalar instructions (102 scalars do not fit and are kept in lanes of vector
+// registers) and 270 vector ones, which the SIMDs issue for 40% of the time, with two waves
+// each.  Rows copied to shared memory instead, without registers, were slower (eight
+// sequences of 28 to 32 thousand e2m1 keys 131 against 76 us): every copy's addresses are
+// the wave's work again.
+// Eight sequences of 16384 keys of 8 heads of 128, 32 query heads: bf16 95 us (5.7
+// TB/s), e4m3 67 us (4.1), e2m1 47 us (3.0); eight of 28 to 32 thousand keys in e2m1 78
+// us, the first kernel 66 of it alone (4.2 TB/s) and the join 5.
 //
 // Work is shared out in units of 128 keys, over all sequences and key heads in
 // one line that the workgroups cut into equal parts: the lengths are known on

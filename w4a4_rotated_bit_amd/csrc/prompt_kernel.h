@@ -20,9 +20,10 @@
 // exponential and a sum for each pair of a query and a key, and half a conversion): a
 // step's products and the vector instructions of the step before are written
 // side by side, and two workgroups share a compute unit.  16384 causal tokens of 32 + 8
-// heads of 128: 1.84 to 1.96 ms, 1.12 to 1.20 PFLOP/s, where a bf16 matrix product of
-// torch reaches 1.15 (8192) to 1.37 (16384) on such values: the clock falls to 1.9 GHz
-// under either, with the matrix cores 60% busy here.  Eight waves and 256
+// heads of 128: 1.87 to 1.93 ms, 1.14 to 1.18 PFLOP/s, where a bf16 matrix product of
+// torch reaches 1.15 (8192) to 1.37 (16384) on such values.  Counted over launches one
+// after the other, the matrix cores are busy for 70% of the cycles and the vector unit for
+// 60%, at a clock that falls to 1.6 GHz.  Eight waves and 256
 // queries a workgroup: 1.91 against 1.90 ms; 64 queries a wave, to read each operand
 // once for two products, spills registers (4.0 ms).
 #pragma once
