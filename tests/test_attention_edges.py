@@ -596,3 +596,73 @@ def test_prompts_past_32_bit_offsets(gpu, place):
         for h in range(heads):
             want, bound, _, _ = formula(*(x[a:b, h].double() for x in rows), dim ** -0.5, torch.bfloat16, seen)
             close(out[a:b, h], want, bound, f"rows from {a}, head {h}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,std", [("bf16", 2.0 ** 20), ("bf16", 2.0 ** 45), ("f16", 2.0 ** 12)])
+@pytest.mark.parametrize("dim", [8, 72, 128, 200])
+def test_large_scores_of_packed_and_unaligned_rows(gpu, dtype, std, dim):
+    """Rows computed once more, of several sequences and heads, copied straight to shared memory and by
+    way of registers: the same bits, and the value of the key with the largest score."""
+    dt, lens, heads = TYPES[dtype], [200, 1, 0, 333], 2
+    n = sum(lens)
+    q, k, v = (rand((n, heads, dim), 1 + i, dt, std if i < 2 else 1.0) for i in range(3))
+    starts = torch.tensor([sum(lens[:i]) for i in range(len(lens) + 1)], dtype=torch.int32, device="cuda")
+    for causal in (False, True):
+        outs = []
+        for pad, place in ((0, 0), (1, 0), (8, 3)):
+            views = []
+            for x in (q, k, v):
+                wide = torch.full((n * (heads * dim + pad) + place,), math.nan, dtype=dt, device="cuda")
+                views.append(wide[place:].view(n, heads * dim + pad)[:, :heads * dim].unflatten(1, (heads, dim)))
+                views[-1].copy_(x)
+            outs.append(B.convrot_attention(*views, q_starts=starts, causal=causal, want_lse=True))
+        assert all(torch.equal(a, b) for o in outs[1:] for a, b in zip(o, outs[0]))
+        out, lse = (t.cpu().double() for t in outs[0])
+        at = clear = 0
+        for m in lens:
+            for h in range(heads if m else 0):
+                qq, kk = q[at:at + m, h].double(), k[at:at + m, h].double()
+                s = qq @ kk.T * dim ** -0.5
+                lost = (dim + 4) * U * (qq.abs() @ kk.abs().T) * dim ** -0.5 + 8 * U * s.abs()
+                if causal:
+                    hidden = torch.ones(m, m, dtype=torch.bool).triu(1)
+                    s, lost = s.masked_fill(hidden, -math.inf), lost.masked_fill(hidden, 0.0)
+                best = s.argmax(-1)
+                top = s.gather(1, best[:, None])[:, 0]
+                others = (s + lost).scatter(1, best[:, None], -math.inf).amax(-1)
+                alone = top - lost.gather(1, best[:, None])[:, 0] - others > 40     # the others' weights sum to less than 2^-40
+                clear += int(alone.sum())
+                # up to 2^24 the exact score is what the weight is taken from, and the reference a rounded one: the weight is
+                # a power of two within half a binary place, rounded to the type (half a step of it), as the output is
+                want = v[at:at + m, h][best].double()
+                bound = (torch.finfo(dt).eps / 2 + 2 * (n + 16) * U) * want.abs() + 2.0 ** -39
+                close(out[at:at + m, h][alone], want[alone], (bound + half_step(dt, want.abs() + bound))[alone])
+                assert ((lse[at:at + m, h] - top).abs() <= lost.amax(-1) + 8 * U * top.abs()).all()
+            at += m
+        assert clear > 0.9 * n * heads
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("place", [0, 1])
+def test_masked_places_of_packed_and_unaligned_rows(gpu, place):
+    """Values that are no numbers in a packed sequence reach its own later rows alone."""
+    lens, heads, dim = [70, 130, 260], 2, 72
+    n = sum(lens)
+    q, k, v = (rand((n, heads, dim), 1 + i, torch.bfloat16) for i in range(3))
+    starts = torch.tensor([0, 70, 200, 460], dtype=torch.int32, device="cuda")
+    memory = torch.empty(3 * n * heads * dim + place, dtype=torch.bfloat16, device="cuda")[place:].view(3, n, heads, dim)
+    for at in (0, 69, 70, 133, 199, 330, 459):
+        x = v.clone()
+        x[at, 1, 5] = math.nan
+        for to, t in zip(memory, (q, k, x)):
+            to.copy_(t)
+        out = B.convrot_attention(*memory, q_starts=starts, causal=True)
+        for a, b in ((0, 70), (70, 200), (200, 460)):
+            seen = torch.arange(b - a)[None] <= torch.arange(b - a)[:, None]
+            for h in range(heads):
+                want, bound, _, _ = formula(*(t[a:b, h].double() for t in (q, k, v)), dim ** -0.5, torch.bfloat16, seen)
+                if h == 1 and a <= at < b:
+                    assert out[at:b, h, 5].isnan().all()
+                    want[at - a:, 5] = math.nan
+                close(out[a:b, h], want, bound, f"rows from {a}, head {h}, key {at}")
